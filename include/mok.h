@@ -61,7 +61,9 @@ typedef enum {
   MOK_ERR_DEVICE = -4            /* no gfx950 device, or a launch failed       */
 } mok_status;
 
-typedef enum { MOK_BF16 = 0, MOK_MXFP8 = 1 } mok_dtype;
+/* MOK_MXFP4 is a format of the dense block and the MX product below; the
+ * mixture layer's problems take the first two. */
+typedef enum { MOK_BF16 = 0, MOK_MXFP8 = 1, MOK_MXFP4 = 2 } mok_dtype;
 
 /* Status word bits, written by mok_build_schedule (and the second by
  * mok_forward with driver 2 and by mok_forward_fused); read the word after
@@ -337,6 +339,93 @@ mok_status mok_router_backward(const mok_problem* problem, const mok_config* con
                                const void* x, const float* w_router, const int32_t* topk_ids,
                                const float* topk_w, const float* d_topk_w, float* d_sel, void* dx,
                                float* d_w_router, void* stream);
+
+/* ---------------------------------------------------------------- MXFP4
+ * [OCP MX] MXFP4: E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) with one E8M0 scale per 32 consecutive elements of a row. A row
+ * of K elements takes K/2 bytes, element 2i in the low nibble of byte i, and
+ * K/32 scale bytes.
+ * src [rows][K] bf16 -> q [rows][K/2] and scales [rows][K/32]: per block
+ * s = clamp(floor(log2 amax) - 2 + 127, 0, 254) (0 for an all-zero block) and
+ * q = E2M1(v * 2^(127-s)), round to nearest even, saturating at 6, the sign of
+ * a zero kept. A block with a NaN or an infinity gets scale 255 (NaN) and zero
+ * codes. K must be a multiple of 32; rows >= 0; src 16-byte and q 4-byte
+ * aligned; rows * K <= 2^38 (MOK_ERR_UNSUPPORTED). */
+mok_status mok_mxfp4_quantize(const void* src, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
+                              void* stream);
+
+/* The values the codes stand for: dst [rows][K] bf16 = E2M1 * 2^(s-127), exact
+ * (a block of scale 255 is NaN; values above bf16's range, which the quantizer
+ * never writes, become infinities). Sizes and limits as mok_mxfp4_quantize,
+ * dst 16-byte aligned. */
+mok_status mok_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, void* dst,
+                                void* stream);
+
+/* Product with an MXFP4 matrix: D [M][N] bf16 (row pitch ld_d elements,
+ * 0 = N) = A . B^T, B [N][K] MXFP4, A [M][K] MXFP4 or MXFP8 (a_dtype), each
+ * with its scales [rows][K/32]; products on the scaled matrix instructions,
+ * summed in fp32 in a fixed order, one rounding to bf16. A block of scale 255
+ * makes its row of D (or, in B, its column) NaN. K a multiple of 128 and at
+ * most 2^20 (MOK_ERR_UNSUPPORTED otherwise); M, N >= 0, any value up to 2^30;
+ * a and b 16-byte, scales 4-byte aligned; D may start and step anywhere.
+ * Columns N .. ld_d-1 of D are not touched. */
+typedef struct {
+  int64_t M, N, K;
+  int64_t ld_d;
+  int32_t a_dtype;               /* MOK_MXFP4 or MOK_MXFP8 */
+} mok_mx_problem;
+
+/* [host] Workspace bytes of mok_mx_matmul (0 for many shapes; not monotonic in
+ * M: few rows are split along K to fill the device). */
+mok_status mok_mx_matmul_workspace(const mok_mx_problem* problem, size_t* workspace_bytes);
+
+mok_status mok_mx_matmul(const mok_mx_problem* problem, const uint8_t* a, const uint8_t* a_scales,
+                         const uint8_t* b, const uint8_t* b_scales, void* d, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- dense block
+ * The gated feed-forward block that every token passes (the shared expert
+ * beside the routed ones), without a schedule:
+ *   a = x Wg^T, b = x Wu^T, h = act(a) * b, y = h Wd^T (+ residual)
+ * act is SiLU a*s(a) or GELU in its tanh form. x, dx [T][H] have row pitch
+ * ld_x, and y, residual, dy row pitch ld_y (elements, multiples of 8, 0 = H).
+ * Weights as in mok_weights for one expert: w_gate, w_up [I][H], w_down [H][I].
+ *   MOK_BF16:  any T >= 0, H and I multiples of 8; fp32 sums; a, b, h, da, db
+ *              rounded to bf16 once where they are stored.
+ *   MOK_MXFP4: forward only; H and I multiples of 128; weights from
+ *              mok_mxfp4_quantize with s_gate, s_up [I][H/32], s_down [H][I/32].
+ *              x is quantized to MXFP8 along H and h, from its fp32 values, to
+ *              MXFP8 along I; a token with a NaN or an infinity comes out NaN.
+ * Pointers to bf16 data and codes are 16-byte aligned, scales 4-byte. */
+typedef enum { MOK_ACT_SILU = 0, MOK_ACT_GELU_TANH = 1 } mok_activation;
+typedef struct {
+  int64_t T, H, I;
+  int32_t dtype;                 /* MOK_BF16 or MOK_MXFP4 */
+  int32_t activation;            /* mok_activation */
+  int64_t ld_x, ld_y;
+} mok_ffn_problem;
+
+/* [host] Bytes of the caller's buffers: workspace (scratch of either call, not
+ * monotonic in T) and ctx, what the forward saves for the backward: the
+ * pre-activations [T][2I] bf16, a in columns [0, I), b in [I, 2I) (MOK_MXFP4:
+ * 0). */
+mok_status mok_ffn_buffer_sizes(const mok_ffn_problem* problem, size_t* workspace_bytes, size_t* ctx_bytes);
+
+/* residual NULL = none, and may be y itself (y += block(x)): the routed
+ * layer's output goes in here and the shared expert is added before the one
+ * rounding. ctx NULL for inference. Columns H .. ld_y-1 of y are not touched.
+ * x and y may be NULL when T = 0. */
+mok_status mok_ffn_forward(const mok_ffn_problem* problem, const void* x, const mok_weights* weights,
+                           const void* residual, void* y, void* ctx, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Gradients of <dy, y> from the forward's x and ctx: dx [T][H], dw_gate, dw_up
+ * [I][H], dw_down [H][I] (bf16, overwritten; the residual's gradient is dy).
+ * With T = 0 the weight gradients are zeros and the other pointers may be NULL.
+ * MOK_MXFP4: MOK_ERR_UNSUPPORTED. */
+mok_status mok_ffn_backward(const mok_ffn_problem* problem, const void* ctx, const void* x,
+                            const mok_weights* weights, const void* dy, void* dx, void* dw_gate, void* dw_up,
+                            void* dw_down, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- tracing
  * Per-kernel timing for profiling ([MoK clip] How-to item 1: profile first to

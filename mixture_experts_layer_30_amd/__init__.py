@@ -22,6 +22,9 @@ MOK_ERR_BUFFER_TOO_SMALL = -3
 MOK_ERR_DEVICE = -4
 MOK_BF16 = 0
 MOK_MXFP8 = 1
+MOK_MXFP4 = 2
+ACT_SILU = 0
+ACT_GELU_TANH = 1
 STATUS_BAD_EXPERT_ID = 0x1
 STATUS_WATCHDOG = 0x2
 
@@ -60,13 +63,24 @@ class ScheduleLayout(ctypes.Structure):
             "fwd_tile_rows", "bwd_tile_rows")] + [("arrays", ctypes.c_size_t), ("expert_order", ctypes.c_size_t)]
 
 
+class MxProblem(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("ld_d", ctypes.c_int64),
+                ("a_dtype", ctypes.c_int32)]
+
+
+class FfnProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("I", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64)]
+
+
 _lib = None
 
 EXPORTS = ("mok_version", "mok_status_string", "mok_buffer_sizes", "mok_get_schedule_layout",
            "mok_build_schedule", "mok_forward", "mok_backward", "mok_mxfp8_quantize",
            "mok_router_forward", "mok_router_backward", "mok_trace_enable", "mok_trace_collect",
            "mok_mxfp8_quantize_transposed", "mok_probe_mfma", "mok_build_schedule_noalloc",
-           "mok_forward_fused")
+           "mok_forward_fused", "mok_mxfp4_quantize", "mok_mxfp4_dequantize", "mok_mx_matmul_workspace",
+           "mok_mx_matmul", "mok_ffn_buffer_sizes", "mok_ffn_forward", "mok_ffn_backward")
 
 
 class TraceStat(ctypes.Structure):
@@ -119,6 +133,20 @@ def lib():
         L.mok_trace_enable.argtypes = [ctypes.c_int32]
         L.mok_trace_collect.restype = ctypes.c_int
         L.mok_trace_collect.argtypes = [P(TraceStat), ctypes.c_int32, P(ctypes.c_int32)]
+        for name in ("mok_mxfp4_quantize", "mok_mxfp4_dequantize"):
+            getattr(L, name).restype = ctypes.c_int
+        L.mok_mxfp4_quantize.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, vp, vp, vp]
+        L.mok_mxfp4_dequantize.argtypes = [vp, vp, ctypes.c_int64, ctypes.c_int64, vp, vp]
+        L.mok_mx_matmul_workspace.restype = ctypes.c_int
+        L.mok_mx_matmul_workspace.argtypes = [P(MxProblem), P(sz)]
+        L.mok_mx_matmul.restype = ctypes.c_int
+        L.mok_mx_matmul.argtypes = [P(MxProblem), vp, vp, vp, vp, vp, vp, sz, vp]
+        L.mok_ffn_buffer_sizes.restype = ctypes.c_int
+        L.mok_ffn_buffer_sizes.argtypes = [P(FfnProblem), P(sz), P(sz)]
+        L.mok_ffn_forward.restype = ctypes.c_int
+        L.mok_ffn_forward.argtypes = [P(FfnProblem), vp, P(Weights), vp, vp, vp, vp, sz, vp]
+        L.mok_ffn_backward.restype = ctypes.c_int
+        L.mok_ffn_backward.argtypes = [P(FfnProblem), vp, vp, P(Weights), vp, vp, vp, vp, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -216,7 +244,8 @@ def forward_fused(problem, topk_ids, schedule, x, topk_w, weights, y, workspace,
                                    schedule.numel() * schedule.element_size(), _ptr(x), _ptr(topk_w),
                                    ctypes.byref(w), _ptr(y), _ptr(fwd_ctx), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(), _stream(stream)),
-           "mok_forward_fused")
+           "mok_forward_fused", "mok_mxfp4_quantize", "mok_mxfp4_dequantize", "mok_mx_matmul_workspace",
+           "mok_mx_matmul", "mok_ffn_buffer_sizes", "mok_ffn_forward", "mok_ffn_backward")
 
 
 def backward(problem, schedule, fwd_ctx, x, topk_w, weights, dy, dx, dw_gate, dw_up, dw_down,
@@ -271,6 +300,173 @@ def router_backward(problem, schedule, x, w_router, topk_ids, topk_w, d_topk_w, 
                                      _ptr(w_router), _ptr(topk_ids), _ptr(topk_w), _ptr(d_topk_w),
                                      _ptr(d_sel), _ptr(dx), _ptr(d_w_router), _stream(stream)),
            "mok_router_backward")
+
+
+# ---------------------------------------------------------------- MXFP4 and the dense block
+# These calls check their tensors (device, type, shape, row layout) and run on
+# the tensors' device: with the caller's stream, or that device's current one.
+
+def _want(what, t, dtype, shape, rows=False, device=None):
+    """t is a device tensor of this type and shape, contiguous (rows=True: with
+    contiguous elements within a row, rows at any pitch)."""
+    import torch
+    names = {"bf16": torch.bfloat16, "u8": torch.uint8}
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise MokError(MOK_ERR_INVALID_ARG, f"{what}: not on the call's GPU ({t.device})")
+    if t.dtype != names[dtype] or tuple(t.shape) != tuple(shape):
+        raise MokError(MOK_ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, wanted {names[dtype]} {tuple(shape)}")
+    if not t.is_contiguous() and not (rows and t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
+        raise MokError(MOK_ERR_INVALID_ARG, f"{what}: strides {t.stride()}")
+
+
+def _pitch(t):
+    """Row pitch of a [rows][cols] tensor in elements (0: contiguous)."""
+    return 0 if t.is_contiguous() else t.stride(0)
+
+
+class _on:
+    """The device of `t` as the current one for the call (nothing where it is already)."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, t):
+        import torch
+        self.ctx = torch.cuda.device(t.device) if t.device.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _rows_K(src):
+    K = src.shape[-1]
+    return (src.numel() // K if K else 0), K
+
+
+def mxfp4_quantize(src, q, scales, stream=None):
+    """src [..., K] bf16 -> q [..., K/2] uint8 (two E2M1 codes a byte), scales [..., K/32] uint8 (E8M0)."""
+    rows, K = _rows_K(src)
+    _want("src", src, "bf16", src.shape)
+    _want("q", q, "u8", (*src.shape[:-1], K // 2), device=src.device)
+    _want("scales", scales, "u8", (*src.shape[:-1], K // 32), device=src.device)
+    with _on(src):
+        _check(lib().mok_mxfp4_quantize(_ptr(src), rows, K, _ptr(q), _ptr(scales), _stream(stream)),
+               "mok_mxfp4_quantize")
+
+
+def mxfp4_dequantize(q, scales, dst, stream=None):
+    """The bf16 values dst [..., K] of the codes q [..., K/2] and scales [..., K/32]."""
+    rows, K = _rows_K(dst)
+    _want("dst", dst, "bf16", dst.shape)
+    _want("q", q, "u8", (*dst.shape[:-1], K // 2), device=dst.device)
+    _want("scales", scales, "u8", (*dst.shape[:-1], K // 32), device=dst.device)
+    with _on(dst):
+        _check(lib().mok_mxfp4_dequantize(_ptr(q), _ptr(scales), rows, K, _ptr(dst), _stream(stream)),
+               "mok_mxfp4_dequantize")
+
+
+def make_mx_problem(M, N, K, a_dtype, ld_d=0) -> MxProblem:
+    return MxProblem(int(M), int(N), int(K), int(ld_d), int(a_dtype))
+
+
+def mx_matmul_workspace(problem):
+    """Workspace bytes of mx_matmul; host only."""
+    n = ctypes.c_size_t()
+    _check(lib().mok_mx_matmul_workspace(ctypes.byref(problem), ctypes.byref(n)), "mok_mx_matmul_workspace")
+    return n.value
+
+
+def mx_matmul(problem, a, a_scales, b, b_scales, d, workspace, stream=None):
+    """d [M][N] bf16 = A . B^T: a [M][K] (MXFP8) or [M][K/2] (MXFP4) uint8, b [N][K/2] uint8, scales
+    [rows][K/32] uint8. The row pitch of d is taken from the tensor (problem.ld_d is ignored)."""
+    M, N, K = problem.M, problem.N, problem.K
+    dev = d.device
+    _want("d", d, "bf16", (M, N), rows=True)
+    _want("a", a, "u8", (M, K if problem.a_dtype == MOK_MXFP8 else K // 2), device=dev)
+    _want("a_scales", a_scales, "u8", (M, K // 32), device=dev)
+    _want("b", b, "u8", (N, K // 2), device=dev)
+    _want("b_scales", b_scales, "u8", (N, K // 32), device=dev)
+    p = MxProblem(M, N, K, _pitch(d), problem.a_dtype)
+    with _on(d):
+        _check(lib().mok_mx_matmul(ctypes.byref(p), _ptr(a), _ptr(a_scales), _ptr(b), _ptr(b_scales), _ptr(d),
+                                   _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                   _stream(stream)), "mok_mx_matmul")
+
+
+def make_ffn_problem(T, H, I, dtype=MOK_BF16, activation=ACT_SILU, ld_x=0, ld_y=0) -> FfnProblem:
+    return FfnProblem(int(T), int(H), int(I), int(dtype), int(activation), int(ld_x), int(ld_y))
+
+
+def ffn_buffer_sizes(problem):
+    """(workspace_bytes, ctx_bytes); host only."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().mok_ffn_buffer_sizes(ctypes.byref(problem), ctypes.byref(a), ctypes.byref(b)),
+           "mok_ffn_buffer_sizes")
+    return a.value, b.value
+
+
+def _ffn_weights(problem, weights, device):
+    H, I = problem.H, problem.I
+    mx = problem.dtype == MOK_MXFP4
+    if len(weights) < (6 if mx else 3):
+        raise MokError(MOK_ERR_INVALID_ARG, "weights: (w_gate, w_up, w_down[, s_gate, s_up, s_down])")
+    t, div = ("u8", 2) if mx else ("bf16", 1)
+    for n, w, shape in zip(("w_gate", "w_up", "w_down"), weights, ((I, H // div), (I, H // div), (H, I // div))):
+        _want(n, w, t, shape, device=device)
+    if mx:
+        for n, w, shape in zip(("s_gate", "s_up", "s_down"), weights[3:], ((I, H // 32), (I, H // 32), (H, I // 32))):
+            _want(n, w, "u8", shape, device=device)
+    return _weights(*weights[:6 if mx else 3])
+
+
+def _ffn_call(problem, ld_x, ld_y):
+    return FfnProblem(problem.T, problem.H, problem.I, problem.dtype, problem.activation, ld_x, ld_y)
+
+
+def ffn_forward(problem, x, weights, y, workspace, residual=None, ctx=None, stream=None):
+    """y [T][H] = block(x) (+ residual); ctx [T][2I] bf16 receives the pre-activations. x, and y with residual,
+    may have any row pitch that is a multiple of 8 (taken from the tensors). weights: (w_gate, w_up, w_down)
+    bf16, or MXFP4 codes with (s_gate, s_up, s_down)."""
+    T, H = problem.T, problem.H
+    dev = x.device
+    _want("x", x, "bf16", (T, H), rows=True)
+    _want("y", y, "bf16", (T, H), rows=True, device=dev)
+    if residual is not None:
+        _want("residual", residual, "bf16", (T, H), rows=True, device=dev)
+        if _pitch(residual) != _pitch(y):
+            raise MokError(MOK_ERR_INVALID_ARG, "residual: another row pitch than y")
+    if ctx is not None:
+        _want("ctx", ctx, "bf16", (T, 2 * problem.I), device=dev)
+    w = _ffn_weights(problem, weights, dev)
+    p = _ffn_call(problem, _pitch(x), _pitch(y))
+    with _on(x):
+        _check(lib().mok_ffn_forward(ctypes.byref(p), _ptr(x), ctypes.byref(w), _ptr(residual), _ptr(y), _ptr(ctx),
+                                     _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                     _stream(stream)), "mok_ffn_forward")
+
+
+def ffn_backward(problem, ctx, x, weights, dy, dx, dw_gate, dw_up, dw_down, workspace, stream=None):
+    """Gradients of <dy, y>; x and dx share one row pitch, dy may have another."""
+    T, H, I = problem.T, problem.H, problem.I
+    dev = x.device
+    _want("x", x, "bf16", (T, H), rows=True)
+    _want("dy", dy, "bf16", (T, H), rows=True, device=dev)
+    _want("dx", dx, "bf16", (T, H), rows=True, device=dev)
+    _want("ctx", ctx, "bf16", (T, 2 * I), device=dev)
+    for n, t, shape in (("dw_gate", dw_gate, (I, H)), ("dw_up", dw_up, (I, H)), ("dw_down", dw_down, (H, I))):
+        _want(n, t, "bf16", shape, device=dev)
+    if _pitch(x) != _pitch(dx):
+        raise MokError(MOK_ERR_INVALID_ARG, "dx: another row pitch than x")
+    w = _ffn_weights(problem, weights, dev)
+    p = _ffn_call(problem, _pitch(x), _pitch(dy))
+    with _on(x):
+        _check(lib().mok_ffn_backward(ctypes.byref(p), _ptr(ctx), _ptr(x), ctypes.byref(w), _ptr(dy), _ptr(dx),
+                                      _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _stream(stream)),
+               "mok_ffn_backward")
 
 
 def trace_enable(on=True):

@@ -1,0 +1,299 @@
+// Dense gated feed-forward block in bf16 (a shared expert, which every token
+// passes): h = act(x Wg^T) * (x Wu^T), y = h Wd^T (+ residual), and its backward
+//
+//   dh = dy Wd          da = dh * b * act'(a)     db = dh * act(a)    h = act(a) * b
+//   dWd = dy^T h        dWg = da^T x              dWu = db^T x        dx = da Wg + db Wu
+//
+// Both projections, the gate and the product are one launch; so are dh with the
+// gate's backward, dWg with dWu, and the two terms of dx (one sum over 2I).
+// Sums are fp32 in ascending K (split products: fp32 partial sums, added in
+// ascending order), so results are bitwise reproducible. Rounded to bf16: y, the
+// saved a and b, and the operands of the next product, h, da and db (the matrix
+// cores take bf16): each adds at most 2^-9 relative to its element.
+#include "dense_core.h"
+#include "dense_launch.h"
+
+using namespace mok;
+
+namespace {
+
+using G256 = Geo<256, 256, 2, 2>;
+constexpr int kNoSeg = 0x7fffffc0;               // one segment of K (CopyT)
+
+// rows, columns and contracted length of a product, in tiles' terms
+struct Shape {
+  int M, N, K, batch;                            // batch 2: dWg and dWu, rows of one product each
+};
+inline Shape shape_of(const mok_ffn_args& a, mok_ffn_op op) {
+  switch (op) {
+    case FFN_GATEUP: return {a.T, 2 * ((a.I + 31) / 32 * 32), a.H, 1};
+    case FFN_DOWN: return {a.T, a.H, a.I, 1};
+    case FFN_DH: return {a.T, a.Ip, a.H, 1};
+    case FFN_DWD: return {a.H, a.I, a.T, 1};
+    case FFN_DWGU: return {a.I, a.H, a.T, 2};
+    default: return {a.T, a.H, 2 * a.Ip, 1};
+  }
+}
+
+// ------------------------------------------------------------------ epilogues
+// Eight columns c .. c+7 of output row r from fp32 sums (gate/up: v = a, w = b).
+template <int OP, int ACT>
+MOK_DEV void finish8(const mok_ffn_args& a, int r, int c, int half, float v[8], const float w[8]) {
+  if constexpr (OP == FFN_GATEUP) {
+    if (c >= a.I) return;
+    float h[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) h[u] = gate_act<ACT>(v[u]) * w[u];
+    store_nt(a.h + (int64_t)r * a.I + c, pack_bf16x8(h));
+    if (a.ab) {
+      bf16_t* p = a.ab + (int64_t)r * 2 * a.I + c;
+      store_nt(p, pack_bf16x8(v));
+      store_nt(p + a.I, pack_bf16x8(w));
+    }
+  } else if constexpr (OP == FFN_DH) {
+    if (c >= a.Ip) return;
+    bf16_t* d = a.dab + (int64_t)r * 2 * a.Ip + c;
+    if (c >= a.I) {                              // the pad columns of da and db
+      store_nt(d, make_uint4(0, 0, 0, 0));
+      store_nt(d + a.Ip, make_uint4(0, 0, 0, 0));
+      return;
+    }
+    const bf16_t* p = a.ab + (int64_t)r * 2 * a.I + c;
+    float av[8], bv[8], da[8], db[8], h[8];
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(p), av);
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(p + a.I), bv);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      float act, dact;
+      gate_act_grad<ACT>(av[u], act, dact);
+      h[u] = act * bv[u];
+      da[u] = v[u] * bv[u] * dact;
+      db[u] = v[u] * act;
+    }
+    store_nt(d, pack_bf16x8(da));
+    store_nt(d + a.Ip, pack_bf16x8(db));
+    store_nt(a.h + (int64_t)r * a.I + c, pack_bf16x8(h));
+  } else if constexpr (OP == FFN_DWD) {
+    if (c >= a.I) return;
+    store_nt(a.dwd + (int64_t)r * a.I + c, pack_bf16x8(v));
+  } else if constexpr (OP == FFN_DWGU) {
+    if (c >= a.H) return;
+    store_nt((half ? a.dwu : a.dwg) + (int64_t)r * a.H + c, pack_bf16x8(v));
+  } else {
+    if (c >= a.H) return;
+    if constexpr (OP == FFN_DOWN)
+      if (a.res) {
+        float s[8];
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(a.res + (int64_t)r * a.ldy + c), s);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] += s[u];
+      }
+    bf16_t* d = OP == FFN_DOWN ? a.y + (int64_t)r * a.ldy : a.dx + (int64_t)r * a.ldx;
+    store_nt(d + c, pack_bf16x8(v));
+  }
+}
+
+// output columns of a tile of N accumulator columns, and the accumulator column
+// of output column c (gate/up tiles alternate 32 gate and 32 up columns)
+template <int OP, int N>
+constexpr int out_cols() { return OP == FFN_GATEUP ? N / 2 : N; }
+template <int OP>
+MOK_DEV int acc_col(int c) { return OP == FFN_GATEUP ? (c >> 5) * 64 + (c & 31) : c; }
+
+// rows [0, nrows) of fp32 staging at pitch P -> finish8; row0/col0 of the tile
+template <int OP, int ACT, int TILE>
+MOK_DEV void finish_rows(const mok_ffn_args& a, const uint8_t* st, int pitch, int nrows, int row0, int col0,
+                         int half) {
+  constexpr int CH = out_cols<OP, TILE>() / 8;
+  for (int idx = threadIdx.x; idx < nrows * CH; idx += kThreads) {
+    const int r = idx / CH, c = (idx % CH) * 8;
+    const uint8_t* p = st + r * pitch + acc_col<OP>(c) * 4;
+    float v[8], w[8];
+    load_f32<8>(p, v);
+    if constexpr (OP == FFN_GATEUP) load_f32<8>(p + 128, w);
+    finish8<OP, ACT>(a, row0 + r, col0 + c, half, v, w);
+  }
+}
+
+// ------------------------------------------------------------------ products
+template <int OP, int TILE, class F>
+MOK_DEV void with_operands(const mok_ffn_args& a, int m0, int n0, int half, F&& f) {
+  const auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
+  if constexpr (OP == FFN_GATEUP) {
+    const CopyK<TILE, 128> la(RowsStrided{u8(a.x + (int64_t)m0 * a.ldx), 2 * a.ldx, a.T - m0}, 2 * a.H);
+    const CopyK<TILE, 128> lb(RowsGateUp{u8(a.wg), u8(a.wu), 2 * (int64_t)a.H, n0, a.I}, 2 * a.H);
+    f(la, lb);
+  } else if constexpr (OP == FFN_DOWN) {
+    const CopyK<TILE, 128> la(RowsStrided{u8(a.h + (int64_t)m0 * a.I), 2 * (int64_t)a.I, a.T - m0}, 2 * a.I);
+    const CopyK<TILE, 128> lb(RowsStrided{u8(a.wd + (int64_t)n0 * a.I), 2 * (int64_t)a.I, a.H - n0}, 2 * a.I);
+    f(la, lb);
+  } else if constexpr (OP == FFN_DH) {
+    const CopyK<TILE, 128> la(RowsStrided{u8(a.dy + (int64_t)m0 * a.ldy), 2 * a.ldy, a.T - m0}, 2 * a.H);
+    const CopyT<TILE> lb(u8(a.wd + n0), u8(a.wd + n0), kNoSeg, a.H, 2 * (int64_t)a.I, a.I - n0);
+    f(la, lb);
+  } else if constexpr (OP == FFN_DWD) {
+    const CopyT<TILE> la(u8(a.dy + m0), u8(a.dy + m0), kNoSeg, a.T, 2 * a.ldy, a.H - m0);
+    const CopyT<TILE> lb(u8(a.h + n0), u8(a.h + n0), kNoSeg, a.T, 2 * (int64_t)a.I, a.I - n0);
+    f(la, lb);
+  } else if constexpr (OP == FFN_DWGU) {
+    const uint8_t* da = u8(a.dab + (half ? a.Ip : 0) + m0);
+    const CopyT<TILE> la(da, da, kNoSeg, a.T, 4 * (int64_t)a.Ip, a.I - m0);
+    const CopyT<TILE> lb(u8(a.x + n0), u8(a.x + n0), kNoSeg, a.T, 2 * a.ldx, a.H - n0);
+    f(la, lb);
+  } else {
+    const CopyK<TILE, 128> la(RowsStrided{u8(a.dab + (int64_t)m0 * 2 * a.Ip), 4 * (int64_t)a.Ip, a.T - m0},
+                              4 * (int64_t)a.Ip);
+    const CopyT<TILE> lb(u8(a.wg + n0), u8(a.wu + n0), a.Ip, a.I, 2 * (int64_t)a.H, a.H - n0);
+    f(la, lb);
+  }
+}
+
+template <int OP, int ACT, bool SPLIT>
+__global__ __launch_bounds__(kThreads, 2) void ffn128_kernel(mok_ffn_args a, int M, int K, int nr, int nc,
+                                                             int batch, int splits) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds128];
+  const int tiles = nr * nc * batch;
+  const int i = dense_index((int64_t)tiles * splits);
+  if (i < 0) return;
+  const int split = SPLIT ? i / tiles : 0, t = SPLIT ? i % tiles : i, half = t / (nr * nc);
+  int row, col;
+  dense_tile(t - half * nr * nc, nr, nc, 8, row, col);
+  const int m0 = row * 128, n0 = col * out_cols<OP, 128>();
+  const int ns = (K + 63) / 64;
+  const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
+  const int j1 = SPLIT ? (int)((int64_t)ns * (split + 1) / splits) : ns;
+  Acc<2, 2> acc;
+  with_operands<OP, 128>(a, m0, n0, half, [&](const auto& la, const auto& lb) { loop128(lds, la, lb, j0, j1, acc); });
+  stage128(lds, acc);
+  const int nrows = min(128, M - m0);
+  if constexpr (SPLIT) {
+    // partial tile (split, t): 128 rows of 128 fp32
+    float* p = a.part + ((int64_t)split * tiles + t) * 16384;
+    for (int idx = threadIdx.x; idx < nrows * 32; idx += kThreads)
+      reinterpret_cast<float4*>(p)[idx] =
+          *reinterpret_cast<const float4*>(lds + (idx >> 5) * kPitch128 + (idx & 31) * 16);
+  } else {
+    finish_rows<OP, ACT, 128>(a, lds, kPitch128, nrows, m0, n0, half);
+  }
+}
+
+// sums of the partial tiles in ascending split order, and the epilogue; one
+// workgroup per 256 chunks of eight output columns
+template <int OP, int ACT>
+__global__ __launch_bounds__(kThreads) void ffn_join_kernel(mok_ffn_args a, int M, int nr, int nc, int batch,
+                                                            int splits) {
+  constexpr int CH = out_cols<OP, 128>() / 8;
+  const int tiles = nr * nc * batch, t = (int)blockIdx.y, half = t / (nr * nc);
+  int row, col;
+  dense_tile(t - half * nr * nc, nr, nc, 8, row, col);
+  const int idx = (int)blockIdx.x * kThreads + (int)threadIdx.x;
+  const int r = idx / CH, c = (idx % CH) * 8;
+  if (r >= min(128, M - row * 128)) return;
+  const float* p = a.part + (int64_t)t * 16384 + r * 128 + acc_col<OP>(c);
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int s = 0; s < splits; ++s, p += (int64_t)tiles * 16384) {
+    float q[8];
+    load_f32<8>(p, q);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] += q[u];
+    if constexpr (OP == FFN_GATEUP) {
+      load_f32<8>(p + 32, q);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) w[u] += q[u];
+    }
+  }
+  finish8<OP, ACT>(a, row * 128 + r, col * out_cols<OP, 128>() + c, half, v, w);
+}
+
+// Products that fill the chip with 256 x 256 tiles run the main loop of gemm_core.h.
+template <int OP, int ACT>
+__global__ __launch_bounds__(kThreads, 1) void ffn256_kernel(mok_ffn_args a, int M, int K, int nr, int nc,
+                                                             int batch) {
+  using G = G256;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[tile_lds_bytes<Smem<G, false>>()];
+  Smem<G, false>& sm = *reinterpret_cast<Smem<G, false>*>(lds);
+  const int t = dense_index((int64_t)nr * nc * batch);
+  if (t < 0) return;
+  const int half = t / (nr * nc);
+  int row, col;
+  dense_tile(t - half * nr * nc, nr, nc, 4, row, col);
+  const int m0 = row * 256, n0 = col * out_cols<OP, 256>();
+  const int nrows = min(256, M - m0);
+  Acc<G::FM, G::FN> acc;
+  with_operands<OP, 256>(a, m0, n0, half, [&](const auto& la, const auto& lb) {
+    NoScales ns;
+    mainloop_rows<false, G, false>(sm, la, lb, ns, ns, 2 * ((K + 63) / 64), nrows, acc);
+  });
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    barrier_lds_only();
+    HalfF32<G>::put(lds, acc, hf);
+    barrier_lds_only();
+    finish_rows<OP, ACT, 256>(a, lds, HalfF32<G>::PITCH, min(128, nrows - 128 * hf), m0 + 128 * hf, n0, half);
+  }
+}
+
+// ------------------------------------------------------------------ host
+struct Plan {
+  Shape s;
+  int tile, nr, nc, splits;
+};
+
+Plan plan_of(const mok_ffn_args& a, mok_ffn_op op) {
+  Plan p;
+  p.s = shape_of(a, op);
+  const auto tiles = [&](int n) {
+    return (int64_t)((p.s.M + n - 1) / n) * ((p.s.N + n - 1) / n) * p.s.batch;
+  };
+  p.tile = tiles(256) >= 256 ? 256 : 128;
+  p.nr = (p.s.M + p.tile - 1) / p.tile;
+  p.nc = (p.s.N + p.tile - 1) / p.tile;
+  p.splits = 1;
+  if (p.tile == 128) {
+    const int64_t n = tiles(128), slots = (p.s.K + 63) / 64;
+    int64_t sp = n > 0 ? 512 / n : 1;
+    sp = sp < slots / 4 ? sp : slots / 4;
+    p.splits = sp < 1 ? 1 : (int)sp;
+  }
+  return p;
+}
+
+template <int OP, int ACT>
+hipError_t launch(const mok_ffn_args& a, const Plan& p, hipStream_t st) {
+  const int64_t tiles = (int64_t)p.nr * p.nc * p.s.batch;
+  if (tiles * p.splits > (1 << 30)) return hipErrorInvalidValue;
+  if (tiles == 0) return hipSuccess;
+  const dim3 grid(dense_grid(tiles * p.splits)), block(kThreads);
+  if (p.tile == 256)
+    hipLaunchKernelGGL((ffn256_kernel<OP, ACT>), grid, block, 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch);
+  else if (p.splits == 1)
+    hipLaunchKernelGGL((ffn128_kernel<OP, ACT, false>), grid, block, 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch, 1);
+  else {
+    hipLaunchKernelGGL((ffn128_kernel<OP, ACT, true>), grid, block, 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch,
+                       p.splits);
+    const int ch = 128 * out_cols<OP, 128>() / 8;
+    hipLaunchKernelGGL((ffn_join_kernel<OP, ACT>), dim3((ch + kThreads - 1) / kThreads, (unsigned)tiles), block, 0, st,
+                       a, p.s.M, p.nr, p.nc, p.s.batch, p.splits);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t mok_ffn_part_bytes(const mok_ffn_args& a, mok_ffn_op op) {
+  const Plan p = plan_of(a, op);
+  return p.splits > 1 ? (size_t)p.splits * p.nr * p.nc * p.s.batch * 65536 : 0;
+}
+
+hipError_t mok_launch_ffn(const mok_ffn_args& a, mok_ffn_op op, int act, hipStream_t st) {
+  const Plan p = plan_of(a, op);
+  switch (op) {
+    case FFN_GATEUP: return act == 0 ? launch<FFN_GATEUP, 0>(a, p, st) : launch<FFN_GATEUP, 1>(a, p, st);
+    case FFN_DOWN: return launch<FFN_DOWN, 0>(a, p, st);
+    case FFN_DH: return act == 0 ? launch<FFN_DH, 0>(a, p, st) : launch<FFN_DH, 1>(a, p, st);
+    case FFN_DWD: return launch<FFN_DWD, 0>(a, p, st);
+    case FFN_DWGU: return launch<FFN_DWGU, 0>(a, p, st);
+    case FFN_DX: return launch<FFN_DX, 0>(a, p, st);
+    default: return hipErrorInvalidValue;
+  }
+}

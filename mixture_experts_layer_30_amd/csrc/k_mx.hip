@@ -1,0 +1,403 @@
+// MXFP4 (OCP Microscaling Formats v1.0: E2M1 elements, one E8M0 scale per 32
+// along a row): quantization, reading back, and the product of an MXFP4 or
+// MXFP8 matrix with an MXFP4 matrix on the scaled matrix instructions,
+//
+//   D[m][n] = sum over blocks of 32 k of 2^(sa + sb - 254) * sum_k A[m][k] B[n][k],
+//
+// fp32 accumulation. With the gate it computes the first half of a feed-forward
+// block with 4-bit weights: h = act(A Wg^T) * (A Wu^T), quantized along its row
+// to MXFP8 from the fp32 values (no bf16 rounding between).
+#include "dense_core.h"
+#include "dense_launch.h"
+
+using namespace mok;
+
+namespace {
+
+// ------------------------------------------------------------------ quantize
+// Scale byte of a block: clamp(floor(log2 amax) - 2 + 127, 0, 254), 0 for zeros
+// (2: the exponent of the largest E2M1 value, 6 = 1.5 * 2^2).
+MOK_DEV int mxfp4_scale_byte(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  if (b == 0) return 0;
+  const int field = (int)(b >> 23);
+  const int e = field > 0 ? field - 127 : (31 - __clz((int)b)) - 149;
+  return max(0, min(254, e - 2 + 127));
+}
+
+// E2M1 code of q, nearest value of 0, 0.5, 1, 1.5, 2, 3, 4, 6, ties to the even
+// code, saturating at 6: the code counts the midpoints that |q| has passed.
+MOK_DEV uint32_t e2m1_encode(float q) {
+  const float a = fabsf(q);
+  const uint32_t m = (uint32_t)(a > 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a > 1.25f) +
+                     (uint32_t)(a >= 1.75f) + (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.0f);
+  return m | ((__float_as_uint(q) >> 28) & 8u);
+}
+MOK_DEV float e2m1_decode(uint32_t c) {
+  const uint32_t m = c & 7u;
+  const uint32_t bits = m >= 2 ? ((126u + (m >> 1)) << 23) | ((m & 1u) << 22) : (m ? 0x3F000000u : 0u);
+  return __uint_as_float(bits | ((c & 8u) << 28));
+}
+
+// bits of the largest magnitude of a block held by four adjacent lanes, eight
+// elements each (as integers, so that a NaN is the largest of all)
+MOK_DEV uint32_t block_max_bits(const float v[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(v[u]) & 0x7FFFFFFFu);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+  return max(m, (uint32_t)__shfl_xor((int)m, 2));
+}
+
+// Four adjacent lanes per block, eight elements each: 16-byte loads along the
+// row, the block's largest magnitude over the four lanes, 4 bytes of codes per
+// lane. A block that holds a NaN or an infinity, which the format cannot, gets
+// the NaN scale 255: it reads back, and multiplies, as NaN.
+__global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const bf16_t* __restrict__ src, int64_t n8,
+                                                            uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= n8) return;                         // n8 is a multiple of 4: whole blocks leave
+  const uint4 raw = reinterpret_cast<const uint4*>(src)[idx];
+  float v[8];
+  unpack_bf16x8(raw, v);
+  const uint32_t m = block_max_bits(v);
+  const bool nan = m >= 0x7F800000u;
+  const int sc = nan ? 255 : mxfp4_scale_byte(__uint_as_float(m));
+  const float inv = mx_inv_scale(sc);
+  uint32_t w = 0;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) w |= e2m1_encode(v[u] * inv) << (4 * u);
+  reinterpret_cast<uint32_t*>(q)[idx] = nan ? 0u : w;
+  if ((idx & 3) == 0) scales[idx >> 2] = (uint8_t)sc;
+}
+
+__global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __restrict__ q,
+                                                              const uint8_t* __restrict__ scales, int64_t n8,
+                                                              bf16_t* __restrict__ dst) {
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= n8) return;
+  const uint32_t w = reinterpret_cast<const uint32_t*>(q)[idx];
+  const int sc = scales[idx >> 2];
+  const float x = sc == 255 ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, sc - 127);
+  float v[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) v[u] = e2m1_decode((w >> (4 * u)) & 15u) * x;
+  reinterpret_cast<uint4*>(dst)[idx] = pack_bf16x8(v);
+}
+
+// MXFP8 rows (E4M3, the scale rule of the layer's quantizer) of a bf16 matrix of
+// row pitch ld, for the activations of a block with 4-bit weights; blocks that
+// are not finite get the scale 255, so that their tokens come out as NaN.
+__global__ __launch_bounds__(256) void mxfp8_rows_kernel(const bf16_t* __restrict__ src, int64_t ld, int64_t n8,
+                                                        int k8, uint8_t* __restrict__ q,
+                                                        uint8_t* __restrict__ scales) {
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= n8) return;
+  const int64_t r = idx / k8, c = idx - r * k8;
+  float v[8];
+  unpack_bf16x8(reinterpret_cast<const uint4*>(src + r * ld)[c], v);
+  const uint32_t m = block_max_bits(v);
+  const bool nan = m >= 0x7F800000u;
+  const int sc = nan ? 255 : mx_scale_byte(__uint_as_float(m));
+  const float inv = mx_inv_scale(sc);
+  const uint32_t lo = e4m3_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+  const uint32_t hi = e4m3_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+  reinterpret_cast<uint2*>(q)[idx] = nan ? make_uint2(0, 0) : make_uint2(lo, hi);
+  if ((idx & 3) == 0) scales[idx >> 2] = (uint8_t)sc;
+}
+
+// ------------------------------------------------------------------ product, 128 x 128 tile
+// A slot holds SK elements of K per row: 128 where A is E4M3 (128-byte rows of A,
+// 64-byte rows of B), 256 where both are E2M1 (128-byte rows of both). A lane of
+// v_mfma_scale_f32_32x32x64_f8f6f4 supplies row l % 32: of E2M1 the 32 elements
+// from 32 * (l / 32) on (16 bytes), of E4M3 the 16 bytes from 16 * (l / 32) on and
+// those 32 further; the scale of block l / 32 of its row (checked on gfx950).
+template <bool A8>
+struct MxTile {
+  static constexpr int SK = A8 ? 128 : 256;
+  static constexpr int RBA = 128, RBB = SK / 2;
+  static constexpr int kA = 128 * RBA, kB = 128 * RBB, kS = SK / 128 * 1024;
+  static constexpr int kSlot = kA + kB + kS;
+  static constexpr int kLds = 2 * kSlot > kLds128 ? 2 * kSlot : kLds128;
+};
+
+// scale words (four blocks of 32, one word per 128 of K) of the tile's 128 A rows
+// (wavefronts 0 and 1) and 128 B rows (2 and 3); words past K read as zero
+template <int WORDS>
+struct CopyScales {
+  static constexpr int kDma = WORDS;
+  const uint8_t* p;
+  int nb;                                        // scale bytes per row
+  template <class RA, class RB>
+  MOK_DEV CopyScales(const RA& ra, const RB& rb, int K) : nb(K / 32) {
+    const int w = wave_id(), r = 64 * (w & 1) + lane_id();
+    p = w < 2 ? ra.row(r) : rb.row(r);
+  }
+  MOK_DEV void dma(int j, uint32_t slot) const {
+#pragma unroll
+    for (int q = 0; q < WORDS; ++q) {
+      const int o = (j * WORDS + q) * 4;
+      copy4_to_lds(o < nb ? p + o : kZeroRow, slot + q * 1024 + wave_id() * 256);
+    }
+  }
+};
+
+template <bool A8, class LA, class LB, class LS>
+MOK_DEV void mx_loop128(uint8_t* lds, const LA& la, const LB& lb, const LS& ls, int j0, int j1, Acc<2, 2>& acc) {
+  using X = MxTile<A8>;
+  constexpr int kD = LA::kDma + LB::kDma + LS::kDma;
+  const uint32_t base = lds_addr(lds);
+  const int l = lane_id(), lr = l & 31, hl = l >> 5;
+  acc.zero();
+  const auto issue = [&](int j, int s) {
+    la.dma(j, base + s * X::kSlot);
+    lb.dma(j, base + s * X::kSlot + X::kA);
+    ls.dma(j, base + s * X::kSlot + X::kA + X::kB);
+  };
+  if (j0 < j1) issue(j0, 0);
+  if (j0 + 1 < j1) issue(j0 + 1, 1);
+  for (int j = j0; j < j1; ++j) {
+    const int s = (j - j0) & 1;
+    if (j + 1 < j1) wait_vm_lds<kD>();
+    else wait_vm_lds<0>();
+    barrier_lds();
+    const uint8_t* ta = lds + s * X::kSlot;
+    const uint8_t* tb = ta + X::kA;
+    const uint32_t* sc = reinterpret_cast<const uint32_t*>(tb + X::kB);
+#pragma unroll
+    for (int ks = 0; ks < X::SK / 64; ++ks) {
+      i32x8_t a[2], b[2];
+      int as[2], bs[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ra = G128::wm() * 64 + 32 * i + lr, rb = G128::wn() * 64 + 32 * i + lr;
+        const auto at = [](const uint8_t* p) { return *reinterpret_cast<const i32x4_t*>(p); };
+        const i32x4_t z = {0, 0, 0, 0};
+        i32x4_t a0, a1 = z, b0;
+        if constexpr (A8) {
+          a0 = at(ta + lds_at(ra, 4 * ks + hl));
+          a1 = at(ta + lds_at(ra, 4 * ks + 2 + hl));
+          b0 = at(tb + lds_at64(rb, 2 * ks + hl));
+        } else {
+          a0 = at(ta + lds_at(ra, 2 * ks + hl));
+          b0 = at(tb + lds_at(rb, 2 * ks + hl));
+        }
+        a[i] = i32x8_t{a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
+        b[i] = i32x8_t{b0[0], b0[1], b0[2], b0[3], 0, 0, 0, 0};
+        const int sh = 8 * (2 * (ks & 1) + hl), wd = (ks >> 1) * 256;
+        as[i] = (int)((sc[wd + ra] >> sh) & 0xFFu);
+        bs[i] = (int)((sc[wd + 128 + rb] >> sh) & 0xFFu);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          acc.c[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[i], b[n], acc.c[i][n], A8 ? 0 : 4, 4, 0,
+                                                                        as[i], 0, bs[n]);
+    }
+    barrier_lds_only();
+    if (j + 2 < j1) issue(j + 2, s);
+  }
+}
+
+// ------------------------------------------------------------------ epilogues
+// Eight columns from c on of row r as bf16, with the residual added before the
+// one rounding; rows that start off a 16-byte boundary, or end inside the eight
+// columns, go by element.
+MOK_DEV void mx_store8(const mok_mx_args& a, bool vec, int r, int c, float v[8]) {
+  if (c >= a.N) return;
+  const int64_t o = (int64_t)r * a.ldd + c;
+  if (vec && c + 8 <= a.N) {
+    if (a.res) {
+      float s[8];
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(a.res + o), s);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] += s[u];
+    }
+    store_nt(a.d + o, pack_bf16x8(v));
+  } else {
+    for (int u = 0; u < 8 && c + u < a.N; ++u)
+      a.d[o + u] = f32_to_bf16(a.res ? v[u] + bf16_to_f32(a.res[o + u]) : v[u]);
+  }
+}
+
+// 32 columns from c on of row r of h = act(g) * u, as E4M3 codes and a scale
+template <int ACT>
+MOK_DEV void mx_gate32(const mok_mx_args& a, int r, int c, const float g[32], const float u[32]) {
+  float h[32];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    h[i] = gate_act<ACT>(g[i]) * u[i];
+    m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+  }
+  const bool nan = m >= 0x7F800000u;
+  const int sc = nan ? 255 : mx_scale_byte(__uint_as_float(m));
+  const float inv = mx_inv_scale(sc);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = nan ? 0u : e4m3_pack4(h[4 * i] * inv, h[4 * i + 1] * inv, h[4 * i + 2] * inv, h[4 * i + 3] * inv);
+  uint4* d = reinterpret_cast<uint4*>(a.hq + (int64_t)r * a.N + c);
+  d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  a.hs[(int64_t)r * (a.N / 32) + c / 32] = (uint8_t)sc;
+}
+
+template <bool GLU>
+constexpr int mx_cols() { return GLU ? 64 : 128; }   // output columns of a tile
+
+template <bool A8, bool GLU, int ACT, bool SPLIT>
+__global__ __launch_bounds__(kThreads, 2) void mx128_kernel(mok_mx_args a, bool vec, int nr, int nc, int splits) {
+  using X = MxTile<A8>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[X::kLds];
+  const int tiles = nr * nc, i = dense_index((int64_t)tiles * splits);
+  if (i < 0) return;
+  const int split = SPLIT ? i / tiles : 0, t = SPLIT ? i % tiles : i;
+  int row, col;
+  dense_tile(t, nr, nc, 8, row, col);
+  const int m0 = row * 128, n0 = col * mx_cols<GLU>(), nrows = min(128, a.M - m0);
+  const int ns = (a.K + X::SK - 1) / X::SK;
+  const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
+  const int j1 = SPLIT ? (int)((int64_t)ns * (split + 1) / splits) : ns;
+  const int64_t ka = A8 ? a.K : a.K / 2, kb = a.K / 2, ks = a.K / 32;
+  const RowsStrided ra{a.a + m0 * ka, ka, nrows}, rsa{a.sa + m0 * ks, ks, nrows};
+  Acc<2, 2> acc;
+  const auto run = [&](const auto& rb, const auto& rsb) {
+    const CopyK<128, X::RBA> la(ra, ka);
+    const CopyK<128, X::RBB> lb(rb, kb);
+    const CopyScales<X::SK / 128> ls(rsa, rsb, a.K);
+    mx_loop128<A8>(lds, la, lb, ls, j0, j1, acc);
+  };
+  if constexpr (GLU) run(RowsGateUp(a.b, a.b2, kb, n0, a.N), RowsGateUp(a.sb, a.sb2, ks, n0, a.N));
+  else run(RowsStrided{a.b + n0 * kb, kb, a.N - n0}, RowsStrided{a.sb + n0 * ks, ks, a.N - n0});
+  stage128(lds, acc);
+  if constexpr (SPLIT) {
+    float* p = a.part + ((int64_t)split * tiles + t) * 16384;
+    for (int idx = threadIdx.x; idx < nrows * 32; idx += kThreads)
+      reinterpret_cast<float4*>(p)[idx] =
+          *reinterpret_cast<const float4*>(lds + (idx >> 5) * kPitch128 + (idx & 31) * 16);
+  } else if constexpr (GLU) {
+    const int r = (int)threadIdx.x >> 1, c = ((int)threadIdx.x & 1) * 32;
+    if (r < nrows && n0 + c < a.N) {
+      float g[32], u[32];
+      load_f32<32>(lds + r * kPitch128 + c * 8, g);
+      load_f32<32>(lds + r * kPitch128 + c * 8 + 128, u);
+      mx_gate32<ACT>(a, m0 + r, n0 + c, g, u);
+    }
+  } else {
+    for (int idx = threadIdx.x; idx < nrows * 16; idx += kThreads) {
+      const int r = idx >> 4, c = (idx & 15) * 8;
+      float v[8];
+      load_f32<8>(lds + r * kPitch128 + c * 4, v);
+      mx_store8(a, vec, m0 + r, n0 + c, v);
+    }
+  }
+}
+
+template <bool GLU, int ACT>
+__global__ __launch_bounds__(kThreads) void mx_join_kernel(mok_mx_args a, bool vec, int nr, int nc, int splits) {
+  const int tiles = nr * nc, t = (int)blockIdx.y;
+  int row, col;
+  dense_tile(t, nr, nc, 8, row, col);
+  const int idx = (int)blockIdx.x * kThreads + (int)threadIdx.x;
+  constexpr int W = GLU ? 32 : 8, CH = mx_cols<GLU>() / W;
+  const int r = idx / CH, c = (idx % CH) * W;
+  if (r >= min(128, a.M - row * 128)) return;
+  const int gc = col * mx_cols<GLU>() + c;
+  if (gc >= a.N) return;
+  const float* p = a.part + (int64_t)t * 16384 + r * 128 + (GLU ? 2 * c : c);
+  float v[W], u[W];
+#pragma unroll
+  for (int q = 0; q < W; ++q) v[q] = u[q] = 0.f;
+  for (int s = 0; s < splits; ++s, p += (int64_t)tiles * 16384) {
+    float q[W];
+    load_f32<W>(p, q);
+#pragma unroll
+    for (int x = 0; x < W; ++x) v[x] += q[x];
+    if constexpr (GLU) {
+      load_f32<W>(p + 32, q);
+#pragma unroll
+      for (int x = 0; x < W; ++x) u[x] += q[x];
+    }
+  }
+  if constexpr (GLU) mx_gate32<ACT>(a, row * 128 + r, gc, v, u);
+  else mx_store8(a, vec, row * 128 + r, gc, v);
+}
+
+// ------------------------------------------------------------------ host
+struct Plan {
+  int nr, nc, splits;
+};
+Plan plan_of(const mok_mx_args& a, bool glu) {
+  Plan p;
+  p.nr = (a.M + 127) / 128;
+  p.nc = glu ? (a.N + 63) / 64 : (a.N + 127) / 128;
+  const int64_t n = (int64_t)p.nr * p.nc, slots = a.K / (a.a8 ? 128 : 256);
+  int64_t sp = n > 0 ? 512 / n : 1;
+  sp = sp < slots / 4 ? sp : slots / 4;
+  p.splits = sp < 1 ? 1 : (int)sp;
+  return p;
+}
+
+template <bool A8, bool GLU, int ACT>
+hipError_t launch(const mok_mx_args& a, const Plan& p, hipStream_t st) {
+  const int64_t tiles = (int64_t)p.nr * p.nc;
+  if (tiles * p.splits > (1 << 30)) return hipErrorInvalidValue;
+  if (tiles == 0) return hipSuccess;
+  const bool vec = a.ldd % 8 == 0 && ((uintptr_t)a.d | (uintptr_t)a.res) % 16 == 0;
+  const dim3 grid(dense_grid(tiles * p.splits)), block(kThreads);
+  if (p.splits == 1) {
+    hipLaunchKernelGGL((mx128_kernel<A8, GLU, ACT, false>), grid, block, 0, st, a, vec, p.nr, p.nc, 1);
+  } else {
+    hipLaunchKernelGGL((mx128_kernel<A8, GLU, ACT, true>), grid, block, 0, st, a, vec, p.nr, p.nc, p.splits);
+    const int ch = 128 * (GLU ? 2 : 16);
+    hipLaunchKernelGGL((mx_join_kernel<GLU, ACT>), dim3(ch / kThreads, (unsigned)tiles), block, 0, st, a, vec, p.nr,
+                       p.nc, p.splits);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t mok_launch_mxfp4_quantize(const bf16_t* src, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
+                                     hipStream_t st) {
+  const int64_t n8 = rows * (K / 8);
+  if (n8 <= 0) return hipSuccess;
+  const int64_t grid = (n8 + 255) / 256;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(mxfp4_quantize_kernel, dim3((unsigned)grid), dim3(256), 0, st, src, n8, q, scales);
+  return hipGetLastError();
+}
+
+hipError_t mok_launch_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K,
+                                       bf16_t* dst, hipStream_t st) {
+  const int64_t n8 = rows * (K / 8);
+  if (n8 <= 0) return hipSuccess;
+  const int64_t grid = (n8 + 255) / 256;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(mxfp4_dequantize_kernel, dim3((unsigned)grid), dim3(256), 0, st, q, scales, n8, dst);
+  return hipGetLastError();
+}
+
+hipError_t mok_launch_mxfp8_rows(const bf16_t* src, int64_t ld, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
+                                 hipStream_t st) {
+  const int64_t n8 = rows * (K / 8);
+  if (n8 <= 0) return hipSuccess;
+  const int64_t grid = (n8 + 255) / 256;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(mxfp8_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, src, ld, n8, (int)(K / 8), q, scales);
+  return hipGetLastError();
+}
+
+size_t mok_mx_part_bytes(const mok_mx_args& a, bool glu) {
+  const Plan p = plan_of(a, glu);
+  return p.splits > 1 ? (size_t)p.splits * p.nr * p.nc * 65536 : 0;
+}
+
+hipError_t mok_launch_mx(const mok_mx_args& a, bool glu, int act, hipStream_t st) {
+  const Plan p = plan_of(a, glu);
+  if (!glu) return a.a8 ? launch<true, false, 0>(a, p, st) : launch<false, false, 0>(a, p, st);
+  if (!a.a8) return hipErrorInvalidValue;
+  return act == 0 ? launch<true, true, 0>(a, p, st) : launch<true, true, 1>(a, p, st);
+}

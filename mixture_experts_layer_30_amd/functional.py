@@ -9,8 +9,11 @@ import dataclasses
 
 import torch
 
-from . import (MOK_BF16, backward, buffer_sizes, build_schedule, forward, forward_fused, make_config,
-               make_problem, mxfp8_quantize, mxfp8_quantize_transposed, schedule_layout)
+from . import (ACT_SILU, MOK_BF16, backward, buffer_sizes, build_schedule, ffn_backward, ffn_buffer_sizes,
+               ffn_forward, forward, forward_fused, make_config, make_ffn_problem, make_mx_problem, make_problem,
+               mx_matmul, mx_matmul_workspace, mxfp8_quantize, mxfp8_quantize_transposed, schedule_layout)
+from . import mxfp4_dequantize as _mxfp4_dequantize
+from . import mxfp4_quantize as _mxfp4_quantize
 
 
 @dataclasses.dataclass
@@ -114,3 +117,78 @@ def read_schedule(w: Workspace):
         "M": L.minibatch_rows, "n_slots": L.ring_slots, "n_mb": L.n_minibatches,
         "fwd_tile_rows": L.fwd_tile_rows, "bwd_tile_rows": L.bwd_tile_rows,
     }
+
+
+# ---------------------------------------------------------------- MXFP4 and the dense block
+def mxfp4_quantize(src):
+    """(codes [..., K/2], scales [..., K/32]) of the bf16 rows of src [..., K]."""
+    q = torch.empty((*src.shape[:-1], src.shape[-1] // 2), dtype=torch.uint8, device=src.device)
+    s = torch.empty((*src.shape[:-1], src.shape[-1] // 32), dtype=torch.uint8, device=src.device)
+    _mxfp4_quantize(src, q, s)
+    return q, s
+
+
+def mxfp4_dequantize(q, scales):
+    """The bf16 values [..., K] of MXFP4 codes and scales."""
+    out = torch.empty((*q.shape[:-1], 2 * q.shape[-1]), dtype=torch.bfloat16, device=q.device)
+    _mxfp4_dequantize(q, scales, out)
+    return out
+
+
+@dataclasses.dataclass
+class MxWorkspace:
+    problem: object
+    workspace: torch.Tensor | None
+
+
+def get_mx_matmul_workspace(M, N, K, a_dtype, device="cuda"):
+    """The problem and scratch of one product shape."""
+    problem = make_mx_problem(M, N, K, a_dtype)
+    n = mx_matmul_workspace(problem)
+    return MxWorkspace(problem, torch.empty(n, dtype=torch.uint8, device=device) if n else None)
+
+
+def run_mx_matmul(w: MxWorkspace, a, a_scales, b, b_scales, out=None):
+    """out [M][N] bf16 = A . B^T, B in MXFP4, A in the workspace's a_dtype."""
+    if out is None:
+        out = torch.empty((w.problem.M, w.problem.N), dtype=torch.bfloat16, device=a.device)
+    mx_matmul(w.problem, a, a_scales, b, b_scales, out, w.workspace)
+    return out
+
+
+@dataclasses.dataclass
+class FfnWorkspace:
+    problem: object
+    workspace: torch.Tensor
+    ctx: torch.Tensor | None     # [T][2I] bf16: the pre-activations a | b of the last forward
+
+
+def get_ffn_workspace(T, H, I, dtype=MOK_BF16, activation=ACT_SILU, device="cuda", training=True):
+    """Allocate the workspace and (training) the saved context of one dense block."""
+    problem = make_ffn_problem(T, H, I, dtype, activation)
+    ws, cb = ffn_buffer_sizes(problem)
+    ctx = torch.empty((T, 2 * I), dtype=torch.bfloat16, device=device) if training and dtype == MOK_BF16 else None
+    return FfnWorkspace(problem, torch.empty(max(ws, 16), dtype=torch.uint8, device=device), ctx)
+
+
+def run_ffn_forward(w: FfnWorkspace, x, weights, residual=None, y=None):
+    """y = block(x) (+ residual, which may be the y passed in); saves the context if the workspace holds one."""
+    if y is None:
+        y = torch.empty((x.shape[0], x.shape[1]), dtype=x.dtype, device=x.device)
+    ffn_forward(w.problem, x, weights, y, w.workspace, residual=residual, ctx=w.ctx)
+    return y
+
+
+def run_ffn_backward(w: FfnWorkspace, x, weights, dy):
+    """(dx, dw_gate, dw_up, dw_down) from the context of the last forward."""
+    wg, wu, wd = weights[:3]
+    dx = torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=x.device)
+    dwg, dwu, dwd = torch.empty_like(wg), torch.empty_like(wu), torch.empty_like(wd)
+    ffn_backward(w.problem, w.ctx, x, weights, dy, dx, dwg, dwu, dwd, w.workspace)
+    return dx, dwg, dwu, dwd
+
+
+def quantize_ffn_weights_mxfp4(wg, wu, wd):
+    """The six tensors a dense block with MXFP4 weights takes (codes, then scales)."""
+    (qg, sg), (qu, su), (qd, sd) = (mxfp4_quantize(m) for m in (wg, wu, wd))
+    return qg, qu, qd, sg, su, sd

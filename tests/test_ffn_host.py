@@ -1,0 +1,122 @@
+"""Host-side tests of the dense block's and the MXFP4 calls (no GPU needed): sizes,
+and every argument error found before anything touches a device."""
+import ctypes
+
+import pytest
+import torch
+
+import mixture_experts_layer_30_amd as mok
+from mixture_experts_layer_30_amd import functional as F
+
+FAKE = ctypes.c_void_p(0x1000)
+INV, UNS, SMALL = mok.MOK_ERR_INVALID_ARG, mok.MOK_ERR_UNSUPPORTED, mok.MOK_ERR_BUFFER_TOO_SMALL
+
+
+def test_ffn_sizes():
+    ws, ctx = mok.ffn_buffer_sizes(mok.make_ffn_problem(300, 264, 136))
+    assert ctx == 300 * 2 * 136 * 2 and ws >= 300 * (136 + 2 * 192) * 2
+    ws, ctx = mok.ffn_buffer_sizes(mok.make_ffn_problem(300, 256, 128, mok.MOK_MXFP4))
+    assert ctx == 0 and ws >= 300 * (256 + 8 + 128 + 4)
+    assert mok.ffn_buffer_sizes(mok.make_ffn_problem(0, 8, 8))[1] == 0
+    # the partial tiles of a product split along K stay within 512 of them
+    for T in (1, 17, 64, 500, 4096):
+        for H, I in ((7168, 2048), (2048, 768), (256, 512)):
+            ws, _ = mok.ffn_buffer_sizes(mok.make_ffn_problem(T, H, I))
+            assert ws <= T * 2 * (3 * (I + 64) + H) + 600 * 65536
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INV), (dict(H=0), INV), (dict(I=0), INV), (dict(dtype=7), INV), (dict(activation=2), INV),
+    (dict(activation=-1), INV), (dict(dtype=mok.MOK_MXFP8), UNS), (dict(H=12), UNS), (dict(I=20), UNS),
+    (dict(dtype=mok.MOK_MXFP4, H=192), UNS), (dict(dtype=mok.MOK_MXFP4, I=64), UNS), (dict(ld_x=248), INV),
+    (dict(ld_y=260), INV), (dict(T=(1 << 30) + 1), UNS), (dict(H=(1 << 20) + 8), UNS),
+    (dict(T=1 << 30, H=1 << 20), UNS),
+])
+def test_ffn_problems_refused(kw, status):
+    p = dict(T=64, H=256, I=256)
+    p.update(kw)
+    with pytest.raises(mok.MokError) as e:
+        mok.ffn_buffer_sizes(mok.make_ffn_problem(**p))
+    assert e.value.status == status
+
+
+def test_ffn_calls_refuse_before_any_launch():
+    L = mok.lib()
+    p = mok.make_ffn_problem(64, 256, 256)
+    ws, _ = mok.ffn_buffer_sizes(p)
+    w = mok.Weights(0x1000, 0x1000, 0x1000)
+
+    def fwd(p=p, x=FAKE, w=w, res=None, y=FAKE, ctx=None, wsp=FAKE, n=ws):
+        return L.mok_ffn_forward(ctypes.byref(p), x, ctypes.byref(w), res, y, ctx, wsp, n, None)
+
+    odd = ctypes.c_void_p(0x1008)
+    assert fwd(x=None) == INV and fwd(y=None) == INV
+    assert fwd(x=odd) == INV and fwd(y=odd) == INV and fwd(res=odd) == INV and fwd(ctx=odd) == INV
+    assert fwd(w=mok.Weights(0x1000, None, 0x1000)) == INV and fwd(w=mok.Weights(0x1000, 0x1008, 0x1000)) == INV
+    assert fwd(n=ws - 1) == SMALL and fwd(wsp=None) == SMALL
+    m = mok.make_ffn_problem(64, 256, 256, mok.MOK_MXFP4)
+    nm, _ = mok.ffn_buffer_sizes(m)
+    wm = mok.Weights(0x1000, 0x1000, 0x1000, 0x1000, 0x1000, 0x1000)
+    assert fwd(p=m, n=nm) == INV                                   # no scales
+    assert fwd(p=m, n=nm, w=mok.Weights(0x1000, 0x1000, 0x1000, 0x1000, 0x1002, 0x1000)) == INV
+    assert fwd(p=m, n=nm, w=wm, ctx=FAKE) == UNS
+    assert fwd(p=m, n=nm - 1, w=wm) == SMALL
+
+    def bwd(p=p, ctx=FAKE, x=FAKE, w=w, dy=FAKE, dx=FAKE, g=FAKE, u=FAKE, d=FAKE, n=ws):
+        return L.mok_ffn_backward(ctypes.byref(p), ctx, x, ctypes.byref(w), dy, dx, g, u, d, FAKE, n, None)
+
+    for k in ("ctx", "x", "dy", "dx", "g", "u", "d"):
+        assert bwd(**{k: None}) == INV, k
+        assert bwd(**{k: odd}) == INV, k
+    assert bwd(n=16) == SMALL and bwd(p=m, w=wm) == UNS
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), INV), (dict(N=-1), INV), (dict(K=0), INV), (dict(K=160), UNS), (dict(a_dtype=0), INV),
+    (dict(ld_d=99), INV), (dict(K=1 << 21), UNS), (dict(M=1 << 30, N=1 << 30), UNS),
+])
+def test_mx_problems_refused(kw, status):
+    p = dict(M=10, N=100, K=256, a_dtype=mok.MOK_MXFP4)
+    p.update(kw)
+    with pytest.raises(mok.MokError) as e:
+        mok.mx_matmul_workspace(mok.make_mx_problem(**p))
+    assert e.value.status == status
+
+
+def test_mx_calls_refuse_before_any_launch():
+    L = mok.lib()
+    odd, odd4 = ctypes.c_void_p(0x1008), ctypes.c_void_p(0x1002)
+    for f in (lambda s, q, c, r=4, K=64: L.mok_mxfp4_quantize(s, r, K, q, c, None),
+              lambda s, q, c, r=4, K=64: L.mok_mxfp4_dequantize(q, c, r, K, s, None)):
+        assert f(None, FAKE, FAKE) == INV and f(FAKE, None, FAKE) == INV and f(FAKE, FAKE, None) == INV
+        assert f(odd, FAKE, FAKE) == INV and f(FAKE, odd4, FAKE) == INV
+        assert f(FAKE, FAKE, FAKE, K=48) == INV and f(FAKE, FAKE, FAKE, K=0) == INV and f(FAKE, FAKE, FAKE, r=-1) == INV
+        assert f(FAKE, FAKE, FAKE, r=1 << 35, K=32) == UNS
+    p = mok.make_mx_problem(3, 512, 8192, mok.MOK_MXFP4)
+    n = mok.mx_matmul_workspace(p)
+    args = [FAKE] * 5
+
+    def mm(i=None, v=None, ws=FAKE, n=n):
+        a = list(args)
+        if i is not None:
+            a[i] = v
+        return L.mok_mx_matmul(ctypes.byref(p), *a, ws, n, None)
+
+    for i in range(5):
+        assert mm(i, None) == INV
+    assert mm(0, odd) == INV and mm(2, odd) == INV and mm(1, odd4) == INV and mm(3, odd4) == INV
+    assert mm(4, ctypes.c_void_p(0x1001)) == INV
+    if n:
+        assert mm(n=n - 1) == SMALL and mm(ws=None) == SMALL
+
+
+def test_binding_refuses_tensors_off_the_gpu():
+    x = torch.zeros((4, 256), dtype=torch.bfloat16)
+    with pytest.raises(mok.MokError) as e:
+        F.mxfp4_quantize(x)
+    assert e.value.status == INV
+    p = mok.make_ffn_problem(4, 256, 256)
+    w = tuple(torch.zeros((256, 256), dtype=torch.bfloat16) for _ in range(3))
+    with pytest.raises(mok.MokError) as e:
+        mok.ffn_forward(p, x, w, x, torch.zeros(16, dtype=torch.uint8))
+    assert e.value.status == INV
