@@ -306,16 +306,21 @@ def router_backward(problem, schedule, x, w_router, topk_ids, topk_w, d_topk_w, 
 # These calls check their tensors (device, type, shape, row layout) and run on
 # the tensors' device: with the caller's stream, or that device's current one.
 
+_types = None
+
+
 def _want(what, t, dtype, shape, rows=False, device=None):
     """t is a device tensor of this type and shape, contiguous (rows=True: with
     contiguous elements within a row, rows at any pitch)."""
-    import torch
-    names = {"bf16": torch.bfloat16, "u8": torch.uint8}
+    global _types
+    if _types is None:
+        import torch
+        _types = {"bf16": torch.bfloat16, "u8": torch.uint8}
     if not t.is_cuda or (device is not None and t.device != device):
         raise MokError(MOK_ERR_INVALID_ARG, f"{what}: not on the call's GPU ({t.device})")
-    if t.dtype != names[dtype] or tuple(t.shape) != tuple(shape):
-        raise MokError(MOK_ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, wanted {names[dtype]} {tuple(shape)}")
-    if not t.is_contiguous() and not (rows and t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
+    if t.dtype is not _types[dtype] or t.shape != shape:
+        raise MokError(MOK_ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, wanted {dtype} {tuple(shape)}")
+    if not t.is_contiguous() and not (rows and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
         raise MokError(MOK_ERR_INVALID_ARG, f"{what}: strides {t.stride()}")
 
 
@@ -324,21 +329,28 @@ def _pitch(t):
     return 0 if t.is_contiguous() else t.stride(0)
 
 
-class _on:
-    """The device of `t` as the current one for the call (nothing where it is already)."""
-    __slots__ = ("ctx",)
+def _scratch(workspace, device):
+    """(pointer, bytes) of a workspace tensor or None."""
+    if workspace is None:
+        return None, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise MokError(MOK_ERR_INVALID_ARG, f"workspace: not contiguous memory of {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
-    def __init__(self, t):
-        import torch
-        self.ctx = torch.cuda.device(t.device) if t.device.index != torch.cuda.current_device() else None
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _run(what, t, stream, fn, *args):
+    """fn(*args, stream) on the device of t: the caller's stream, or that device's current one."""
+    import torch
+    index = t.device.index
+    # (the raw handle: torch.cuda.current_stream builds a Stream object, 3 us a call)
+    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if index == torch.cuda.current_device():
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, st)
+    if status != MOK_OK:
+        raise MokError(status, what)
 
 
 def _rows_K(src):
@@ -352,9 +364,8 @@ def mxfp4_quantize(src, q, scales, stream=None):
     _want("src", src, "bf16", src.shape)
     _want("q", q, "u8", (*src.shape[:-1], K // 2), device=src.device)
     _want("scales", scales, "u8", (*src.shape[:-1], K // 32), device=src.device)
-    with _on(src):
-        _check(lib().mok_mxfp4_quantize(_ptr(src), rows, K, _ptr(q), _ptr(scales), _stream(stream)),
-               "mok_mxfp4_quantize")
+    _run("mok_mxfp4_quantize", src, stream, lib().mok_mxfp4_quantize, src.data_ptr(), rows, K, q.data_ptr(),
+         scales.data_ptr())
 
 
 def mxfp4_dequantize(q, scales, dst, stream=None):
@@ -363,9 +374,8 @@ def mxfp4_dequantize(q, scales, dst, stream=None):
     _want("dst", dst, "bf16", dst.shape)
     _want("q", q, "u8", (*dst.shape[:-1], K // 2), device=dst.device)
     _want("scales", scales, "u8", (*dst.shape[:-1], K // 32), device=dst.device)
-    with _on(dst):
-        _check(lib().mok_mxfp4_dequantize(_ptr(q), _ptr(scales), rows, K, _ptr(dst), _stream(stream)),
-               "mok_mxfp4_dequantize")
+    _run("mok_mxfp4_dequantize", dst, stream, lib().mok_mxfp4_dequantize, q.data_ptr(), scales.data_ptr(), rows, K,
+         dst.data_ptr())
 
 
 def make_mx_problem(M, N, K, a_dtype, ld_d=0) -> MxProblem:
@@ -390,10 +400,8 @@ def mx_matmul(problem, a, a_scales, b, b_scales, d, workspace, stream=None):
     _want("b", b, "u8", (N, K // 2), device=dev)
     _want("b_scales", b_scales, "u8", (N, K // 32), device=dev)
     p = MxProblem(M, N, K, _pitch(d), problem.a_dtype)
-    with _on(d):
-        _check(lib().mok_mx_matmul(ctypes.byref(p), _ptr(a), _ptr(a_scales), _ptr(b), _ptr(b_scales), _ptr(d),
-                                   _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                   _stream(stream)), "mok_mx_matmul")
+    _run("mok_mx_matmul", d, stream, lib().mok_mx_matmul, ctypes.byref(p), a.data_ptr(), a_scales.data_ptr(),
+         b.data_ptr(), b_scales.data_ptr(), d.data_ptr(), *_scratch(workspace, dev))
 
 
 def make_ffn_problem(T, H, I, dtype=MOK_BF16, activation=ACT_SILU, ld_x=0, ld_y=0) -> FfnProblem:
@@ -442,16 +450,16 @@ def ffn_forward(problem, x, weights, y, workspace, residual=None, ctx=None, stre
         _want("ctx", ctx, "bf16", (T, 2 * problem.I), device=dev)
     w = _ffn_weights(problem, weights, dev)
     p = _ffn_call(problem, _pitch(x), _pitch(y))
-    with _on(x):
-        _check(lib().mok_ffn_forward(ctypes.byref(p), _ptr(x), ctypes.byref(w), _ptr(residual), _ptr(y), _ptr(ctx),
-                                     _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                     _stream(stream)), "mok_ffn_forward")
+    _run("mok_ffn_forward", x, stream, lib().mok_ffn_forward, ctypes.byref(p), x.data_ptr(), ctypes.byref(w),
+         _ptr(residual), y.data_ptr(), _ptr(ctx), *_scratch(workspace, dev))
 
 
 def ffn_backward(problem, ctx, x, weights, dy, dx, dw_gate, dw_up, dw_down, workspace, stream=None):
     """Gradients of <dy, y>; x and dx share one row pitch, dy may have another."""
     T, H, I = problem.T, problem.H, problem.I
     dev = x.device
+    if ctx is None:
+        raise MokError(MOK_ERR_INVALID_ARG, "ctx: no context was saved by a forward")
     _want("x", x, "bf16", (T, H), rows=True)
     _want("dy", dy, "bf16", (T, H), rows=True, device=dev)
     _want("dx", dx, "bf16", (T, H), rows=True, device=dev)
@@ -462,11 +470,9 @@ def ffn_backward(problem, ctx, x, weights, dy, dx, dw_gate, dw_up, dw_down, work
         raise MokError(MOK_ERR_INVALID_ARG, "dx: another row pitch than x")
     w = _ffn_weights(problem, weights, dev)
     p = _ffn_call(problem, _pitch(x), _pitch(dy))
-    with _on(x):
-        _check(lib().mok_ffn_backward(ctypes.byref(p), _ptr(ctx), _ptr(x), ctypes.byref(w), _ptr(dy), _ptr(dx),
-                                      _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream(stream)),
-               "mok_ffn_backward")
+    _run("mok_ffn_backward", x, stream, lib().mok_ffn_backward, ctypes.byref(p), ctx.data_ptr(), x.data_ptr(),
+         ctypes.byref(w), dy.data_ptr(), dx.data_ptr(), dw_gate.data_ptr(), dw_up.data_ptr(), dw_down.data_ptr(),
+         *_scratch(workspace, dev))
 
 
 def trace_enable(on=True):

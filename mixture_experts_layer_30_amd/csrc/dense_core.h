@@ -209,6 +209,50 @@ MOK_DEV void load_f32(const void* p, float v[W]) {
   }
 }
 
+// ------------------------------------------------------------------ few rows
+// Products with at most kFewRows rows of x read the weights once and are bound by
+// that. A workgroup of eight wavefronts takes 16 weight rows (one 16 x 16
+// fragment; for gate|up 8 gate and 8 up rows, so that the gate's product stays in
+// the workgroup) and every wavefront a contiguous eighth of K, straight from
+// global memory into registers in the layout of the matrix instructions, two
+// batches of K in flight and no barrier until the eight partial sums meet in
+// LDS, in wavefront order. Sixteen rows per workgroup make enough workgroups to
+// draw on every CU's share of the bandwidth (an expert of 2048 x 7168: 256).
+constexpr int kFewRows = 64;
+constexpr int kFewThreads = 512, kFewWaves = 8;
+typedef __attribute__((ext_vector_type(4))) float f4_t;
+
+// acc[nt][q] of lane l: weight row 4 * (l / 16) + q, token 16 nt + l % 16
+template <int NT>
+MOK_DEV void few_put(float* red, const f4_t acc[NT]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    *reinterpret_cast<f4_t*>(red + ((wave_id() * NT + n) * 64 + lane_id()) * 4) = acc[n];
+  __syncthreads();
+}
+// the sum over the wavefronts of weight row `row`, token `t`
+template <int NT>
+MOK_DEV float few_get(const float* red, int row, int t) {
+  const float* p = red + ((t >> 4) * 64 + (row >> 2) * 16 + (t & 15)) * 4 + (row & 3);
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < kFewWaves; ++w) s += p[w * NT * 256];
+  return s;
+}
+// batches [b, e) of this wavefront in units of K: run load(buffer, k), compute(buffer, k)
+// with the next batch's loads issued before the current one is used
+template <int U, class Load, class Compute>
+MOK_DEV void few_pipeline(int b, int e, Load&& load, Compute&& compute) {
+  if (b >= e) return;
+  load(0, b);
+  for (int j = b; j < e; j += 2 * U) {
+    if (j + U < e) load(1, j + U);
+    compute(0, j);
+    if (j + 2 * U < e) load(0, j + 2 * U);
+    if (j + U < e) compute(1, j + U);
+  }
+}
+
 // ------------------------------------------------------------------ tile order
 // The nr x nc tiles of a product are numbered in groups of `grp` row tiles,
 // column by column within a group, and XCD k (workgroups wg with wg mod 8 = k)

@@ -69,7 +69,7 @@ mok_mx_args mx_down(const Ffn& r) {
 
 // Workspace carve-up; forward and backward share the bytes.
 struct FfnWs {
-  size_t h, hs, xq, xs, part, total;             // forward (hs, xq, xs: MXFP4)
+  size_t h, hf, hs, xq, xs, part, total;         // forward (hf, hs, xq, xs: MXFP4)
 };
 struct FfnBwdWs {
   size_t h, dab, part, total;
@@ -79,6 +79,7 @@ FfnWs fwd_ws(const Ffn& r) {
   const size_t T = (size_t)r.T, H = (size_t)r.H, I = (size_t)r.I;
   size_t o = 0, part;
   w.h = o;    o = align_up(o + T * I * (r.mx ? 1 : 2));
+  w.hf = o;   o = align_up(o + (r.mx && mok_mx_few((int)r.T) ? T * I * 4 : 0));
   w.hs = o;   o = align_up(o + (r.mx ? T * (I / 32) : 0));
   w.xq = o;   o = align_up(o + (r.mx ? T * H : 0));
   w.xs = o;   o = align_up(o + (r.mx ? T * (H / 32) : 0));
@@ -170,9 +171,11 @@ mok_status mok_ffn_forward(const mok_ffn_problem* problem, const void* x, const 
     d.a = u.hq; d.sa = u.hs;
     d.b = static_cast<const uint8_t*>(weights->w_down); d.sb = weights->s_down;
     d.d = static_cast<bf16_t*>(y); d.res = static_cast<const bf16_t*>(residual); d.part = part;
-    MOK_RUN("ffn_quantize_x", mok_launch_mxfp8_rows(static_cast<const bf16_t*>(x), r.ldx, r.T, r.H, ws + W.xq,
-                                                    ws + W.xs, st));
+    u.hf = reinterpret_cast<float*>(ws + W.hf);
+    MOK_RUN("ffn_quantize_x", mok_launch_mxfp8_rows(x, false, r.ldx, r.T, r.H, ws + W.xq, ws + W.xs, st));
     MOK_RUN("ffn_gateup_mxfp4", mok_launch_mx(u, true, r.act, st));
+    if (mok_mx_few((int)r.T))
+      MOK_RUN("ffn_quantize_h", mok_launch_mxfp8_rows(u.hf, true, r.I, r.T, r.I, ws + W.h, ws + W.hs, st));
     MOK_RUN("ffn_down_mxfp4", mok_launch_mx(d, false, 0, st));
     return MOK_OK;
   }

@@ -43,12 +43,13 @@ hipError_t mok_launch_mxfp4_quantize(const bf16_t* src, int64_t rows, int64_t K,
                                      hipStream_t st);
 hipError_t mok_launch_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K,
                                        bf16_t* dst, hipStream_t st);
-hipError_t mok_launch_mxfp8_rows(const bf16_t* src, int64_t ld, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
-                                 hipStream_t st);
+hipError_t mok_launch_mxfp8_rows(const void* src, bool f32, int64_t ld, int64_t rows, int64_t K, uint8_t* q,
+                                 uint8_t* scales, hipStream_t st);
 
 // d [M][N] (pitch ldd) = A . B^T (+ res), A in MXFP4 or MXFP8, B in MXFP4; with
 // glu: B = [Wg; Wu] interleaved by the kernel, N = I, and act(a)*b is written
-// as MXFP8 rows hq [M][N] with scales hs [M][N/32].
+// as MXFP8 rows hq [M][N] with scales hs [M][N/32], or, with few rows (mok_mx_few),
+// as fp32 rows hf [M][N].
 struct mok_mx_args {
   int M, N, K;
   bool a8;               // A is E4M3 (else E2M1)
@@ -64,6 +65,8 @@ struct mok_mx_args {
   uint8_t* hq;
   uint8_t* hs;
   float* part;
+  float* hf;
 };
+bool mok_mx_few(int M);
 size_t mok_mx_part_bytes(const mok_mx_args& a, bool glu);
 hipError_t mok_launch_mx(const mok_mx_args& a, bool glu, int act, hipStream_t st);

@@ -233,10 +233,98 @@ __global__ __launch_bounds__(kThreads, 1) void ffn256_kernel(mok_ffn_args a, int
   }
 }
 
+// ------------------------------------------------------------------ few tokens
+// One 16-row slice of the weights against every token (scheme in dense_core.h).
+// A slot is 64 elements of K: two 16-byte pieces per lane and row.
+template <int OP, int ACT, int NT>
+__global__ __launch_bounds__(kFewThreads) void ffn_few_kernel(mok_ffn_args a) {
+  static_assert(OP == FFN_GATEUP || OP == FFN_DOWN, "forward products");
+  constexpr int U = NT <= 2 ? 4 : 2;
+  __shared__ __attribute__((aligned(16))) float red[kFewWaves * NT * 256];
+  const int l = lane_id(), lr = l & 15, g = l >> 4;
+  const int K = OP == FFN_GATEUP ? a.H : a.I;
+  const bf16_t* wp;
+  const bf16_t* xp[NT];
+  const int c0 = (int)blockIdx.x * (OP == FFN_GATEUP ? 8 : 16);
+  if constexpr (OP == FFN_GATEUP) wp = (lr < 8 ? a.wg : a.wu) + (int64_t)(c0 + (lr & 7)) * K;
+  else wp = a.wd + (int64_t)min(c0 + lr, a.H - 1) * K;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int t = min(16 * n + lr, a.T - 1);
+    xp[n] = OP == FFN_GATEUP ? a.x + t * a.ldx : a.h + (int64_t)t * a.I;
+  }
+  const int ns = (K + 63) / 64;
+  const int b = ns * wave_id() / kFewWaves, e = ns * (wave_id() + 1) / kFewWaves;
+  bf16x8_t wv[2][U][2], xv[2][U][2][NT];
+  f4_t acc[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[n] = f4_t{0.f, 0.f, 0.f, 0.f};
+  // element of K of piece p of slot j (clamped into the row where it is past K)
+  const auto at = [&](int j, int p) { return min(64 * j + 32 * p + 8 * g, K - 8); };
+  const auto load = [&](int s, int j) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (j + u >= e) continue;                  // wave-uniform
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        wv[s][u][p] = *reinterpret_cast<const bf16x8_t*>(wp + at(j + u, p));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xv[s][u][p][n] = *reinterpret_cast<const bf16x8_t*>(xp[n] + at(j + u, p));
+      }
+    }
+  };
+  const auto compute = [&](int s, int j) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (j + u >= e) continue;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        // pieces past K: zeros on both sides
+        const bool in = 64 * (j + u) + 32 * p + 8 * g < K;
+        const bf16x8_t z = {};
+        const bf16x8_t w = in ? wv[s][u][p] : z;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, in ? xv[s][u][p][n] : z, acc[n], 0, 0, 0);
+      }
+    }
+  };
+  few_pipeline<U>(b, e, load, compute);
+  few_put<NT>(red, acc);
+  if constexpr (OP == FFN_GATEUP) {
+    for (int i = threadIdx.x; i < 8 * a.T; i += kFewThreads) {
+      const int c = i & 7, t = i >> 3;
+      const float v = few_get<NT>(red, c, t), w = few_get<NT>(red, c + 8, t);
+      a.h[(int64_t)t * a.I + c0 + c] = f32_to_bf16(gate_act<ACT>(v) * w);
+      if (a.ab) {
+        a.ab[(int64_t)t * 2 * a.I + c0 + c] = f32_to_bf16(v);
+        a.ab[(int64_t)t * 2 * a.I + a.I + c0 + c] = f32_to_bf16(w);
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < 16 * a.T; i += kFewThreads) {
+      const int c = i & 15, t = i >> 4;
+      if (c0 + c >= a.H) continue;
+      float v = few_get<NT>(red, c, t);
+      if (a.res) v += bf16_to_f32(a.res[t * a.ldy + c0 + c]);
+      a.y[t * a.ldy + c0 + c] = f32_to_bf16(v);
+    }
+  }
+}
+
+template <int OP, int ACT>
+hipError_t launch_few(const mok_ffn_args& a, hipStream_t st) {
+  const dim3 grid(OP == FFN_GATEUP ? a.I / 8 : (a.H + 15) / 16), block(kFewThreads);
+  if (a.T <= 16) hipLaunchKernelGGL((ffn_few_kernel<OP, ACT, 1>), grid, block, 0, st, a);
+  else if (a.T <= 32) hipLaunchKernelGGL((ffn_few_kernel<OP, ACT, 2>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((ffn_few_kernel<OP, ACT, 4>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
 // ------------------------------------------------------------------ host
 struct Plan {
   Shape s;
-  int tile, nr, nc, splits;
+  int tile, nr, nc, splits;                      // tile 0: few tokens
 };
 
 Plan plan_of(const mok_ffn_args& a, mok_ffn_op op) {
@@ -245,6 +333,11 @@ Plan plan_of(const mok_ffn_args& a, mok_ffn_op op) {
   const auto tiles = [&](int n) {
     return (int64_t)((p.s.M + n - 1) / n) * ((p.s.N + n - 1) / n) * p.s.batch;
   };
+  if (a.T <= kFewRows && (op == FFN_GATEUP || op == FFN_DOWN)) {
+    p.tile = p.nr = p.nc = 0;
+    p.splits = 1;
+    return p;
+  }
   p.tile = tiles(256) >= 256 ? 256 : 128;
   p.nr = (p.s.M + p.tile - 1) / p.tile;
   p.nc = (p.s.N + p.tile - 1) / p.tile;
@@ -260,6 +353,8 @@ Plan plan_of(const mok_ffn_args& a, mok_ffn_op op) {
 
 template <int OP, int ACT>
 hipError_t launch(const mok_ffn_args& a, const Plan& p, hipStream_t st) {
+  if constexpr (OP == FFN_GATEUP || OP == FFN_DOWN)
+    if (p.tile == 0) return a.T > 0 ? launch_few<OP, ACT>(a, st) : hipSuccess;
   const int64_t tiles = (int64_t)p.nr * p.nc * p.s.batch;
   if (tiles * p.splits > (1 << 30)) return hipErrorInvalidValue;
   if (tiles == 0) return hipSuccess;

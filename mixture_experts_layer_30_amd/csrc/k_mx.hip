@@ -85,17 +85,19 @@ __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __
   reinterpret_cast<uint4*>(dst)[idx] = pack_bf16x8(v);
 }
 
-// MXFP8 rows (E4M3, the scale rule of the layer's quantizer) of a bf16 matrix of
-// row pitch ld, for the activations of a block with 4-bit weights; blocks that
-// are not finite get the scale 255, so that their tokens come out as NaN.
-__global__ __launch_bounds__(256) void mxfp8_rows_kernel(const bf16_t* __restrict__ src, int64_t ld, int64_t n8,
+// MXFP8 rows (E4M3, the scale rule of the layer's quantizer) of a bf16 or fp32
+// matrix of row pitch ld, for the activations of a block with 4-bit weights;
+// blocks that are not finite get the scale 255, so that their tokens come out NaN.
+template <class T>
+__global__ __launch_bounds__(256) void mxfp8_rows_kernel(const T* __restrict__ src, int64_t ld, int64_t n8,
                                                         int k8, uint8_t* __restrict__ q,
                                                         uint8_t* __restrict__ scales) {
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= n8) return;
   const int64_t r = idx / k8, c = idx - r * k8;
   float v[8];
-  unpack_bf16x8(reinterpret_cast<const uint4*>(src + r * ld)[c], v);
+  if constexpr (sizeof(T) == 2) unpack_bf16x8(reinterpret_cast<const uint4*>(src + r * ld)[c], v);
+  else load_f32<8>(src + r * ld + 8 * c, v);
   const uint32_t m = block_max_bits(v);
   const bool nan = m >= 0x7F800000u;
   const int sc = nan ? 255 : mx_scale_byte(__uint_as_float(m));
@@ -325,12 +327,120 @@ __global__ __launch_bounds__(kThreads) void mx_join_kernel(mok_mx_args a, bool v
   else mx_store8(a, vec, row * 128 + r, gc, v);
 }
 
+// ------------------------------------------------------------------ few rows
+// The scheme of dense_core.h with v_mfma_scale_f32_16x16x128_f8f6f4: the 16 weight
+// rows (E2M1) are the first operand, 16 rows of A the second; lane l supplies row
+// l % 16 with the 32 weights from 32 g on (g = l / 16, 16 bytes), of E4M3 the 16 bytes
+// from 16 g on and those 64 further, and the scale of block g (checked on gfx950).
+// The rows of A are quantized by a launch of their own: every workgroup quantizing
+// them as it reads them took 9 us more at 16 rows of 7168 (256 workgroups repeat
+// the work) against 2.5 us for the launch. So h, of which a workgroup makes 8
+// columns and a block has 32, goes out as fp32.
+constexpr int kMxFewRows = 32;
+
+template <bool A8, bool GLU, int ACT, int NT>
+__global__ __launch_bounds__(kFewThreads) void mx_few_kernel(mok_mx_args a) {
+  constexpr int kX = A8 ? 2 : 1;                 // 16-byte pieces of a row of A per step
+  constexpr int U = 4;                           // steps per batch: one scale word per lane group
+  __shared__ __attribute__((aligned(16))) float red[kFewWaves * NT * 256];
+  const int l = lane_id(), lr = l & 15, g = l >> 4;
+  const int c0 = (int)blockIdx.x * (GLU ? 8 : 16);
+  const int64_t kb = a.K / 2, ks = a.K / 32;
+  const uint8_t* wp;
+  const uint8_t* wsp;
+  if constexpr (GLU) {
+    wp = (lr < 8 ? a.b : a.b2) + (c0 + (lr & 7)) * kb;
+    wsp = (lr < 8 ? a.sb : a.sb2) + (c0 + (lr & 7)) * ks;
+  } else {
+    wp = a.b + min(c0 + lr, a.N - 1) * kb;
+    wsp = a.sb + min(c0 + lr, a.N - 1) * ks;
+  }
+  const uint8_t* xp[NT];
+  const uint8_t* xsp[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int t = min(16 * n + lr, a.M - 1);
+    xp[n] = a.a + t * (A8 ? (int64_t)a.K : kb);
+    xsp[n] = a.sa + t * ks;
+  }
+  const int ns = a.K / 128;
+  const int b = ns * wave_id() / kFewWaves, e = ns * (wave_id() + 1) / kFewWaves;
+  i32x4_t wv[2][U], xv[2][U][NT][kX];
+  int wsv[2], xsv[2][NT];                        // scale words of step j0 + g
+  f4_t acc[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[n] = f4_t{0.f, 0.f, 0.f, 0.f};
+  const auto load = [&](int s, int j0) {
+    const int jg = min(j0 + g, ns - 1);
+    wsv[s] = *reinterpret_cast<const int*>(wsp + 4 * jg);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xsv[s][n] = *reinterpret_cast<const int*>(xsp[n] + 4 * jg);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u;
+      if (j >= e) continue;                      // wave-uniform
+      wv[s][u] = *reinterpret_cast<const i32x4_t*>(wp + 64 * j + 16 * g);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < kX; ++q)
+          xv[s][u][n][q] = *reinterpret_cast<const i32x4_t*>(xp[n] + (A8 ? 128 * j + 64 * q : 64 * j) + 16 * g);
+    }
+  };
+  const auto compute = [&](int s, int j0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (j0 + u >= e) continue;                 // wave-uniform
+      const i32x4_t w = wv[s][u];
+      const i32x8_t wa = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+      const int from = 16 * u + lr;              // the lane that holds this step's scale words
+      const int sw = (__shfl(wsv[s], from) >> (8 * g)) & 0xFF;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        i32x8_t x = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < kX; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[4 * q + i] = xv[s][u][n][q][i];
+        const int sx = (__shfl(xsv[s][n], from) >> (8 * g)) & 0xFF;
+        acc[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, x, acc[n], 4, A8 ? 0 : 4, 0, sw, 0, sx);
+      }
+    }
+  };
+  few_pipeline<U>(b, e, load, compute);
+  few_put<NT>(red, acc);
+  if constexpr (GLU) {
+    for (int i = threadIdx.x; i < 8 * a.M; i += kFewThreads) {
+      const int c = i & 7, t = i >> 3;
+      a.hf[(int64_t)t * a.N + c0 + c] = gate_act<ACT>(few_get<NT>(red, c, t)) * few_get<NT>(red, c + 8, t);
+    }
+  } else {
+    for (int i = threadIdx.x; i < 16 * a.M; i += kFewThreads) {
+      const int c = i & 15, t = i >> 4;
+      if (c0 + c >= a.N) continue;
+      float v = few_get<NT>(red, c, t);
+      const int64_t o = t * a.ldd + c0 + c;
+      if (a.res) v += bf16_to_f32(a.res[o]);
+      a.d[o] = f32_to_bf16(v);
+    }
+  }
+}
+
+template <bool A8, bool GLU, int ACT>
+hipError_t launch_few(const mok_mx_args& a, hipStream_t st) {
+  const dim3 grid(GLU ? a.N / 8 : (a.N + 15) / 16), block(kFewThreads);
+  if (a.M <= 16) hipLaunchKernelGGL((mx_few_kernel<A8, GLU, ACT, 1>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((mx_few_kernel<A8, GLU, ACT, 2>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
 // ------------------------------------------------------------------ host
 struct Plan {
   int nr, nc, splits;
 };
 Plan plan_of(const mok_mx_args& a, bool glu) {
   Plan p;
+  if (mok_mx_few(a.M)) return Plan{0, 0, 1};
   p.nr = (a.M + 127) / 128;
   p.nc = glu ? (a.N + 63) / 64 : (a.N + 127) / 128;
   const int64_t n = (int64_t)p.nr * p.nc, slots = a.K / (a.a8 ? 128 : 256);
@@ -380,13 +490,18 @@ hipError_t mok_launch_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, 
   return hipGetLastError();
 }
 
-hipError_t mok_launch_mxfp8_rows(const bf16_t* src, int64_t ld, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
-                                 hipStream_t st) {
+hipError_t mok_launch_mxfp8_rows(const void* src, bool f32, int64_t ld, int64_t rows, int64_t K, uint8_t* q,
+                                 uint8_t* scales, hipStream_t st) {
   const int64_t n8 = rows * (K / 8);
   if (n8 <= 0) return hipSuccess;
   const int64_t grid = (n8 + 255) / 256;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(mxfp8_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, src, ld, n8, (int)(K / 8), q, scales);
+  if (f32)
+    hipLaunchKernelGGL(mxfp8_rows_kernel<float>, dim3((unsigned)grid), dim3(256), 0, st, static_cast<const float*>(src),
+                       ld, n8, (int)(K / 8), q, scales);
+  else
+    hipLaunchKernelGGL(mxfp8_rows_kernel<bf16_t>, dim3((unsigned)grid), dim3(256), 0, st,
+                       static_cast<const bf16_t*>(src), ld, n8, (int)(K / 8), q, scales);
   return hipGetLastError();
 }
 
@@ -395,7 +510,14 @@ size_t mok_mx_part_bytes(const mok_mx_args& a, bool glu) {
   return p.splits > 1 ? (size_t)p.splits * p.nr * p.nc * 65536 : 0;
 }
 
+bool mok_mx_few(int M) { return M <= kMxFewRows; }
+
 hipError_t mok_launch_mx(const mok_mx_args& a, bool glu, int act, hipStream_t st) {
+  if (mok_mx_few(a.M)) {
+    if (a.M <= 0 || a.N <= 0) return hipSuccess;
+    if (glu) return act == 0 ? launch_few<true, true, 0>(a, st) : launch_few<true, true, 1>(a, st);
+    return a.a8 ? launch_few<true, false, 0>(a, st) : launch_few<false, false, 0>(a, st);
+  }
   const Plan p = plan_of(a, glu);
   if (!glu) return a.a8 ? launch<true, false, 0>(a, p, st) : launch<false, false, 0>(a, p, st);
   if (!a.a8) return hipErrorInvalidValue;
