@@ -388,7 +388,8 @@ mok_status mok_mx_matmul(const mok_mx_problem* problem, const uint8_t* a, const 
  * beside the routed ones), without a schedule:
  *   a = x Wg^T, b = x Wu^T, h = act(a) * b, y = h Wd^T (+ residual)
  * act is SiLU a*s(a) or GELU in its tanh form. x, dx [T][H] have row pitch
- * ld_x, and y, residual, dy row pitch ld_y (elements, multiples of 8, 0 = H).
+ * ld_x, and y, residual, dy row pitch ld_y (elements, multiples of 8, 0 = H,
+ * at most 2^22).
  * Weights as in mok_weights for one expert: w_gate, w_up [I][H], w_down [H][I].
  *   MOK_BF16:  any T >= 0, H and I multiples of 8; fp32 sums; a, b, h, da, db
  *              rounded to bf16 once where they are stored.

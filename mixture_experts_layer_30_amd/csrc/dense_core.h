@@ -23,108 +23,127 @@ MOK_DEV int lds_at64(int row, int chunk) {
 }
 
 // ------------------------------------------------------------------ copies
-// K-contiguous operand of R rows, RB bytes of K per row and slot. Rows past the
-// end repeat the last row (their products land in rows that are not stored);
-// bytes past kbytes read as zero, on both operands, so that nothing stored
-// behind a row (or behind the matrix) enters a product.
-template <int R, int RB>
+// All copies are buffer loads into LDS: a descriptor in scalar registers (base,
+// bytes), one 32-bit offset per lane and a scalar offset per copy. What lies past
+// the descriptor's bytes reads as zero, which covers rows past the last one and
+// k-rows past K without a branch. Measured on gfx950 with four wavefronts that
+// copy the panels of 256 x 256 tiles and four that multiply, nothing else and no
+// barrier between them: copies alone 42 us, products alone 37 us, both 52 us; with
+// global_load_lds and its 64-bit address per lane 43, 41 and 82 us: those
+// copies and the matrix instructions ran one after the other.
+typedef i32x4_t srd_t;
+MOK_DEV int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+MOK_DEV srd_t make_srd(const void* p, int64_t bytes) {
+  const uint64_t u = (uint64_t)p;
+  const int64_t n = bytes < 0 ? 0 : bytes;       // (callers stay below 2^31)
+  return srd_t{uni((int)u), uni((int)(u >> 32) & 0xFFFF), uni((int)n), 0x00020000};
+}
+// Bounds: a lane's offset alone has to be past the descriptor's bytes where nothing
+// may be read (the scalar offset, only ever a step along K inside a row, does not
+// move the bound), and offsets stay below 2^31: row pitches are at most 2^23 bytes.
+constexpr int kNowhere = 0x7ffffff0;             // past every descriptor's bytes
+// (the five wait states cover a descriptor or offset written by v_readfirstlane
+// right before, which the compiler does not see; m0 needs one of them)
+MOK_DEV void buf16_to_lds(srd_t srd, int off, int soff, uint32_t lds) {
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %2, %3 offen lds" ::"v"(off), "{m0}"(lds), "s"(srd), "s"(soff)
+               : "memory");
+}
+MOK_DEV void buf4_to_lds(srd_t srd, int off, int soff, uint32_t lds) {
+  asm volatile("s_nop 4\n\tbuffer_load_dword %0, %2, %3 offen lds" ::"v"(off), "{m0}"(lds), "s"(srd), "s"(soff)
+               : "memory");
+}
+MOK_DEV int copy_wave() { return wave_id() & 3; }  // four wavefronts share an operand's copies
+
+// Rows of a K-contiguous operand: row r at base + r * ld bytes; or, with two
+// bases, 32-row groups alternating between them (gate and up rows of the same
+// columns side by side, as in gemm_core.h).
+struct Rows1 {
+  static constexpr bool kTwo = false;
+  const void* p;
+  int64_t ld;
+  int n;                   // rows (>= 1)
+};
+struct Rows2 {
+  static constexpr bool kTwo = true;
+  const void* p;
+  const void* p2;
+  int64_t ld;
+  int n;                   // rows of each (>= 1)
+};
+
+// K-contiguous operand of 128 rows, RB bytes of K per row and slot; bytes past
+// kbytes read as zero, on both operands, so that nothing stored behind a row
+// enters a product.
+template <int RB, bool TWO>
 struct CopyK {
   static_assert(RB == 64 || RB == 128, "bytes of K per row and slot");
-  static constexpr int kDma = R * RB / 4096;     // 1 KiB windows per wavefront
-  static constexpr int kReads = 1;
-  const uint8_t* rowp[kDma];                     // this lane's 16 bytes of slot 0, per copy
-  int lcb, kbytes;
-  mutable uint32_t mb;
-  mutable bool tail;
+  static constexpr int kDma = 128 * RB / 4096;   // 1 KiB windows per wavefront
+  srd_t srd, srd2;
+  int off, step, lcb, kbytes;
   template <class Rows>
-  MOK_DEV CopyK(const Rows& src, int64_t kbytes_) : kbytes((int)kbytes_) {
-    const int w = (int)(threadIdx.x >> 6), l = lane_id();
-    // the window's rows differ between copies q by multiples of 32 (64-byte
-    // rows: 64) only, which leaves the chunk of a lane the same in all of them
-    int row0, lc;
-    if constexpr (RB == 128) {
-      row0 = swap03(8 * w + (l >> 3));
-      lc = (l & 7) ^ (row0 & 7);
-    } else {
-      row0 = 2 * swap02(8 * w + (l >> 3)) + ((l >> 2) & 1);
-      lc = (l & 3) ^ ((row0 >> 1) & 3);
+  MOK_DEV CopyK(const Rows& r, int64_t kbytes_) : kbytes((int)kbytes_) {
+    static_assert(Rows::kTwo == TWO, "row source");
+    const int w = copy_wave(), l = lane_id();
+    const int64_t bytes = (int64_t)(min(r.n, 128) - 1) * r.ld + kbytes_;
+    int row, lc;
+    if constexpr (RB == 128) {                   // copy q: rows 32 q .. +31
+      row = swap03(8 * w + (l >> 3));
+      lc = (l & 7) ^ (row & 7);
+    } else {                                     // copy q: rows 64 q + 16 w .. +15
+      row = 2 * swap02(8 * w + (l >> 3)) + ((l >> 2) & 1);
+      lc = (l & 3) ^ ((row >> 1) & 3);
     }
     lcb = lc * 16;
-#pragma unroll
-    for (int q = 0; q < kDma; ++q) rowp[q] = src.row(row0 + q * (RB == 128 ? 32 : 64)) + lcb;
-  }
-  MOK_DEV void dma1(int j, uint32_t slot, int q) const {
-    if (q == 0) {
-      mb = slot + wave_id() * 1024;
-      tail = (j + 1) * RB > kbytes;
+    srd = make_srd(r.p, bytes);
+    srd2 = srd;
+    if constexpr (TWO) {
+      srd2 = make_srd(r.p2, bytes);
+      if (RB == 64 && (w & 2)) srd = srd2;       // wavefronts 2, 3 copy up rows
+      row &= 31;
     }
-    const uint8_t* gp = rowp[q] + (int64_t)j * RB;
-    if (tail) {                                  // wave-uniform branch
-      asm volatile("");
-      if (j * RB + lcb >= kbytes) gp = kZeroRow;
-    }
-    copy16_to_lds(gp, mb + q * 4096);
+    off = row * (int)r.ld + lcb;
+    step = uni((RB == 64 && !TWO ? 64 : 32) * (int)r.ld);
   }
   MOK_DEV void dma(int j, uint32_t slot) const {
+    const uint32_t mb = slot + copy_wave() * 1024;
+    const bool past = (j + 1) * RB > kbytes && j * RB + lcb >= kbytes;
 #pragma unroll
-    for (int q = 0; q < kDma; ++q) dma1(j, slot, q);
+    for (int q = 0; q < kDma; ++q) {
+      const bool alt = TWO && RB == 128;         // groups q = 0, 2 gate, 1, 3 up
+      const int o = off + (alt ? q >> 1 : q) * step;
+      buf16_to_lds(alt && (q & 1) ? srd2 : srd, past ? kNowhere : o, uni(j * RB), mb + q * 4096);
+    }
   }
-  // bf16 fragment of 32 rows from r0: 16-wide K step kk of stage half h
+  // bf16 fragment of 32 rows from r0: 16-wide K step kk of half h
   MOK_DEV static bf16x8_t frag(const uint8_t* t, int r0, int h, int kk) {
     const int l = lane_id();
     return *reinterpret_cast<const bf16x8_t*>(t + lds_at(r0 + (l & 31), 4 * h + 2 * kk + (l >> 5)));
   }
 };
 
-// K-outer bf16 operand of R columns: element (k, n) at src0 + k*ld + 2n for the
-// first segment of kseg k-rows (a multiple of 64) and at src1 + (k - kseg)*ld +
-// 2n for the second; k-rows past kvalid in either segment read as zero, columns
-// past ncols repeat the last ones.
-template <int R>
+// K-outer bf16 operand of 128 columns: element (k, n) at src0 + k*ld + 2n for the
+// first segment of kseg k-rows (a multiple of 64) and at src1 + (k - kseg)*ld + 2n
+// for the second; k-rows past kvalid in either segment read as zero. Columns past
+// ncols read what follows them and land in output that is not stored.
 struct CopyT {
-  static constexpr int kDma = R / 32;
-  static constexpr int kReads = 2;
-  static constexpr int kCh = R / 8;              // 16-byte chunks per k-row
-  static constexpr int kRows = 64 / kCh;         // k-rows per 1 KiB window
+  static constexpr int kDma = 4;
   const uint8_t* src0;
   const uint8_t* src1;
-  int kseg, kvalid;
-  int64_t ld;
-  int64_t off[kDma];
-  int zoff;                                      // this lane's chunk of the zero row
-  mutable const uint8_t* pb;
-  mutable uint32_t mb;
-  mutable int kr;
-  MOK_DEV CopyT(const uint8_t* s0, const uint8_t* s1, int kseg_, int kvalid_, int64_t ld_, int ncols)
-      : src0(s0), src1(s1), kseg(kseg_), kvalid(kvalid_), ld(ld_) {
-    const int w = (int)(threadIdx.x >> 6), l = lane_id();
-#pragma unroll
-    for (int q = 0; q < kDma; ++q) {
-      const int kl = kRows * (w + 4 * q) + l / kCh;
-      const int c = min((l % kCh) ^ ((kl & 3) << 2), (ncols >> 3) - 1);
-      off[q] = (int64_t)kl * ld + c * 16;
-    }
-    zoff = (l & 31) * 16;
-  }
-  MOK_DEV void dma1(int j, uint32_t slot, int q) const {
-    if (q == 0) {
-      const bool second = j * 64 >= kseg;
-      const int k0 = second ? j * 64 - kseg : j * 64;
-      pb = (second ? src1 : src0) + (int64_t)k0 * ld;
-      mb = slot + wave_id() * 1024;
-      kr = kvalid - k0;
-    }
-    const uint8_t* gp = pb + off[q];
-    if (kr < 64) {
-      asm volatile("");
-      const int kl = kRows * ((int)(threadIdx.x >> 6) + 4 * q) + lane_id() / kCh;
-      if (kl >= kr) gp = kZeroRow + zoff;
-    }
-    copy16_to_lds(gp, mb + q * 4096);
+  int kseg, kvalid, ncols, off, ld;
+  MOK_DEV CopyT(const void* s0, const void* s1, int kseg_, int kvalid_, int64_t ld_, int ncols_)
+      : src0((const uint8_t*)s0), src1((const uint8_t*)s1), kseg(kseg_), kvalid(kvalid_), ncols(ncols_),
+        ld((int)ld_) {
+    const int l = lane_id(), kl = 4 * copy_wave() + (l >> 4);
+    off = kl * ld + (((l & 15) ^ ((kl & 3) << 2)) << 4);
   }
   MOK_DEV void dma(int j, uint32_t slot) const {
+    const bool second = j * 64 >= kseg;
+    const int k0 = second ? j * 64 - kseg : j * 64, kr = min(kvalid - k0, 64);
+    const srd_t srd = make_srd((second ? src1 : src0) + (int64_t)k0 * ld,
+                               kr > 0 ? (int64_t)(kr - 1) * ld + 2 * min(ncols, 128) : 0);
+    const uint32_t mb = slot + copy_wave() * 1024;
 #pragma unroll
-    for (int q = 0; q < kDma; ++q) dma1(j, slot, q);
+    for (int q = 0; q < kDma; ++q) buf16_to_lds(srd, off + q * 16 * ld, 0, mb + q * 4096);
   }
   MOK_DEV static bf16x8_t frag(const uint8_t* t, int r0, int h, int kk) {
     const int l = lane_id(), g = l >> 4, L = l & 15;
@@ -132,7 +151,7 @@ struct CopyT {
     const int k = 32 * h + 16 * kk + 8 * (g >> 1) + (L >> 2);
     typedef __attribute__((address_space(3))) v4i16_t* lds_v4_ptr;
     const auto at = [&](int kk_) {
-      return (lds_v4_ptr)(t + kk_ * (2 * R) + (((n >> 3) ^ ((kk_ & 3) << 2)) << 4) + ((2 * n) & 15));
+      return (lds_v4_ptr)(t + kk_ * 256 + (((n >> 3) ^ ((kk_ & 3) << 2)) << 4) + ((2 * n) & 15));
     };
     const v4i16_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(k));
     const v4i16_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(k + 4));
@@ -197,6 +216,158 @@ MOK_DEV void stage128(uint8_t* lds, const Acc<2, 2>& acc) {
       for (int q = 0; q < 16; ++q)
         *reinterpret_cast<float*>(lds + G128::row(i, q) * kPitch128 + G128::col(n) * 4) = acc.c[i][n][q];
   barrier_lds_only();
+}
+
+// ------------------------------------------------------------------ 256 x 256 tile
+// Eight wavefronts in two groups of four, one of each group on every SIMD. Group
+// g owns tile rows 128 g .. +127, its wavefront c columns 64 c .. +63 (4 x 2
+// fragments, 128 accumulators a lane; the products are formed transposed, so that a
+// lane holds four adjacent columns of a row: element 4 q + e of fragment (i, n) is
+// row 32 i + l % 32, column 32 n + 8 q + 4 (l / 32) + e). The groups run half a step apart: in each
+// interval between two workgroup barriers one group reads fragments from LDS and
+// issues copies while the other multiplies, so a copy that waits for the address
+// unit or for the L1 never holds up a matrix instruction. (One wavefront per
+// SIMD that does both in turn keeps the matrix cores half busy: the copies of
+// a tile come in at 17-19 bytes per clock and CU, where the same copies alone
+// reach 43-45.)
+//
+// A slot is 64 bf16 of K; a half operand (128 rows or columns of it) takes 16 KiB.
+// LDS holds three slots of A and two of B. Group 0 copies B, group 1 copies A:
+//
+//   interval  group 0                                group 1
+//   4s        read steps 0, 1 of s; copy B of s+1    multiply steps 2, 3 of s-1
+//   4s+1      multiply                               read steps 0, 1 of s; copy half of A of s+2
+//   4s+2      read steps 2, 3                        multiply
+//   4s+3      multiply; wait for B of s+1            read steps 2, 3; copy half of A of s+2;
+//                                                    wait for A of s+1
+//
+// with a workgroup barrier at the end of each. Both waits lie before the barrier that
+// opens slot s+1, B has three intervals to arrive and A more than a slot (with two
+// slots of each and a quarter of the copies in every interval, the last quarter had
+// one interval: 1.59 us per slot of a 4096 x 4096 product against 1.34 now). Group 1
+// reads slot s last in interval 4s+3, with its reads complete before the barrier; B of
+// s+2 is written over it from 4s+4 on, A of s+3 from 4s+5 on.
+constexpr int kPpThreads = 512;
+constexpr int kPpHalf = 16384, kPpA = 2 * kPpHalf, kPpB = 2 * kPpHalf;
+constexpr int kPpLds = 3 * kPpA + 2 * kPpB;      // 160 KiB, all of it
+MOK_DEV int pp_group() { return wave_id() >> 2; }
+MOK_DEV int pp_col() { return wave_id() & 3; }
+
+template <class LA, class LB>
+MOK_DEV void pp_loop(uint8_t* lds, const LA& la0, const LA& la1, const LB& lb0, const LB& lb1, int ns,
+                     Acc<4, 2>& acc) {
+  static_assert(LA::kDma == 4 && LB::kDma == 4, "four copies per half and wavefront");
+  const uint32_t base = lds_addr(lds);
+  const int grp = pp_group(), c = pp_col();
+  acc.zero();
+  if (ns <= 0) return;
+  if (grp) {
+    la0.dma(0, base);
+    la1.dma(0, base + kPpHalf);
+    if (ns > 1) {
+      la0.dma(1, base + kPpA);
+      la1.dma(1, base + kPpA + kPpHalf);
+      wait_vm_lds<8>();
+    } else {
+      wait_vm_lds<0>();
+    }
+  } else {
+    lb0.dma(0, base + 3 * kPpA);
+    lb1.dma(0, base + 3 * kPpA + kPpHalf);
+    wait_vm_lds<0>();
+  }
+  barrier_lds();
+  if (grp) barrier_lds();
+  bf16x8_t a[2][4], b[2][2];
+  const auto read = [&](const uint8_t* ta, const uint8_t* tb, int h) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) b[kk][n] = LB::frag(tb, 64 * (c & 1) + 32 * n, h, kk);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[kk][i] = LA::frag(ta, 32 * i, h, kk);
+    }
+  };
+  const auto multiply = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          acc.c[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[kk][n], a[kk][i], acc.c[i][n], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  uint32_t s0 = 0, s2 = 2 * kPpA;                // A's slot of s, and of s + 2
+  for (int s = 0; s < ns; ++s) {
+    const uint8_t* ta = lds + s0 + grp * kPpHalf;
+    const uint8_t* tb = lds + 3 * kPpA + (s & 1) * kPpB + (c >> 1) * kPpHalf;
+    const uint32_t nb = base + 3 * kPpA + ((s + 1) & 1) * kPpB, na = base + s2;
+    read(ta, tb, 0);
+    if (grp) {
+      if (s + 2 < ns) la0.dma(s + 2, na);
+    } else if (s + 1 < ns) {
+      lb0.dma(s + 1, nb);
+      lb1.dma(s + 1, nb + kPpHalf);
+    }
+    barrier_lds_only();
+    multiply();
+    barrier_lds();
+    read(ta, tb, 1);
+    if (grp) {
+      if (s + 2 < ns) {
+        la1.dma(s + 2, na + kPpHalf);
+        wait_vm_lds<8>();
+      } else {
+        wait_vm_lds<0>();
+      }
+      barrier_lds();
+    } else {
+      barrier_lds_only();
+    }
+    multiply();
+    if (!grp) wait_vm_lds<0>();
+    barrier_lds();
+    s0 = s0 == 2 * kPpA ? 0 : s0 + kPpA;
+    s2 = s2 == 2 * kPpA ? 0 : s2 + kPpA;
+  }
+  if (!grp) barrier_lds();
+}
+
+// Row of the tile of this lane's fragments i, and its first column of (n, q)
+MOK_DEV int pp_row(int i) { return 128 * pp_group() + 32 * i + (lane_id() & 31); }
+MOK_DEV int pp_col0(int n, int q) { return 64 * pp_col() + 32 * n + 8 * q + 4 * (lane_id() >> 5); }
+
+// bf16 staging of 256 rows x W columns: 16-byte chunk c of row r at c ^ (r & 15) (the 32
+// rows of a store instruction spread over all banks), 8 bytes a lane in, 16 out
+template <int W>
+MOK_DEV int pp_at16(int r, int c) { return r * 2 * W + (((c >> 3) ^ (r & 15)) << 4) + ((c & 7) << 1); }
+MOK_DEV void pp_put4(uint8_t* p, float x, float y, float z, float w) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
+}
+// rows [0, nrows) of the staging, chunk by chunk: put(row, column, value) with eight columns
+template <int W, class Put>
+MOK_DEV void pp_rows16(const uint8_t* lds, int nrows, Put&& put) {
+  constexpr int CH = W / 8;
+#pragma unroll 4
+  for (int idx = threadIdx.x; idx < 256 * CH; idx += kPpThreads) {
+    const int r = idx / CH, c = (idx % CH) * 8;
+    if (r < nrows) put(r, c, *reinterpret_cast<const uint4*>(lds + pp_at16<W>(r, c)));
+  }
+}
+// fp32 staging of fragment columns n: 256 rows x 128 columns, column 32 k + x of it being
+// tile column 64 k + 32 n + x
+constexpr int kPpPitch = 128 * 4 + 16;
+MOK_DEV void pp_stage32(uint8_t* lds, const Acc<4, 2>& acc, int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4*>(lds + pp_row(i) * kPpPitch + (32 * pp_col() + 8 * q + 4 * (lane_id() >> 5)) * 4) =
+          make_float4(acc.c[i][n][4 * q], acc.c[i][n][4 * q + 1], acc.c[i][n][4 * q + 2], acc.c[i][n][4 * q + 3]);
 }
 
 // W consecutive fp32 values (W a multiple of 4) at p

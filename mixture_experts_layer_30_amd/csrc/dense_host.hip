@@ -13,6 +13,7 @@ using namespace mok;
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxK = (int64_t)1 << 20, kMaxTiles = (int64_t)1 << 28;
+constexpr int64_t kMaxPitch = (int64_t)1 << 22;  // row pitch of x, y, dy, dx in elements (copies: 32-bit offsets)
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -38,7 +39,7 @@ mok_status resolve(const mok_ffn_problem* p, Ffn* r) {
   r->ldx = p->ld_x ? p->ld_x : p->H;
   r->ldy = p->ld_y ? p->ld_y : p->H;
   if (r->ldx < p->H || r->ldy < p->H || r->ldx % 8 || r->ldy % 8) return MOK_ERR_INVALID_ARG;
-  if (r->ldx > ((int64_t)1 << 40) || r->ldy > ((int64_t)1 << 40)) return MOK_ERR_UNSUPPORTED;
+  if (r->ldx > kMaxPitch || r->ldy > kMaxPitch) return MOK_ERR_UNSUPPORTED;
   if (!tiles_fit(p->T, std::max(p->H, 2 * p->I)) || !tiles_fit(p->H, 2 * p->I)) return MOK_ERR_UNSUPPORTED;
   return MOK_OK;
 }

@@ -17,7 +17,6 @@ using namespace mok;
 
 namespace {
 
-using G256 = Geo<256, 256, 2, 2>;
 constexpr int kNoSeg = 0x7fffffc0;               // one segment of K (CopyT)
 
 // rows, columns and contracted length of a product, in tiles' terms
@@ -36,6 +35,26 @@ inline Shape shape_of(const mok_ffn_args& a, mok_ffn_op op) {
 }
 
 // ------------------------------------------------------------------ epilogues
+// da, db and h of eight columns (c < I) from dh and the saved a, b
+template <int ACT>
+MOK_DEV void gate_backward8(const mok_ffn_args& a, int r, int c, const float dh[8], uint4 araw, uint4 braw) {
+  float av[8], bv[8], da[8], db[8], h[8];
+  unpack_bf16x8(araw, av);
+  unpack_bf16x8(braw, bv);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    float act, dact;
+    gate_act_grad<ACT>(av[u], act, dact);
+    h[u] = act * bv[u];
+    da[u] = dh[u] * bv[u] * dact;
+    db[u] = dh[u] * act;
+  }
+  bf16_t* d = a.dab + (int64_t)r * 2 * a.Ip + c;
+  store_nt(d, pack_bf16x8(da));
+  store_nt(d + a.Ip, pack_bf16x8(db));
+  store_nt(a.h + (int64_t)r * a.I + c, pack_bf16x8(h));
+}
+
 // Eight columns c .. c+7 of output row r from fp32 sums (gate/up: v = a, w = b).
 template <int OP, int ACT>
 MOK_DEV void finish8(const mok_ffn_args& a, int r, int c, int half, float v[8], const float w[8]) {
@@ -59,20 +78,7 @@ MOK_DEV void finish8(const mok_ffn_args& a, int r, int c, int half, float v[8], 
       return;
     }
     const bf16_t* p = a.ab + (int64_t)r * 2 * a.I + c;
-    float av[8], bv[8], da[8], db[8], h[8];
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(p), av);
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(p + a.I), bv);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      float act, dact;
-      gate_act_grad<ACT>(av[u], act, dact);
-      h[u] = act * bv[u];
-      da[u] = v[u] * bv[u] * dact;
-      db[u] = v[u] * act;
-    }
-    store_nt(d, pack_bf16x8(da));
-    store_nt(d + a.Ip, pack_bf16x8(db));
-    store_nt(a.h + (int64_t)r * a.I + c, pack_bf16x8(h));
+    gate_backward8<ACT>(a, r, c, v, *reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + a.I));
   } else if constexpr (OP == FFN_DWD) {
     if (c >= a.I) return;
     store_nt(a.dwd + (int64_t)r * a.I + c, pack_bf16x8(v));
@@ -101,10 +107,10 @@ template <int OP>
 MOK_DEV int acc_col(int c) { return OP == FFN_GATEUP ? (c >> 5) * 64 + (c & 31) : c; }
 
 // rows [0, nrows) of fp32 staging at pitch P -> finish8; row0/col0 of the tile
-template <int OP, int ACT, int TILE>
+template <int OP, int ACT>
 MOK_DEV void finish_rows(const mok_ffn_args& a, const uint8_t* st, int pitch, int nrows, int row0, int col0,
                          int half) {
-  constexpr int CH = out_cols<OP, TILE>() / 8;
+  constexpr int CH = out_cols<OP, 128>() / 8;
   for (int idx = threadIdx.x; idx < nrows * CH; idx += kThreads) {
     const int r = idx / CH, c = (idx % CH) * 8;
     const uint8_t* p = st + r * pitch + acc_col<OP>(c) * 4;
@@ -116,35 +122,42 @@ MOK_DEV void finish_rows(const mok_ffn_args& a, const uint8_t* st, int pitch, in
 }
 
 // ------------------------------------------------------------------ products
-template <int OP, int TILE, class F>
-MOK_DEV void with_operands(const mok_ffn_args& a, int m0, int n0, int half, F&& f) {
-  const auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
-  if constexpr (OP == FFN_GATEUP) {
-    const CopyK<TILE, 128> la(RowsStrided{u8(a.x + (int64_t)m0 * a.ldx), 2 * a.ldx, a.T - m0}, 2 * a.H);
-    const CopyK<TILE, 128> lb(RowsGateUp{u8(a.wg), u8(a.wu), 2 * (int64_t)a.H, n0, a.I}, 2 * a.H);
-    f(la, lb);
-  } else if constexpr (OP == FFN_DOWN) {
-    const CopyK<TILE, 128> la(RowsStrided{u8(a.h + (int64_t)m0 * a.I), 2 * (int64_t)a.I, a.T - m0}, 2 * a.I);
-    const CopyK<TILE, 128> lb(RowsStrided{u8(a.wd + (int64_t)n0 * a.I), 2 * (int64_t)a.I, a.H - n0}, 2 * a.I);
-    f(la, lb);
-  } else if constexpr (OP == FFN_DH) {
-    const CopyK<TILE, 128> la(RowsStrided{u8(a.dy + (int64_t)m0 * a.ldy), 2 * a.ldy, a.T - m0}, 2 * a.H);
-    const CopyT<TILE> lb(u8(a.wd + n0), u8(a.wd + n0), kNoSeg, a.H, 2 * (int64_t)a.I, a.I - n0);
-    f(la, lb);
-  } else if constexpr (OP == FFN_DWD) {
-    const CopyT<TILE> la(u8(a.dy + m0), u8(a.dy + m0), kNoSeg, a.T, 2 * a.ldy, a.H - m0);
-    const CopyT<TILE> lb(u8(a.h + n0), u8(a.h + n0), kNoSeg, a.T, 2 * (int64_t)a.I, a.I - n0);
-    f(la, lb);
+// The copies of 128 rows from m0 of the first operand and 128 columns from n0 (gate/up: 64 of
+// gate and 64 of up) of the second. A half of a 256 x 256 tile that lies past the matrix copies
+// its last rows or columns instead; those products are not stored.
+template <int OP>
+MOK_DEV auto copy_a(const mok_ffn_args& a, int m0, int half) {
+  if constexpr (OP == FFN_DWD) {
+    m0 = min(m0, a.H - 8);
+    return CopyT(a.dy + m0, a.dy + m0, kNoSeg, a.T, 2 * a.ldy, a.H - m0);
   } else if constexpr (OP == FFN_DWGU) {
-    const uint8_t* da = u8(a.dab + (half ? a.Ip : 0) + m0);
-    const CopyT<TILE> la(da, da, kNoSeg, a.T, 4 * (int64_t)a.Ip, a.I - m0);
-    const CopyT<TILE> lb(u8(a.x + n0), u8(a.x + n0), kNoSeg, a.T, 2 * a.ldx, a.H - n0);
-    f(la, lb);
+    m0 = min(m0, a.I - 8);
+    const bf16_t* da = a.dab + (half ? a.Ip : 0) + m0;
+    return CopyT(da, da, kNoSeg, a.T, 4 * (int64_t)a.Ip, a.I - m0);
   } else {
-    const CopyK<TILE, 128> la(RowsStrided{u8(a.dab + (int64_t)m0 * 2 * a.Ip), 4 * (int64_t)a.Ip, a.T - m0},
-                              4 * (int64_t)a.Ip);
-    const CopyT<TILE> lb(u8(a.wg + n0), u8(a.wu + n0), a.Ip, a.I, 2 * (int64_t)a.H, a.H - n0);
-    f(la, lb);
+    const int64_t ld = OP == FFN_GATEUP ? a.ldx : OP == FFN_DOWN ? a.I : OP == FFN_DH ? a.ldy : 2 * a.Ip;
+    const int K = OP == FFN_DOWN ? a.I : OP == FFN_DX ? 2 * a.Ip : a.H;
+    const bf16_t* p = OP == FFN_GATEUP ? a.x : OP == FFN_DOWN ? a.h : OP == FFN_DH ? a.dy : a.dab;
+    m0 = min(m0, a.T - 1);
+    return CopyK<128, false>(Rows1{p + m0 * ld, 2 * ld, a.T - m0}, 2 * K);
+  }
+}
+template <int OP>
+MOK_DEV auto copy_b(const mok_ffn_args& a, int n0) {
+  n0 = min(n0, (OP == FFN_DOWN || OP == FFN_DWGU || OP == FFN_DX ? a.H : a.I) - 8);
+  if constexpr (OP == FFN_GATEUP) {
+    const int64_t o = (int64_t)n0 * a.H;
+    return CopyK<128, true>(Rows2{a.wg + o, a.wu + o, 2 * (int64_t)a.H, a.I - n0}, 2 * a.H);
+  } else if constexpr (OP == FFN_DOWN) {
+    return CopyK<128, false>(Rows1{a.wd + (int64_t)n0 * a.I, 2 * (int64_t)a.I, a.H - n0}, 2 * a.I);
+  } else if constexpr (OP == FFN_DH) {
+    return CopyT(a.wd + n0, a.wd + n0, kNoSeg, a.H, 2 * (int64_t)a.I, a.I - n0);
+  } else if constexpr (OP == FFN_DWD) {
+    return CopyT(a.h + n0, a.h + n0, kNoSeg, a.T, 2 * (int64_t)a.I, a.I - n0);
+  } else if constexpr (OP == FFN_DWGU) {
+    return CopyT(a.x + n0, a.x + n0, kNoSeg, a.T, 2 * a.ldx, a.H - n0);
+  } else {
+    return CopyT(a.wg + n0, a.wu + n0, a.Ip, a.I, 2 * (int64_t)a.H, a.H - n0);
   }
 }
 
@@ -163,7 +176,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn128_kernel(mok_ffn_args a, int
   const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
   const int j1 = SPLIT ? (int)((int64_t)ns * (split + 1) / splits) : ns;
   Acc<2, 2> acc;
-  with_operands<OP, 128>(a, m0, n0, half, [&](const auto& la, const auto& lb) { loop128(lds, la, lb, j0, j1, acc); });
+  loop128(lds, copy_a<OP>(a, m0, half), copy_b<OP>(a, n0), j0, j1, acc);
   stage128(lds, acc);
   const int nrows = min(128, M - m0);
   if constexpr (SPLIT) {
@@ -173,7 +186,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn128_kernel(mok_ffn_args a, int
       reinterpret_cast<float4*>(p)[idx] =
           *reinterpret_cast<const float4*>(lds + (idx >> 5) * kPitch128 + (idx & 31) * 16);
   } else {
-    finish_rows<OP, ACT, 128>(a, lds, kPitch128, nrows, m0, n0, half);
+    finish_rows<OP, ACT>(a, lds, kPitch128, nrows, m0, n0, half);
   }
 }
 
@@ -205,13 +218,125 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(mok_ffn_args a, int 
   finish8<OP, ACT>(a, row * 128 + r, col * out_cols<OP, 128>() + c, half, v, w);
 }
 
-// Products that fill the chip with 256 x 256 tiles run the main loop of gemm_core.h.
+// Epilogue of a 256 x 256 tile (the main loop ends in a barrier: LDS is free).
 template <int OP, int ACT>
-__global__ __launch_bounds__(kThreads, 1) void ffn256_kernel(mok_ffn_args a, int M, int K, int nr, int nc,
-                                                             int batch) {
-  using G = G256;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[tile_lds_bytes<Smem<G, false>>()];
-  Smem<G, false>& sm = *reinterpret_cast<Smem<G, false>*>(lds);
+MOK_DEV void finish256(const mok_ffn_args& a, uint8_t* lds, Acc<4, 2>& acc, int nrows, int m0, int n0, int half) {
+  if constexpr (OP == FFN_GATEUP) {
+    // fragment columns n = 0, 1 are gate and up of the same 32 columns: h in registers, then
+    // [h | a] and b through LDS, 128 columns each
+    const auto put = [&](int plane, auto&& f) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = f(acc.c[i][0][4 * q + e], acc.c[i][1][4 * q + e]);
+          const int c = 32 * pp_col() + 8 * q + 4 * (lane_id() >> 5);
+          pp_put4(lds + plane * 65536 + pp_at16<128>(pp_row(i), c), v[0], v[1], v[2], v[3]);
+        }
+    };
+    put(0, [](float g, float u) { return gate_act<ACT>(g) * u; });
+    if (a.ab) put(1, [](float g, float) { return g; });
+    barrier_lds_only();
+    pp_rows16<128>(lds, nrows, [&](int r, int c, uint4 v) {
+      if (n0 + c < a.I) store_nt(a.h + (int64_t)(m0 + r) * a.I + n0 + c, v);
+    });
+    if (!a.ab) return;
+    pp_rows16<128>(lds + 65536, nrows, [&](int r, int c, uint4 v) {
+      if (n0 + c < a.I) store_nt(a.ab + (int64_t)(m0 + r) * 2 * a.I + n0 + c, v);
+    });
+    barrier_lds_only();
+    put(0, [](float, float u) { return u; });
+    barrier_lds_only();
+    pp_rows16<128>(lds, nrows, [&](int r, int c, uint4 v) {
+      if (n0 + c < a.I) store_nt(a.ab + (int64_t)(m0 + r) * 2 * a.I + a.I + n0 + c, v);
+    });
+  } else if constexpr (OP == FFN_DH) {
+    // dh stays fp32 until the gate's backward has used it: two passes of 128 columns, each
+    // with its loads of a, b issued before the staging and its stores after
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      uint4 av[8], bv[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int idx = (int)threadIdx.x + u * kPpThreads, r = idx >> 4, x = (idx & 15) * 8;
+        const int c = n0 + 64 * (x >> 5) + 32 * n + (x & 31);
+        if (r < nrows && c < a.I) {
+          const bf16_t* p = a.ab + (int64_t)(m0 + r) * 2 * a.I + c;
+          av[u] = *reinterpret_cast<const uint4*>(p);
+          bv[u] = *reinterpret_cast<const uint4*>(p + a.I);
+        }
+      }
+      if (n) barrier_lds_only();
+      pp_stage32(lds, acc, n);
+      barrier_lds_only();
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int idx = (int)threadIdx.x + u * kPpThreads, r = idx >> 4, x = (idx & 15) * 8;
+        const int c = n0 + 64 * (x >> 5) + 32 * n + (x & 31);
+        if (r >= nrows || c >= a.Ip) continue;
+        float v[8];
+        load_f32<8>(lds + r * kPpPitch + x * 4, v);
+        if (c < a.I) {
+          gate_backward8<ACT>(a, m0 + r, c, v, av[u], bv[u]);
+        } else {
+          bf16_t* d = a.dab + (int64_t)(m0 + r) * 2 * a.Ip + c;
+          store_nt(d, make_uint4(0, 0, 0, 0));
+          store_nt(d + a.Ip, make_uint4(0, 0, 0, 0));
+        }
+      }
+    }
+  } else {
+    if constexpr (OP == FFN_DOWN)
+      if (a.res) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          __builtin_amdgcn_sched_barrier(0);     // (one row's loads at a time: all of them spill)
+          if (pp_row(i) >= nrows) continue;
+          const bf16_t* p = a.res + (int64_t)(m0 + pp_row(i)) * a.ldy + n0;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (n0 + pp_col0(n, q) >= a.H) continue;
+              const uint2 s = *reinterpret_cast<const uint2*>(p + pp_col0(n, q));
+              acc.c[i][n][4 * q] += __uint_as_float(s.x << 16);
+              acc.c[i][n][4 * q + 1] += __uint_as_float(s.x & 0xFFFF0000u);
+              acc.c[i][n][4 * q + 2] += __uint_as_float(s.y << 16);
+              acc.c[i][n][4 * q + 3] += __uint_as_float(s.y & 0xFFFF0000u);
+            }
+        }
+        // a residual that is y itself: every row is read before its stores, which other
+        // wavefronts make
+        __syncthreads();
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          pp_put4(lds + pp_at16<256>(pp_row(i), pp_col0(n, q)), acc.c[i][n][4 * q], acc.c[i][n][4 * q + 1],
+                  acc.c[i][n][4 * q + 2], acc.c[i][n][4 * q + 3]);
+    barrier_lds_only();
+    bf16_t* d;
+    int64_t ld;
+    int cols;
+    if constexpr (OP == FFN_DOWN) { d = a.y; ld = a.ldy; cols = a.H; }
+    else if constexpr (OP == FFN_DX) { d = a.dx; ld = a.ldx; cols = a.H; }
+    else if constexpr (OP == FFN_DWD) { d = a.dwd; ld = a.I; cols = a.I; }
+    else { d = half ? a.dwu : a.dwg; ld = a.H; cols = a.H; }
+    pp_rows16<256>(lds, nrows, [&](int r, int c, uint4 v) {
+      if (n0 + c < cols) store_nt(d + (m0 + r) * ld + n0 + c, v);
+    });
+  }
+}
+
+template <int OP, int ACT>
+__global__ __launch_bounds__(kPpThreads, 1) void ffn256_kernel(mok_ffn_args a, int M, int K, int nr, int nc,
+                                                               int batch) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kPpLds];
   const int t = dense_index((int64_t)nr * nc * batch);
   if (t < 0) return;
   const int half = t / (nr * nc);
@@ -219,18 +344,10 @@ __global__ __launch_bounds__(kThreads, 1) void ffn256_kernel(mok_ffn_args a, int
   dense_tile(t - half * nr * nc, nr, nc, 4, row, col);
   const int m0 = row * 256, n0 = col * out_cols<OP, 256>();
   const int nrows = min(256, M - m0);
-  Acc<G::FM, G::FN> acc;
-  with_operands<OP, 256>(a, m0, n0, half, [&](const auto& la, const auto& lb) {
-    NoScales ns;
-    mainloop_rows<false, G, false>(sm, la, lb, ns, ns, 2 * ((K + 63) / 64), nrows, acc);
-  });
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    barrier_lds_only();
-    HalfF32<G>::put(lds, acc, hf);
-    barrier_lds_only();
-    finish_rows<OP, ACT, 256>(a, lds, HalfF32<G>::PITCH, min(128, nrows - 128 * hf), m0 + 128 * hf, n0, half);
-  }
+  Acc<4, 2> acc;
+  pp_loop(lds, copy_a<OP>(a, m0, half), copy_a<OP>(a, m0 + 128, half), copy_b<OP>(a, n0),
+          copy_b<OP>(a, n0 + out_cols<OP, 128>()), (K + 63) / 64, acc);
+  finish256<OP, ACT>(a, lds, acc, nrows, m0, n0, half);
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -360,7 +477,7 @@ hipError_t launch(const mok_ffn_args& a, const Plan& p, hipStream_t st) {
   if (tiles == 0) return hipSuccess;
   const dim3 grid(dense_grid(tiles * p.splits)), block(kThreads);
   if (p.tile == 256)
-    hipLaunchKernelGGL((ffn256_kernel<OP, ACT>), grid, block, 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch);
+    hipLaunchKernelGGL((ffn256_kernel<OP, ACT>), grid, dim3(kPpThreads), 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch);
   else if (p.splits == 1)
     hipLaunchKernelGGL((ffn128_kernel<OP, ACT, false>), grid, block, 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch, 1);
   else {

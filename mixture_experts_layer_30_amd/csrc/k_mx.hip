@@ -123,28 +123,34 @@ struct MxTile {
   static constexpr int kLds = 2 * kSlot > kLds128 ? 2 * kSlot : kLds128;
 };
 
-// scale words (four blocks of 32, one word per 128 of K) of the tile's 128 A rows
-// (wavefronts 0 and 1) and 128 B rows (2 and 3); words past K read as zero
+// Scale words (four blocks of 32, one word per 128 of K) of 64 rows: lane l copies those
+// of row l; words past K read as zero.
 template <int WORDS>
 struct CopyScales {
   static constexpr int kDma = WORDS;
-  const uint8_t* p;
-  int nb;                                        // scale bytes per row
-  template <class RA, class RB>
-  MOK_DEV CopyScales(const RA& ra, const RB& rb, int K) : nb(K / 32) {
-    const int w = wave_id(), r = 64 * (w & 1) + lane_id();
-    p = w < 2 ? ra.row(r) : rb.row(r);
+  srd_t srd;
+  int off, nb;                                   // nb: scale bytes per row
+  MOK_DEV CopyScales(const uint8_t* p, int n, int K) : nb(K / 32) {
+    srd = make_srd(p, (int64_t)min(n, 64) * nb);
+    off = lane_id() * nb;
   }
-  MOK_DEV void dma(int j, uint32_t slot) const {
+  // word q of every row at lds + q * pitch
+  MOK_DEV void dma(int j, uint32_t lds, int pitch) const {
 #pragma unroll
     for (int q = 0; q < WORDS; ++q) {
       const int o = (j * WORDS + q) * 4;
-      copy4_to_lds(o < nb ? p + o : kZeroRow, slot + q * 1024 + wave_id() * 256);
+      buf4_to_lds(srd, o < nb ? off + o : kNowhere, 0, lds + q * pitch);
     }
   }
 };
+// of a tile's scale words: the place of second-operand row r. With the gate the rows go in
+// blocks of 128, each 64 gate rows and then the 64 up rows of the same columns.
+template <bool GLU>
+MOK_DEV int scale_at(int r) {
+  return GLU ? (r & ~127) | ((r >> 5) & 1) << 6 | ((r >> 6) & 1) << 5 | (r & 31) : r;
+}
 
-template <bool A8, class LA, class LB, class LS>
+template <bool A8, bool GLU, class LA, class LB, class LS>
 MOK_DEV void mx_loop128(uint8_t* lds, const LA& la, const LB& lb, const LS& ls, int j0, int j1, Acc<2, 2>& acc) {
   using X = MxTile<A8>;
   constexpr int kD = LA::kDma + LB::kDma + LS::kDma;
@@ -154,7 +160,7 @@ MOK_DEV void mx_loop128(uint8_t* lds, const LA& la, const LB& lb, const LS& ls, 
   const auto issue = [&](int j, int s) {
     la.dma(j, base + s * X::kSlot);
     lb.dma(j, base + s * X::kSlot + X::kA);
-    ls.dma(j, base + s * X::kSlot + X::kA + X::kB);
+    ls.dma(j, base + s * X::kSlot + X::kA + X::kB + wave_id() * 256, 1024);
   };
   if (j0 < j1) issue(j0, 0);
   if (j0 + 1 < j1) issue(j0 + 1, 1);
@@ -188,7 +194,7 @@ MOK_DEV void mx_loop128(uint8_t* lds, const LA& la, const LB& lb, const LS& ls, 
         b[i] = i32x8_t{b0[0], b0[1], b0[2], b0[3], 0, 0, 0, 0};
         const int sh = 8 * (2 * (ks & 1) + hl), wd = (ks >> 1) * 256;
         as[i] = (int)((sc[wd + ra] >> sh) & 0xFFu);
-        bs[i] = (int)((sc[wd + 128 + rb] >> sh) & 0xFFu);
+        bs[i] = (int)((sc[wd + 128 + scale_at<GLU>(rb)] >> sh) & 0xFFu);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -249,6 +255,34 @@ MOK_DEV void mx_gate32(const mok_mx_args& a, int r, int c, const float g[32], co
 template <bool GLU>
 constexpr int mx_cols() { return GLU ? 64 : 128; }   // output columns of a tile
 
+// The copies of 128 rows of A from m0, of 128 rows of B from n0 (with the gate 64 gate and 64
+// up rows), and of the scale words of these by four wavefronts: the first two A's, the others B's.
+// (halves past the matrix: as in k_ffn.hip)
+template <bool A8>
+MOK_DEV auto mx_copy_a(const mok_mx_args& a, int m0) {
+  const int64_t ka = A8 ? a.K : a.K / 2;
+  m0 = min(m0, a.M - 1);
+  return CopyK<MxTile<A8>::RBA, false>(Rows1{a.a + m0 * ka, ka, a.M - m0}, ka);
+}
+template <bool A8, bool GLU>
+MOK_DEV auto mx_copy_b(const mok_mx_args& a, int n0) {
+  const int64_t kb = a.K / 2;
+  n0 = min(n0, a.N - 1);
+  if constexpr (GLU) return CopyK<MxTile<A8>::RBB, true>(Rows2{a.b + n0 * kb, a.b2 + n0 * kb, kb, a.N - n0}, kb);
+  else return CopyK<MxTile<A8>::RBB, false>(Rows1{a.b + n0 * kb, kb, a.N - n0}, kb);
+}
+template <bool A8, bool GLU>
+MOK_DEV auto mx_copy_s(const mok_mx_args& a, int m0, int n0) {
+  const int64_t ks = a.K / 32;
+  const int w = copy_wave(), second = w & 1;
+  if (w < 2) {
+    m0 = min(m0 + 64 * second, a.M - 1);
+    return CopyScales<MxTile<A8>::SK / 128>(a.sa + m0 * ks, a.M - m0, a.K);
+  }
+  n0 = min(n0 + (GLU ? 0 : 64 * second), a.N - 1);
+  return CopyScales<MxTile<A8>::SK / 128>((GLU && second ? a.sb2 : a.sb) + n0 * ks, a.N - n0, a.K);
+}
+
 template <bool A8, bool GLU, int ACT, bool SPLIT>
 __global__ __launch_bounds__(kThreads, 2) void mx128_kernel(mok_mx_args a, bool vec, int nr, int nc, int splits) {
   using X = MxTile<A8>;
@@ -262,17 +296,8 @@ __global__ __launch_bounds__(kThreads, 2) void mx128_kernel(mok_mx_args a, bool 
   const int ns = (a.K + X::SK - 1) / X::SK;
   const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
   const int j1 = SPLIT ? (int)((int64_t)ns * (split + 1) / splits) : ns;
-  const int64_t ka = A8 ? a.K : a.K / 2, kb = a.K / 2, ks = a.K / 32;
-  const RowsStrided ra{a.a + m0 * ka, ka, nrows}, rsa{a.sa + m0 * ks, ks, nrows};
   Acc<2, 2> acc;
-  const auto run = [&](const auto& rb, const auto& rsb) {
-    const CopyK<128, X::RBA> la(ra, ka);
-    const CopyK<128, X::RBB> lb(rb, kb);
-    const CopyScales<X::SK / 128> ls(rsa, rsb, a.K);
-    mx_loop128<A8>(lds, la, lb, ls, j0, j1, acc);
-  };
-  if constexpr (GLU) run(RowsGateUp(a.b, a.b2, kb, n0, a.N), RowsGateUp(a.sb, a.sb2, ks, n0, a.N));
-  else run(RowsStrided{a.b + n0 * kb, kb, a.N - n0}, RowsStrided{a.sb + n0 * ks, ks, a.N - n0});
+  mx_loop128<A8, GLU>(lds, mx_copy_a<A8>(a, m0), mx_copy_b<A8, GLU>(a, n0), mx_copy_s<A8, GLU>(a, m0, n0), j0, j1, acc);
   stage128(lds, acc);
   if constexpr (SPLIT) {
     float* p = a.part + ((int64_t)split * tiles + t) * 16384;

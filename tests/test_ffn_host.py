@@ -30,7 +30,7 @@ def test_ffn_sizes():
     (dict(activation=-1), INV), (dict(dtype=mok.MOK_MXFP8), UNS), (dict(H=12), UNS), (dict(I=20), UNS),
     (dict(dtype=mok.MOK_MXFP4, H=192), UNS), (dict(dtype=mok.MOK_MXFP4, I=64), UNS), (dict(ld_x=248), INV),
     (dict(ld_y=260), INV), (dict(T=(1 << 30) + 1), UNS), (dict(H=(1 << 20) + 8), UNS),
-    (dict(T=1 << 30, H=1 << 20), UNS),
+    (dict(T=1 << 30, H=1 << 20), UNS), (dict(ld_x=(1 << 22) + 8), UNS), (dict(ld_y=(1 << 22) + 8), UNS),
 ])
 def test_ffn_problems_refused(kw, status):
     p = dict(T=64, H=256, I=256)
