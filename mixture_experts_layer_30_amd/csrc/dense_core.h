@@ -33,10 +33,9 @@ MOK_DEV int lds_at64(int row, int chunk) {
 // copies and the matrix instructions ran one after the other.
 typedef i32x4_t srd_t;
 MOK_DEV int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
-MOK_DEV srd_t make_srd(const void* p, int64_t bytes) {
+MOK_DEV srd_t make_srd(const void* p, int64_t bytes) {         // (0 <= bytes < 2^31)
   const uint64_t u = (uint64_t)p;
-  const int64_t n = bytes < 0 ? 0 : bytes;       // (callers stay below 2^31)
-  return srd_t{uni((int)u), uni((int)(u >> 32) & 0xFFFF), uni((int)n), 0x00020000};
+  return srd_t{uni((int)u), uni((int)(u >> 32) & 0xFFFF), uni((int)bytes), 0x00020000};
 }
 // Bounds: a lane's offset alone has to be past the descriptor's bytes where nothing
 // may be read (the scalar offset, only ever a step along K inside a row, does not
@@ -140,7 +139,7 @@ struct CopyT {
     const bool second = j * 64 >= kseg;
     const int k0 = second ? j * 64 - kseg : j * 64, kr = min(kvalid - k0, 64);
     const srd_t srd = make_srd((second ? src1 : src0) + (int64_t)k0 * ld,
-                               kr > 0 ? (int64_t)(kr - 1) * ld + 2 * min(ncols, 128) : 0);
+                               max((int64_t)(kr - 1) * ld + 2 * min(ncols, 128), (int64_t)0));
     const uint32_t mb = slot + copy_wave() * 1024;
 #pragma unroll
     for (int q = 0; q < kDma; ++q) buf16_to_lds(srd, off + q * 16 * ld, 0, mb + q * 4096);
@@ -232,48 +231,61 @@ MOK_DEV void stage128(uint8_t* lds, const Acc<2, 2>& acc) {
 // reach 43-45.)
 //
 // A slot is 64 bf16 of K; a half operand (128 rows or columns of it) takes 16 KiB.
-// LDS holds three slots of A and two of B. Group 0 copies B, group 1 copies A:
+// Group g copies half g of both operands: of B into two buffers, of A, which only
+// group g reads, into three.
 //
-//   interval  group 0                                group 1
-//   4s        read steps 0, 1 of s; copy B of s+1    multiply steps 2, 3 of s-1
-//   4s+1      multiply                               read steps 0, 1 of s; copy half of A of s+2
-//   4s+2      read steps 2, 3                        multiply
-//   4s+3      multiply; wait for B of s+1            read steps 2, 3; copy half of A of s+2;
-//                                                    wait for A of s+1
+//   interval  group 0                                   group 1
+//   4s        read steps 0, 1 of s; copy B of s+1       multiply steps 2, 3 of s-1
+//   4s+1      multiply                                  read steps 0, 1 of s; copy B of s+1
+//   4s+2      read steps 2, 3; copy A of s+2            multiply
+//   4s+3      multiply; wait for its B of s+1           read steps 2, 3; copy A of s+2;
+//                                                       wait for its B of s+1
 //
-// with a workgroup barrier at the end of each. Both waits lie before the barrier that
-// opens slot s+1, B has three intervals to arrive and A more than a slot (with two
-// slots of each and a quarter of the copies in every interval, the last quarter had
-// one interval: 1.59 us per slot of a 4096 x 4096 product against 1.34 now). Group 1
-// reads slot s last in interval 4s+3, with its reads complete before the barrier; B of
-// s+2 is written over it from 4s+4 on, A of s+3 from 4s+5 on.
+// with a workgroup barrier at the end of each. Every interval has a quarter of the
+// copies (at the matrix cores' full rate 32 bytes per clock and CU). Both waits lie
+// before the barrier that opens slot s+1; B has two or three intervals to arrive, A more
+// than a slot, and no time goes into the waits. The last reads of slot s are complete
+// before the barrier of 4s+3, B of s+2 is written over them from 4s+4 on, A of s+3 from
+// 4s+6 on. (Copies between the matrix instructions of the multiplying group were 13 to
+// 40% slower, all of B in interval 4s TODO, two slots of each operand 5%.)
 constexpr int kPpThreads = 512;
-constexpr int kPpHalf = 16384, kPpA = 2 * kPpHalf, kPpB = 2 * kPpHalf;
-constexpr int kPpLds = 3 * kPpA + 2 * kPpB;      // 160 KiB, all of it
+constexpr int kPpHalf = 16384;
+constexpr int kPpLds = 10 * kPpHalf;             // 160 KiB: 3 + 3 half slots of A, 2 + 2 of B
 MOK_DEV int pp_group() { return wave_id() >> 2; }
 MOK_DEV int pp_col() { return wave_id() & 3; }
 
+// The matrix instructions touch no memory, and the compiler would move them past the
+// barriers into the next interval: these fix their operands and results in place.
+template <class T>
+MOK_DEV void pin(T& v) { asm volatile("" : "+v"(v)); }
+MOK_DEV void pin_acc(Acc<4, 2>& acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) pin(acc.c[i][n]);
+}
+
+// all copies but the last N have arrived (with `more`; without, all have)
+template <int N>
+MOK_DEV void pp_wait(bool more) {
+  if (more) wait_vm_lds<N>();
+  else wait_vm_lds<0>();
+}
+
+// la, lb: this wavefront's group's halves
 template <class LA, class LB>
-MOK_DEV void pp_loop(uint8_t* lds, const LA& la0, const LA& la1, const LB& lb0, const LB& lb1, int ns,
-                     Acc<4, 2>& acc) {
+MOK_DEV void pp_loop(uint8_t* lds, const LA& la, const LB& lb, int ns, Acc<4, 2>& acc) {
   static_assert(LA::kDma == 4 && LB::kDma == 4, "four copies per half and wavefront");
-  const uint32_t base = lds_addr(lds);
   const int grp = pp_group(), c = pp_col();
+  const uint32_t base = lds_addr(lds), oa = grp * 3 * kPpHalf, ob = 6 * kPpHalf;
   acc.zero();
   if (ns <= 0) return;
-  if (grp) {
-    la0.dma(0, base);
-    la1.dma(0, base + kPpHalf);
-    if (ns > 1) {
-      la0.dma(1, base + kPpA);
-      la1.dma(1, base + kPpA + kPpHalf);
-      wait_vm_lds<8>();
-    } else {
-      wait_vm_lds<0>();
-    }
+  lb.dma(0, base + ob + grp * kPpHalf);
+  la.dma(0, base + oa);
+  if (ns > 1) {
+    la.dma(1, base + oa + kPpHalf);
+    wait_vm_lds<4>();
   } else {
-    lb0.dma(0, base + 3 * kPpA);
-    lb1.dma(0, base + 3 * kPpA + kPpHalf);
     wait_vm_lds<0>();
   }
   barrier_lds();
@@ -291,6 +303,7 @@ MOK_DEV void pp_loop(uint8_t* lds, const LA& la0, const LA& la1, const LB& lb0, 
   const auto multiply = [&]() {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
+    pin(b[0][0]);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -298,41 +311,29 @@ MOK_DEV void pp_loop(uint8_t* lds, const LA& la0, const LA& la1, const LB& lb0, 
 #pragma unroll
         for (int n = 0; n < 2; ++n)
           acc.c[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[kk][n], a[kk][i], acc.c[i][n], 0, 0, 0);
+    pin_acc(acc);
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
   };
-  uint32_t s0 = 0, s2 = 2 * kPpA;                // A's slot of s, and of s + 2
+  uint32_t s0 = 0, s2 = 2 * kPpHalf;             // A's buffer of s, and of s + 2
   for (int s = 0; s < ns; ++s) {
-    const uint8_t* ta = lds + s0 + grp * kPpHalf;
-    const uint8_t* tb = lds + 3 * kPpA + (s & 1) * kPpB + (c >> 1) * kPpHalf;
-    const uint32_t nb = base + 3 * kPpA + ((s + 1) & 1) * kPpB, na = base + s2;
+    const uint8_t* ta = lds + oa + s0;
+    const uint8_t* tb = lds + ob + ((s & 1) * 2 + (c >> 1)) * kPpHalf;
+    const bool more = s + 2 < ns;
     read(ta, tb, 0);
-    if (grp) {
-      if (s + 2 < ns) la0.dma(s + 2, na);
-    } else if (s + 1 < ns) {
-      lb0.dma(s + 1, nb);
-      lb1.dma(s + 1, nb + kPpHalf);
-    }
+    if (s + 1 < ns) lb.dma(s + 1, base + ob + (((s + 1) & 1) * 2 + grp) * kPpHalf);
     barrier_lds_only();
     multiply();
     barrier_lds();
     read(ta, tb, 1);
-    if (grp) {
-      if (s + 2 < ns) {
-        la1.dma(s + 2, na + kPpHalf);
-        wait_vm_lds<8>();
-      } else {
-        wait_vm_lds<0>();
-      }
-      barrier_lds();
-    } else {
-      barrier_lds_only();
-    }
+    if (more) la.dma(s + 2, base + oa + s2);
+    if (grp) pp_wait<4>(more);
+    barrier_lds_only();
     multiply();
-    if (!grp) wait_vm_lds<0>();
+    if (!grp) pp_wait<4>(more);
     barrier_lds();
-    s0 = s0 == 2 * kPpA ? 0 : s0 + kPpA;
-    s2 = s2 == 2 * kPpA ? 0 : s2 + kPpA;
+    s0 = s0 == 2 * kPpHalf ? 0 : s0 + kPpHalf;
+    s2 = s2 == 2 * kPpHalf ? 0 : s2 + kPpHalf;
   }
   if (!grp) barrier_lds();
 }
@@ -357,6 +358,21 @@ MOK_DEV void pp_rows16(const uint8_t* lds, int nrows, Put&& put) {
     const int r = idx / CH, c = (idx % CH) * 8;
     if (r < nrows) put(r, c, *reinterpret_cast<const uint4*>(lds + pp_at16<W>(r, c)));
   }
+}
+// c += the residual's row r at this lane's columns of a fragment from column c0 on (8 q + 0 .. 3;
+// N a multiple of 8). Columns past N take others instead, and are not stored.
+MOK_DEV void pp_add_residual(f32x16_t& c, const bf16_t* res, int64_t ld, int r, int c0, int N) {
+  uint2 v[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint2*>(res + r * ld + min(c0 + 8 * q, N - 4));
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    c[4 * q] += __uint_as_float(v[q].x << 16);
+    c[4 * q + 1] += __uint_as_float(v[q].x & 0xFFFF0000u);
+    c[4 * q + 2] += __uint_as_float(v[q].y << 16);
+    c[4 * q + 3] += __uint_as_float(v[q].y & 0xFFFF0000u);
+  }
+  __builtin_amdgcn_sched_barrier(0);             // (all fragments' loads at once spill)
 }
 // fp32 staging of fragment columns n: 256 rows x 128 columns, column 32 k + x of it being
 // tile column 64 k + 32 n + x

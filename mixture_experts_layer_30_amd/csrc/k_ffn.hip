@@ -218,8 +218,9 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(mok_ffn_args a, int 
   finish8<OP, ACT>(a, row * 128 + r, col * out_cols<OP, 128>() + c, half, v, w);
 }
 
-// Epilogue of a 256 x 256 tile (the main loop ends in a barrier: LDS is free).
-template <int OP, int ACT>
+// Epilogue of a 256 x 256 tile (the main loop ends in a barrier: LDS is free). VAR: the
+// gate's kind, or of the down product 1 = with a residual.
+template <int OP, int VAR>
 MOK_DEV void finish256(const mok_ffn_args& a, uint8_t* lds, Acc<4, 2>& acc, int nrows, int m0, int n0, int half) {
   if constexpr (OP == FFN_GATEUP) {
     // fragment columns n = 0, 1 are gate and up of the same 32 columns: h in registers, then
@@ -236,7 +237,7 @@ MOK_DEV void finish256(const mok_ffn_args& a, uint8_t* lds, Acc<4, 2>& acc, int 
           pp_put4(lds + plane * 65536 + pp_at16<128>(pp_row(i), c), v[0], v[1], v[2], v[3]);
         }
     };
-    put(0, [](float g, float u) { return gate_act<ACT>(g) * u; });
+    put(0, [](float g, float u) { return gate_act<VAR>(g) * u; });
     if (a.ab) put(1, [](float g, float) { return g; });
     barrier_lds_only();
     pp_rows16<128>(lds, nrows, [&](int r, int c, uint4 v) {
@@ -279,7 +280,7 @@ MOK_DEV void finish256(const mok_ffn_args& a, uint8_t* lds, Acc<4, 2>& acc, int 
         float v[8];
         load_f32<8>(lds + r * kPpPitch + x * 4, v);
         if (c < a.I) {
-          gate_backward8<ACT>(a, m0 + r, c, v, av[u], bv[u]);
+          gate_backward8<VAR>(a, m0 + r, c, v, av[u], bv[u]);
         } else {
           bf16_t* d = a.dab + (int64_t)(m0 + r) * 2 * a.Ip + c;
           store_nt(d, make_uint4(0, 0, 0, 0));
@@ -288,29 +289,16 @@ MOK_DEV void finish256(const mok_ffn_args& a, uint8_t* lds, Acc<4, 2>& acc, int 
       }
     }
   } else {
-    if constexpr (OP == FFN_DOWN)
-      if (a.res) {
+    if constexpr (OP == FFN_DOWN && VAR == 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          __builtin_amdgcn_sched_barrier(0);     // (one row's loads at a time: all of them spill)
-          if (pp_row(i) >= nrows) continue;
-          const bf16_t* p = a.res + (int64_t)(m0 + pp_row(i)) * a.ldy + n0;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (n0 + pp_col0(n, q) >= a.H) continue;
-              const uint2 s = *reinterpret_cast<const uint2*>(p + pp_col0(n, q));
-              acc.c[i][n][4 * q] += __uint_as_float(s.x << 16);
-              acc.c[i][n][4 * q + 1] += __uint_as_float(s.x & 0xFFFF0000u);
-              acc.c[i][n][4 * q + 2] += __uint_as_float(s.y << 16);
-              acc.c[i][n][4 * q + 3] += __uint_as_float(s.y & 0xFFFF0000u);
-            }
-        }
-        // a residual that is y itself: every row is read before its stores, which other
-        // wavefronts make
-        __syncthreads();
-      }
+        for (int n = 0; n < 2; ++n)
+          pp_add_residual(acc.c[i][n], a.res, a.ldy, m0 + min(pp_row(i), nrows - 1), n0 + pp_col0(n, 0), a.H);
+      // a residual that is y itself: every row is read before its stores, which other
+      // wavefronts make
+      __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -333,7 +321,7 @@ MOK_DEV void finish256(const mok_ffn_args& a, uint8_t* lds, Acc<4, 2>& acc, int 
   }
 }
 
-template <int OP, int ACT>
+template <int OP, int VAR>
 __global__ __launch_bounds__(kPpThreads, 1) void ffn256_kernel(mok_ffn_args a, int M, int K, int nr, int nc,
                                                                int batch) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kPpLds];
@@ -343,11 +331,10 @@ __global__ __launch_bounds__(kPpThreads, 1) void ffn256_kernel(mok_ffn_args a, i
   int row, col;
   dense_tile(t - half * nr * nc, nr, nc, 4, row, col);
   const int m0 = row * 256, n0 = col * out_cols<OP, 256>();
-  const int nrows = min(256, M - m0);
+  const int nrows = min(256, M - m0), g = pp_group();
   Acc<4, 2> acc;
-  pp_loop(lds, copy_a<OP>(a, m0, half), copy_a<OP>(a, m0 + 128, half), copy_b<OP>(a, n0),
-          copy_b<OP>(a, n0 + out_cols<OP, 128>()), (K + 63) / 64, acc);
-  finish256<OP, ACT>(a, lds, acc, nrows, m0, n0, half);
+  pp_loop(lds, copy_a<OP>(a, m0 + 128 * g, half), copy_b<OP>(a, n0 + out_cols<OP, 128>() * g), (K + 63) / 64, acc);
+  finish256<OP, VAR>(a, lds, acc, nrows, m0, n0, half);
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -476,7 +463,10 @@ hipError_t launch(const mok_ffn_args& a, const Plan& p, hipStream_t st) {
   if (tiles * p.splits > (1 << 30)) return hipErrorInvalidValue;
   if (tiles == 0) return hipSuccess;
   const dim3 grid(dense_grid(tiles * p.splits)), block(kThreads);
-  if (p.tile == 256)
+  if (p.tile == 256 && OP == FFN_DOWN && a.res)
+    hipLaunchKernelGGL((ffn256_kernel<OP, OP == FFN_DOWN ? 1 : ACT>), grid, dim3(kPpThreads), 0, st, a, p.s.M, p.s.K,
+                       p.nr, p.nc, p.s.batch);
+  else if (p.tile == 256)
     hipLaunchKernelGGL((ffn256_kernel<OP, ACT>), grid, dim3(kPpThreads), 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch);
   else if (p.splits == 1)
     hipLaunchKernelGGL((ffn128_kernel<OP, ACT, false>), grid, block, 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch, 1);

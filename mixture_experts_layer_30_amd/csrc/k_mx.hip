@@ -283,6 +283,31 @@ MOK_DEV auto mx_copy_s(const mok_mx_args& a, int m0, int n0) {
   return CopyScales<MxTile<A8>::SK / 128>((GLU && second ? a.sb2 : a.sb) + n0 * ks, a.N - n0, a.K);
 }
 
+// scale bytes of 64 rows, 16 a row and copy, bytes past a row's end undefined
+struct CopyScales16 {
+  srd_t srd;
+  int off;
+  MOK_DEV CopyScales16(const uint8_t* p, int n, int K) {
+    srd = make_srd(p, (int64_t)min(n, 64) * (K / 32));
+    off = lane_id() * (K / 32);
+  }
+  MOK_DEV void dma(int m, uint32_t lds) const { buf16_to_lds(srd, off + 16 * m, 0, lds); }
+};
+
+// of a 256 x 256 tile: wavefront c of group 0 the scale bytes of 64 of B's rows, of group 1 of
+// A's (places of scale_at: with the gate 64 gate, 64 up, 64 gate, 64 up rows)
+template <bool GLU>
+MOK_DEV auto mx_copy_s16(const mok_mx_args& a, int m0, int n0) {
+  const int64_t ks = a.K / 32;
+  const int c = pp_col();
+  if (pp_group()) {
+    m0 = min(m0 + 64 * c, a.M - 1);
+    return CopyScales16(a.sa + m0 * ks, a.M - m0, a.K);
+  }
+  n0 = min(n0 + 64 * (GLU ? c >> 1 : c), a.N - 1);
+  return CopyScales16((GLU && (c & 1) ? a.sb2 : a.sb) + n0 * ks, a.N - n0, a.K);
+}
+
 template <bool A8, bool GLU, int ACT, bool SPLIT>
 __global__ __launch_bounds__(kThreads, 2) void mx128_kernel(mok_mx_args a, bool vec, int nr, int nc, int splits) {
   using X = MxTile<A8>;
@@ -350,6 +375,228 @@ __global__ __launch_bounds__(kThreads) void mx_join_kernel(mok_mx_args a, bool v
   }
   if constexpr (GLU) mx_gate32<ACT>(a, row * 128 + r, gc, v, u);
   else mx_store8(a, vec, row * 128 + r, gc, v);
+}
+
+// ------------------------------------------------------------------ product, 256 x 256 tile
+// The two alternating groups of dense_core.h. A slot holds SK elements of K; the
+// products of half a slot take as long as those of half a bf16 slot. With both operands
+// in E2M1 there is room for a third buffer of only one half of A: group 1 copies its
+// half of s+1 in interval 4s+3 and waits for it in 4s+4, before it reads in 4s+5.
+// Scale bytes come 16 per row (512 of K) and copy, every 512 / SK slots: a copy of one
+// word per row takes as long, and they would be a third of all cache lines asked for.
+template <bool A8>
+struct MxPp {
+  static constexpr int SK = A8 ? 128 : 256;
+  static constexpr int RBB = SK / 2;             // bytes of a row of B per slot; of A: 128
+  static constexpr int kD1 = A8 ? 3 : 2;         // buffers of group 1's half of A
+  static constexpr int kHA = 128 * 128, kHB = 128 * RBB;
+  static constexpr int kOffB = (3 + kD1) * kHA, kOffS = kOffB + 4 * kHB, kS = 512 * 16;
+  static constexpr int kLds = kOffS + 2 * kS;    // 144 and 160 KiB
+  static constexpr int kPer = 512 / SK;          // slots per copy of scales
+};
+
+// first operand B (E2M1), second A: the transposed product. OPS: the byte of the scale words
+template <bool A8, int OPS>
+MOK_DEV f32x16_t mx_mma(const i32x8_t& b, const i32x8_t& a, const f32x16_t& c, int sb, int sa) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 4, A8 ? 0 : 4, OPS, sb, OPS, sa);
+}
+
+template <bool A8, bool GLU, class LA, class LB>
+MOK_DEV void mx_pp_loop(uint8_t* lds, const LA& la, const LB& lb, const CopyScales16& ls, int K, Acc<4, 2>& acc) {
+  using X = MxPp<A8>;
+  const int grp = pp_group(), c = pp_col(), l = lane_id(), lr = l & 31, hl = l >> 5;
+  const int ns = (K + X::SK - 1) / X::SK;
+  const bool third = !grp || X::kD1 == 3;        // a third buffer of this group's half of A
+  const uint32_t base = lds_addr(lds), oa = grp * 3 * X::kHA, last = (third ? 2 : 1) * X::kHA;
+  const uint32_t sdst = base + X::kOffS + (grp ? 0 : 4096) + c * 1024;   // A's rows, then B's
+  acc.zero();
+  ls.dma(0, sdst);
+  lb.dma(0, base + X::kOffB + grp * X::kHB);
+  la.dma(0, base + oa);
+  if (third && ns > 1) {
+    la.dma(1, base + oa + X::kHA);
+    wait_vm_lds<4>();
+  } else {
+    wait_vm_lds<0>();
+  }
+  barrier_lds();
+  if (grp) barrier_lds();
+  // fragments of half a slot: one K step of 64 (A8) or two
+  constexpr int KK = A8 ? 1 : 2;
+  i32x4_t a[KK][4][A8 ? 2 : 1], b[KK][2];
+  int as[4], bs[2];
+  const auto read = [&](const uint8_t* ta, const uint8_t* tb, const uint8_t* ts, int s, int h) {
+    const auto at = [](const uint8_t* p) { return *reinterpret_cast<const i32x4_t*>(p); };
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      const int ks = KK * h + kk;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int r = 64 * (c & 1) + 32 * n + lr;
+        b[kk][n] = at(tb + (A8 ? lds_at64(r, 2 * ks + hl) : lds_at(r, 2 * ks + hl)));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 32 * i + lr;
+        if constexpr (A8) {
+          a[kk][i][0] = at(ta + lds_at(r, 4 * ks + hl));
+          a[kk][i][A8 ? 1 : 0] = at(ta + lds_at(r, 4 * ks + 2 + hl));
+        } else {
+          a[kk][i][0] = at(ta + lds_at(r, 2 * ks + hl));
+        }
+      }
+    }
+    if (A8 && h) return;                         // the word of both halves
+    // scale words of these 128 of K: byte 2 kk + hl (A8: 2 h + hl) is this lane's block
+    const int w = 4 * (A8 ? s % X::kPer : 2 * (s % X::kPer) + h);
+    // (past K the bytes are another row's)
+    const uint32_t in = A8 || X::SK * s + 128 * h < K ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(ts + (128 * grp + 32 * i + lr) * 16 + w);
+      as[i] = (int)((v & in) >> (8 * hl));
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const uint32_t v =
+          *reinterpret_cast<const uint32_t*>(ts + 4096 + scale_at<GLU>(64 * c + 32 * n + lr) * 16 + w);
+      bs[n] = (int)((v & in) >> (8 * hl));
+    }
+  };
+  const auto multiply = [&](auto hc) {
+    constexpr int h = decltype(hc)::value;
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+    pin(b[0][0]);
+    const auto step = [&](auto kc) {
+      constexpr int kk = decltype(kc)::value;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const i32x4_t lo = a[kk][i][0];
+        i32x8_t av = {lo[0], lo[1], lo[2], lo[3], 0, 0, 0, 0};
+        if constexpr (A8) {
+          const i32x4_t hi = a[kk][i][A8 ? 1 : 0];
+          av = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const i32x4_t q = b[kk][n];
+          const i32x8_t bv = {q[0], q[1], q[2], q[3], 0, 0, 0, 0};
+          acc.c[i][n] = mx_mma<A8, 2 * (A8 ? h : kk)>(bv, av, acc.c[i][n], bs[n], as[i]);
+        }
+      }
+    };
+    step(std::integral_constant<int, 0>{});
+    if constexpr (KK == 2) step(std::integral_constant<int, 1>{});
+    pin_acc(acc);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const int ahead = third ? 2 : 1;               // A of s + ahead is copied during s
+  uint32_t s0 = 0, sn = last;                    // A's buffers of s and s + ahead
+  for (int s = 0; s < ns; ++s) {
+    const uint8_t* ta = lds + oa + s0;
+    const uint8_t* tb = lds + X::kOffB + ((s & 1) * 2 + (c >> 1)) * X::kHB;
+    const uint8_t* ts = lds + X::kOffS + ((s / X::kPer) & 1) * X::kS;
+    const bool more = s + ahead < ns;
+    read(ta, tb, ts, s, 0);
+    // (the other buffer of scales was last read for slot s - 1)
+    if (s % X::kPer == 0 && (s + X::kPer) < ns)
+      ls.dma(s / X::kPer + 1, sdst + ((s / X::kPer + 1) & 1) * X::kS);
+    if (s + 1 < ns) lb.dma(s + 1, base + X::kOffB + (((s + 1) & 1) * 2 + grp) * X::kHB);
+    barrier_lds_only();
+    multiply(std::integral_constant<int, 0>{});
+    barrier_lds();
+    read(ta, tb, ts, s, 1);
+    if (more) la.dma(s + ahead, base + oa + sn);
+    if (grp) pp_wait<4>(more);
+    barrier_lds_only();
+    multiply(std::integral_constant<int, 1>{});
+    if (!grp) pp_wait<4>(more);
+    else if (X::kD1 == 2) wait_vm_lds<0>();
+    barrier_lds();
+    s0 = s0 == last ? 0 : s0 + X::kHA;
+    sn = sn == last ? 0 : sn + X::kHA;
+  }
+  if (!grp) barrier_lds();
+}
+
+// VAR: the gate's kind, or 1 = with a residual
+template <bool A8, bool GLU, int VAR>
+__global__ __launch_bounds__(kPpThreads, 1) void mx256_kernel(mok_mx_args a, bool vec, int nr, int nc) {
+  using X = MxPp<A8>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[X::kLds];
+  const int t = dense_index((int64_t)nr * nc);
+  if (t < 0) return;
+  int row, col;
+  dense_tile(t, nr, nc, 4, row, col);
+  const int m0 = row * 256, n0 = col * (GLU ? 128 : 256), nrows = min(256, a.M - m0);
+  Acc<4, 2> acc;
+  const int g = pp_group();
+  mx_pp_loop<A8, GLU>(lds, mx_copy_a<A8>(a, m0 + 128 * g), mx_copy_b<A8, GLU>(a, n0 + mx_cols<GLU>() * g),
+                      mx_copy_s16<GLU>(a, m0, n0), a.K, acc);
+  if constexpr (GLU) {
+    // a lane holds 16 of the 32 columns of a block of h, lane l ^ 32 the others. Codes go
+    // through LDS (128 bytes a row, 16-byte chunk c of row r at c ^ (r & 7))
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float h[16];
+      uint32_t m = 0;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        h[q] = gate_act<VAR>(acc.c[i][0][q]) * acc.c[i][1][q];
+        m = max(m, __float_as_uint(h[q]) & 0x7FFFFFFFu);
+      }
+      m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+      const bool nan = m >= 0x7F800000u;
+      const int sc = nan ? 255 : mx_scale_byte(__uint_as_float(m)), r = pp_row(i), c = pp_col(), hl = lane_id() >> 5;
+      const float inv = mx_inv_scale(sc);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t w = e4m3_pack4(h[4 * q] * inv, h[4 * q + 1] * inv, h[4 * q + 2] * inv, h[4 * q + 3] * inv);
+        *reinterpret_cast<uint32_t*>(lds + r * 128 + (((2 * c + (q >> 1)) ^ (r & 7)) << 4) + (q & 1) * 8 + hl * 4) =
+            nan ? 0u : w;
+      }
+      if (hl == 0 && r < nrows && n0 + 32 * c < a.N)
+        a.hs[(int64_t)(m0 + r) * (a.N / 32) + n0 / 32 + c] = (uint8_t)sc;
+    }
+    barrier_lds_only();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int idx = (int)threadIdx.x + u * kPpThreads, r = idx >> 3, ch = idx & 7;
+      if (r < nrows && n0 + 16 * ch < a.N)
+        *reinterpret_cast<uint4*>(a.hq + (int64_t)(m0 + r) * a.N + n0 + 16 * ch) =
+            *reinterpret_cast<const uint4*>(lds + r * 128 + ((ch ^ (r & 7)) << 4));
+    }
+  } else {
+    if constexpr (VAR == 1) {                    // (a block's y: aligned rows, N a multiple of 128)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          pp_add_residual(acc.c[i][n], a.res, a.ldd, m0 + min(pp_row(i), nrows - 1), n0 + pp_col0(n, 0), a.N);
+      __syncthreads();                           // (the residual may be y itself)
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          pp_put4(lds + pp_at16<256>(pp_row(i), pp_col0(n, q)), acc.c[i][n][4 * q], acc.c[i][n][4 * q + 1],
+                  acc.c[i][n][4 * q + 2], acc.c[i][n][4 * q + 3]);
+    barrier_lds_only();
+    pp_rows16<256>(lds, nrows, [&](int r, int c, uint4 v) {
+      if (n0 + c >= a.N) return;
+      bf16_t* d = a.d + (int64_t)(m0 + r) * a.ldd + n0 + c;
+      if (vec && n0 + c + 8 <= a.N) {
+        store_nt(d, v);
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int u = 0; u < 8 && n0 + c + u < a.N; ++u) d[u] = (bf16_t)(w[u >> 1] >> (16 * (u & 1)));
+      }
+    });
+  }
 }
 
 // ------------------------------------------------------------------ few rows
@@ -461,18 +708,17 @@ hipError_t launch_few(const mok_mx_args& a, hipStream_t st) {
 
 // ------------------------------------------------------------------ host
 struct Plan {
-  int nr, nc, splits;
+  int tile, nr, nc, splits;                      // tile 0: few rows
 };
 Plan plan_of(const mok_mx_args& a, bool glu) {
-  Plan p;
-  if (mok_mx_few(a.M)) return Plan{0, 0, 1};
-  p.nr = (a.M + 127) / 128;
-  p.nc = glu ? (a.N + 63) / 64 : (a.N + 127) / 128;
-  const int64_t n = (int64_t)p.nr * p.nc, slots = a.K / (a.a8 ? 128 : 256);
+  if (mok_mx_few(a.M)) return Plan{0, 0, 0, 1};
+  const auto rows = [&](int t) { return (a.M + t - 1) / t; };
+  const auto cols = [&](int t) { return ((glu ? 2 : 1) * (int64_t)a.N + t - 1) / t; };
+  if (rows(256) * cols(256) >= 256) return Plan{256, rows(256), (int)cols(256), 1};
+  const int64_t n = rows(128) * cols(128), slots = a.K / (a.a8 ? 128 : 256);
   int64_t sp = n > 0 ? 512 / n : 1;
   sp = sp < slots / 4 ? sp : slots / 4;
-  p.splits = sp < 1 ? 1 : (int)sp;
-  return p;
+  return Plan{128, rows(128), (int)cols(128), sp < 1 ? 1 : (int)sp};
 }
 
 template <bool A8, bool GLU, int ACT>
@@ -482,7 +728,10 @@ hipError_t launch(const mok_mx_args& a, const Plan& p, hipStream_t st) {
   if (tiles == 0) return hipSuccess;
   const bool vec = a.ldd % 8 == 0 && ((uintptr_t)a.d | (uintptr_t)a.res) % 16 == 0;
   const dim3 grid(dense_grid(tiles * p.splits)), block(kThreads);
-  if (p.splits == 1) {
+  if (p.tile == 256) {
+    if (!GLU && a.res) hipLaunchKernelGGL((mx256_kernel<A8, GLU, GLU ? ACT : 1>), grid, dim3(kPpThreads), 0, st, a, vec, p.nr, p.nc);
+    else hipLaunchKernelGGL((mx256_kernel<A8, GLU, ACT>), grid, dim3(kPpThreads), 0, st, a, vec, p.nr, p.nc);
+  } else if (p.splits == 1) {
     hipLaunchKernelGGL((mx128_kernel<A8, GLU, ACT, false>), grid, block, 0, st, a, vec, p.nr, p.nc, 1);
   } else {
     hipLaunchKernelGGL((mx128_kernel<A8, GLU, ACT, true>), grid, block, 0, st, a, vec, p.nr, p.nc, p.splits);

@@ -107,10 +107,10 @@ def test_row_pitches_and_what_lies_around(T, H, I):
         assert int(big.isnan().sum()) == big.numel() - v.numel()
 
 
-@pytest.mark.parametrize("T", [1, 40, 2500])
-def test_residual_in_place(T):
+@pytest.mark.parametrize("T,H", [(1, 1024), (40, 1024), (2500, 1024), (4111, 4104)])
+def test_residual_in_place(T, H):
     import torch
-    H, I = 1024, 520
+    I = 520
     c = {k: bf(v) for k, v in case(T, H, I, 2).items()}
     w = (c["wg"], c["wu"], c["wd"])
     ws = F.get_ffn_workspace(T, H, I, training=False)

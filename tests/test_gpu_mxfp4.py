@@ -123,7 +123,8 @@ def operands(M, N, K, a_dtype, seed=0):
 
 MM = [(1, 1, 128), (1, 4096, 7168), (2, 513, 256), (16, 1000, 384), (17, 129, 1152), (32, 768, 2048), (33, 768, 2048),
       (64, 2049, 640), (100, 7, 128), (128, 128, 512), (129, 257, 896), (300, 1001, 4096), (1037, 1544, 256),
-      (2500, 2300, 384), (4097, 4100, 256)]
+      (2500, 2300, 384), (4097, 4100, 256),
+      (4100, 4097, 128), (4095, 4225, 640), (2049, 8200, 1152)]
 
 
 @pytest.mark.parametrize("M,N,K", MM)
@@ -144,7 +145,7 @@ def test_matmul(M, N, K, a_dtype):
     assert np.linalg.norm(f64(d) - ref) <= HALF / np.sqrt(2) * np.linalg.norm(ref) or M * N < 64
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 77, 256), (40, 300, 512), (300, 300, 512), (2500, 2304, 256)])
+@pytest.mark.parametrize("M,N,K", [(3, 77, 256), (40, 300, 512), (300, 300, 512), (2500, 2304, 256), (4097, 4100, 384)])
 def test_matmul_output_windows(M, N, K):
     """D as a window of a wider matrix, at even and odd starts and pitches: the bits of a contiguous D, and
     nothing outside the window written."""
@@ -162,11 +163,11 @@ def test_matmul_output_windows(M, N, K):
 
 
 @pytest.mark.parametrize("a_dtype", [mok.MOK_MXFP4, mok.MOK_MXFP8])
-@pytest.mark.parametrize("M", [5, 200, 2500])
-def test_matmul_nan_scales(M, a_dtype):
+@pytest.mark.parametrize("M,K", [(5, 384), (200, 384), (2500, 384), (7300, 384), (7300, 640)])
+def test_matmul_nan_scales(M, K, a_dtype):
     """A NaN block makes its row (or column) NaN and nothing else."""
     import torch
-    N, K = 2304, 384
+    N = 2304
     a, sa, b, sb = operands(M, N, K, a_dtype, 2)[:4]
     ws = F.get_mx_matmul_workspace(M, N, K, a_dtype)
     want = F.run_mx_matmul(ws, u8(a), u8(sa), u8(b), u8(sb))
@@ -195,7 +196,7 @@ def ffn_case(T, H, I, seed=0):
 
 @pytest.mark.parametrize("T,H,I", [(1, 128, 128), (1, 7168, 2048), (5, 2048, 768), (16, 1024, 384), (31, 256, 512),
                                    (33, 384, 256), (64, 2048, 768), (129, 256, 640), (700, 1024, 768),
-                                   (4099, 512, 2176)])
+                                   (4099, 512, 2176), (4200, 4096, 256)])
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
 def test_ffn_forward_with_4bit_weights(T, H, I, kind):
     """Quantize the weights, then the block on them: the chain a server runs."""
@@ -214,11 +215,11 @@ def test_ffn_forward_with_4bit_weights(T, H, I, kind):
     assert_within(f64(y), r["y"], b["y"], "y")
 
 
-@pytest.mark.parametrize("T", [2, 50, 2100])
-def test_ffn_4bit_rows(T):
+@pytest.mark.parametrize("T,H", [(2, 512), (50, 512), (2100, 512), (4111, 4096)])
+def test_ffn_4bit_rows(T, H):
     """Row pitches, the residual in place, and tokens that are not finite, which come out NaN and alone."""
     import torch
-    H, I = 512, 2176
+    I = 2176
     c = ffn_case(T, H, I, 1)
     w = F.quantize_ffn_weights_mxfp4(bf(c["wg"]), bf(c["wu"]), bf(c["wd"]))
     ws = F.get_ffn_workspace(T, H, I, dtype=mok.MOK_MXFP4, training=False)
