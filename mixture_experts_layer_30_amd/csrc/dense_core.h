@@ -272,18 +272,18 @@ MOK_DEV void pp_wait(bool more) {
   else wait_vm_lds<0>();
 }
 
-// la, lb: this wavefront's group's halves
+// slots [j0, ns); la, lb: this wavefront's group's halves
 template <class LA, class LB>
-MOK_DEV void pp_loop(uint8_t* lds, const LA& la, const LB& lb, int ns, Acc<4, 2>& acc) {
+MOK_DEV void pp_loop(uint8_t* lds, const LA& la, const LB& lb, int j0, int ns, Acc<4, 2>& acc) {
   static_assert(LA::kDma == 4 && LB::kDma == 4, "four copies per half and wavefront");
   const int grp = pp_group(), c = pp_col();
   const uint32_t base = lds_addr(lds), oa = grp * 3 * kPpHalf, ob = 6 * kPpHalf;
   acc.zero();
-  if (ns <= 0) return;
-  lb.dma(0, base + ob + grp * kPpHalf);
-  la.dma(0, base + oa);
-  if (ns > 1) {
-    la.dma(1, base + oa + kPpHalf);
+  if (ns <= j0) return;
+  lb.dma(j0, base + ob + grp * kPpHalf);
+  la.dma(j0, base + oa);
+  if (ns > j0 + 1) {
+    la.dma(j0 + 1, base + oa + kPpHalf);
     wait_vm_lds<4>();
   } else {
     wait_vm_lds<0>();
@@ -316,12 +316,13 @@ MOK_DEV void pp_loop(uint8_t* lds, const LA& la, const LB& lb, int ns, Acc<4, 2>
     __builtin_amdgcn_sched_barrier(0);
   };
   uint32_t s0 = 0, s2 = 2 * kPpHalf;             // A's buffer of s, and of s + 2
-  for (int s = 0; s < ns; ++s) {
+  for (int s = j0; s < ns; ++s) {
+    const int par = (s - j0) & 1;
     const uint8_t* ta = lds + oa + s0;
-    const uint8_t* tb = lds + ob + ((s & 1) * 2 + (c >> 1)) * kPpHalf;
+    const uint8_t* tb = lds + ob + (par * 2 + (c >> 1)) * kPpHalf;
     const bool more = s + 2 < ns;
     read(ta, tb, 0);
-    if (s + 1 < ns) lb.dma(s + 1, base + ob + (((s + 1) & 1) * 2 + grp) * kPpHalf);
+    if (s + 1 < ns) lb.dma(s + 1, base + ob + ((par ^ 1) * 2 + grp) * kPpHalf);
     barrier_lds_only();
     multiply();
     barrier_lds();
@@ -386,6 +387,23 @@ MOK_DEV void pp_stage32(uint8_t* lds, const Acc<4, 2>& acc, int n) {
           make_float4(acc.c[i][n][4 * q], acc.c[i][n][4 * q + 1], acc.c[i][n][4 * q + 2], acc.c[i][n][4 * q + 3]);
 }
 
+// the tile as fp32 rows of 256 columns at p (rows [0, nrows)), for products split along K
+MOK_DEV void pp_store32(uint8_t* lds, const Acc<4, 2>& acc, int nrows, float* p) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    if (n) barrier_lds_only();
+    pp_stage32(lds, acc, n);
+    barrier_lds_only();
+#pragma unroll 4
+    for (int idx = threadIdx.x; idx < 256 * 32; idx += kPpThreads) {
+      const int r = idx >> 5, x = (idx & 31) * 4;
+      if (r < nrows)
+        *reinterpret_cast<float4*>(p + r * 256 + 64 * (x >> 5) + 32 * n + (x & 31)) =
+            *reinterpret_cast<const float4*>(lds + r * kPpPitch + x * 4);
+    }
+  }
+}
+
 // W consecutive fp32 values (W a multiple of 4) at p
 template <int W>
 MOK_DEV void load_f32(const void* p, float v[W]) {
@@ -396,8 +414,31 @@ MOK_DEV void load_f32(const void* p, float v[W]) {
   }
 }
 
+// v = the sum over the splits, in ascending order, of eight fp32 values at p, each split's
+// `step` floats after the one before (four splits' loads in flight)
+MOK_DEV void sum_splits(const float* p, int64_t step, int splits, float v[8]) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) v[u] = 0.f;
+  int s = 0;
+  for (; s + 4 <= splits; s += 4) {
+    float q[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load_f32<8>(p + (s + k) * step, q[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] += q[k][u];
+  }
+  for (; s < splits; ++s) {
+    float q[8];
+    load_f32<8>(p + s * step, q);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] += q[u];
+  }
+}
+
 // ------------------------------------------------------------------ few rows
-// Products with at most kFewRows rows of x read the weights once and are bound by
+// Products with few rows of x (at most kFewRows) read the weights once and are bound by
 // that. A workgroup of eight wavefronts takes 16 weight rows (one 16 x 16
 // fragment; for gate|up 8 gate and 8 up rows, so that the gate's product stays in
 // the workgroup) and every wavefront a contiguous eighth of K, straight from
@@ -455,6 +496,44 @@ MOK_DEV void dense_tile(int i, int nr, int nc, int grp, int& row, int& col) {
   const int gi = i / (grp * nc), hg = min(grp, nr - grp * gi), j = i - gi * grp * nc;
   col = j / hg;
   row = grp * gi + j % hg;
+}
+
+// Tile and split of a product of M x N (x batch) over `slots` slots of K: the least
+// estimated time. A pass of 256 workgroups of 256 x 256 tiles (one a CU), or of 512 of
+// 128 x 128 (two a CU), takes a fixed part (launch, first copies, epilogue) and a part
+// per slot, of which a 128 x 128 tile with a CU to itself needs the share `alone`;
+// partial sums add a launch and the traffic of writing and reading them. With the
+// constants fitted to 280 shapes of 65 to 8192 rows, each timed with both tiles and up
+// to 8 splits, the choice was within 1% of the fastest in the mean and 20% at worst.
+struct dense_cost {
+  float fix256, slot256, fix128, slot128, alone; // us
+  float join, rate;                              // us, bytes per us
+};
+inline float dense_plan(int64_t M, int64_t N, int batch, int64_t slots, const dense_cost& c, int* tile, int* splits) {
+  float best = 0.f;
+  *tile = 128;
+  *splits = 1;
+  for (int ts = 256; ts >= 128; ts -= 128) {
+    const int64_t n = ((M + ts - 1) / ts) * ((N + ts - 1) / ts) * batch, fill = ts == 256 ? 256 : 512;
+    for (int64_t s = 1; s == 1 || (n * s <= fill && slots >= 4 * s); ++s) {
+      const int64_t passes = (n * s + fill - 1) / fill, per = (slots + s - 1) / s;
+      float t = ts == 256 ? passes * (c.fix256 + per * c.slot256)
+                          : passes * c.fix128 + per * c.slot128 * (n * s <= 256 ? c.alone : (float)passes);
+      if (s > 1) t += c.join + (float)s * M * N * batch * 8 / c.rate;
+      if (best == 0.f || t < best) {
+        best = t;
+        *tile = ts;
+        *splits = (int)s;
+      }
+    }
+  }
+  return best;
+}
+// The same for few rows: a launch, the weights (`rows` of K elements) once, and x in every
+// workgroup of 16 weight rows, which each CU takes in at 37 bytes per ns (fitted to 1 to 64
+// rows of bf16 at 4096 x 7168, 7168 x 2048, 1536 x 2048 and 2048 x 768).
+inline float few_time(int64_t M, int64_t rows, int64_t K) {
+  return 2.5f + (float)rows * K * 2 / 4.6e6f + (float)M * K * 2 * ((rows / 16 + 255) / 256) / 37e3f;
 }
 inline unsigned dense_grid(int64_t n) { return (unsigned)((n + kXcds - 1) / kXcds * kXcds); }
 

@@ -19,6 +19,10 @@ namespace {
 
 constexpr int kNoSeg = 0x7fffffc0;               // one segment of K (CopyT)
 
+// row tiles that an XCD's tiles in flight span (dense_core.h): about a square block of them
+template <int TS>
+constexpr int kGroup = TS == 256 ? 4 : 8;
+
 // rows, columns and contracted length of a product, in tiles' terms
 struct Shape {
   int M, N, K, batch;                            // batch 2: dWg and dWu, rows of one product each
@@ -170,7 +174,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn128_kernel(mok_ffn_args a, int
   if (i < 0) return;
   const int split = SPLIT ? i / tiles : 0, t = SPLIT ? i % tiles : i, half = t / (nr * nc);
   int row, col;
-  dense_tile(t - half * nr * nc, nr, nc, 8, row, col);
+  dense_tile(t - half * nr * nc, nr, nc, kGroup<128>, row, col);
   const int m0 = row * 128, n0 = col * out_cols<OP, 128>();
   const int ns = (K + 63) / 64;
   const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
@@ -190,32 +194,23 @@ __global__ __launch_bounds__(kThreads, 2) void ffn128_kernel(mok_ffn_args a, int
   }
 }
 
-// sums of the partial tiles in ascending split order, and the epilogue; one
-// workgroup per 256 chunks of eight output columns
-template <int OP, int ACT>
+// sums of the partial tiles of TS x TS, and the epilogue; one workgroup per 256 chunks of
+// eight output columns
+template <int OP, int ACT, int TS>
 __global__ __launch_bounds__(kThreads) void ffn_join_kernel(mok_ffn_args a, int M, int nr, int nc, int batch,
                                                             int splits) {
-  constexpr int CH = out_cols<OP, 128>() / 8;
+  constexpr int CH = out_cols<OP, TS>() / 8;
   const int tiles = nr * nc * batch, t = (int)blockIdx.y, half = t / (nr * nc);
   int row, col;
-  dense_tile(t - half * nr * nc, nr, nc, 8, row, col);
+  dense_tile(t - half * nr * nc, nr, nc, kGroup<TS>, row, col);
   const int idx = (int)blockIdx.x * kThreads + (int)threadIdx.x;
   const int r = idx / CH, c = (idx % CH) * 8;
-  if (r >= min(128, M - row * 128)) return;
-  const float* p = a.part + (int64_t)t * 16384 + r * 128 + acc_col<OP>(c);
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int s = 0; s < splits; ++s, p += (int64_t)tiles * 16384) {
-    float q[8];
-    load_f32<8>(p, q);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] += q[u];
-    if constexpr (OP == FFN_GATEUP) {
-      load_f32<8>(p + 32, q);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) w[u] += q[u];
-    }
-  }
-  finish8<OP, ACT>(a, row * 128 + r, col * out_cols<OP, 128>() + c, half, v, w);
+  if (r >= min(TS, M - row * TS)) return;
+  const float* p = a.part + (int64_t)t * TS * TS + r * TS + acc_col<OP>(c);
+  float v[8], w[8];
+  sum_splits(p, (int64_t)tiles * TS * TS, splits, v);
+  if constexpr (OP == FFN_GATEUP) sum_splits(p + 32, (int64_t)tiles * TS * TS, splits, w);
+  finish8<OP, ACT>(a, row * TS + r, col * out_cols<OP, TS>() + c, half, v, w);
 }
 
 // Epilogue of a 256 x 256 tile (the main loop ends in a barrier: LDS is free). VAR: the
@@ -321,20 +316,25 @@ MOK_DEV void finish256(const mok_ffn_args& a, uint8_t* lds, Acc<4, 2>& acc, int 
   }
 }
 
-template <int OP, int VAR>
+template <int OP, int VAR, bool SPLIT>
 __global__ __launch_bounds__(kPpThreads, 1) void ffn256_kernel(mok_ffn_args a, int M, int K, int nr, int nc,
-                                                               int batch) {
+                                                               int batch, int splits) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kPpLds];
-  const int t = dense_index((int64_t)nr * nc * batch);
-  if (t < 0) return;
-  const int half = t / (nr * nc);
+  const int tiles = nr * nc * batch;
+  const int ix = dense_index((int64_t)tiles * splits);
+  if (ix < 0) return;
+  const int split = SPLIT ? ix / tiles : 0, t = SPLIT ? ix % tiles : ix, half = t / (nr * nc);
   int row, col;
-  dense_tile(t - half * nr * nc, nr, nc, 4, row, col);
+  dense_tile(t - half * nr * nc, nr, nc, kGroup<256>, row, col);
+  const int ns = (K + 63) / 64;
+  const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
+  const int j1 = SPLIT ? (int)((int64_t)ns * (split + 1) / splits) : ns;
   const int m0 = row * 256, n0 = col * out_cols<OP, 256>();
   const int nrows = min(256, M - m0), g = pp_group();
   Acc<4, 2> acc;
-  pp_loop(lds, copy_a<OP>(a, m0 + 128 * g, half), copy_b<OP>(a, n0 + out_cols<OP, 128>() * g), (K + 63) / 64, acc);
-  finish256<OP, VAR>(a, lds, acc, nrows, m0, n0, half);
+  pp_loop(lds, copy_a<OP>(a, m0 + 128 * g, half), copy_b<OP>(a, n0 + out_cols<OP, 128>() * g), j0, j1, acc);
+  if constexpr (SPLIT) pp_store32(lds, acc, nrows, a.part + ((int64_t)split * tiles + t) * 65536);
+  else finish256<OP, VAR>(a, lds, acc, nrows, m0, n0, half);
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -431,27 +431,20 @@ struct Plan {
   int tile, nr, nc, splits;                      // tile 0: few tokens
 };
 
+// (slots of 64)
+constexpr dense_cost kCost = {14.2f, 1.06f, 3.7f, 1.09f, 0.76f, 3.9f, 3.6e6f};
+
 Plan plan_of(const mok_ffn_args& a, mok_ffn_op op) {
   Plan p;
   p.s = shape_of(a, op);
-  const auto tiles = [&](int n) {
-    return (int64_t)((p.s.M + n - 1) / n) * ((p.s.N + n - 1) / n) * p.s.batch;
-  };
-  if (a.T <= kFewRows && (op == FFN_GATEUP || op == FFN_DOWN)) {
+  const float t = dense_plan(p.s.M, p.s.N, p.s.batch, (p.s.K + 63) / 64, kCost, &p.tile, &p.splits);
+  if (a.T <= kFewRows && (op == FFN_GATEUP || op == FFN_DOWN) && few_time(a.T, p.s.N, p.s.K) < t) {
     p.tile = p.nr = p.nc = 0;
     p.splits = 1;
     return p;
   }
-  p.tile = tiles(256) >= 256 ? 256 : 128;
   p.nr = (p.s.M + p.tile - 1) / p.tile;
   p.nc = (p.s.N + p.tile - 1) / p.tile;
-  p.splits = 1;
-  if (p.tile == 128) {
-    const int64_t n = tiles(128), slots = (p.s.K + 63) / 64;
-    int64_t sp = n > 0 ? 512 / n : 1;
-    sp = sp < slots / 4 ? sp : slots / 4;
-    p.splits = sp < 1 ? 1 : (int)sp;
-  }
   return p;
 }
 
@@ -462,20 +455,27 @@ hipError_t launch(const mok_ffn_args& a, const Plan& p, hipStream_t st) {
   const int64_t tiles = (int64_t)p.nr * p.nc * p.s.batch;
   if (tiles * p.splits > (1 << 30)) return hipErrorInvalidValue;
   if (tiles == 0) return hipSuccess;
-  const dim3 grid(dense_grid(tiles * p.splits)), block(kThreads);
-  if (p.tile == 256 && OP == FFN_DOWN && a.res)
-    hipLaunchKernelGGL((ffn256_kernel<OP, OP == FFN_DOWN ? 1 : ACT>), grid, dim3(kPpThreads), 0, st, a, p.s.M, p.s.K,
-                       p.nr, p.nc, p.s.batch);
-  else if (p.tile == 256)
-    hipLaunchKernelGGL((ffn256_kernel<OP, ACT>), grid, dim3(kPpThreads), 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch);
-  else if (p.splits == 1)
-    hipLaunchKernelGGL((ffn128_kernel<OP, ACT, false>), grid, block, 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch, 1);
-  else {
-    hipLaunchKernelGGL((ffn128_kernel<OP, ACT, true>), grid, block, 0, st, a, p.s.M, p.s.K, p.nr, p.nc, p.s.batch,
-                       p.splits);
-    const int ch = 128 * out_cols<OP, 128>() / 8;
-    hipLaunchKernelGGL((ffn_join_kernel<OP, ACT>), dim3((ch + kThreads - 1) / kThreads, (unsigned)tiles), block, 0, st,
-                       a, p.s.M, p.nr, p.nc, p.s.batch, p.splits);
+  const dim3 grid(dense_grid(tiles * p.splits)), block(p.tile == 256 ? kPpThreads : kThreads);
+  const int nr = p.nr, nc = p.nc, nb = p.s.batch;
+  if (p.splits > 1) {
+    if (p.tile == 256)
+      hipLaunchKernelGGL((ffn256_kernel<OP, 0, true>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, p.splits);
+    else
+      hipLaunchKernelGGL((ffn128_kernel<OP, 0, true>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, p.splits);
+    const int ch = p.tile * (OP == FFN_GATEUP ? p.tile / 2 : p.tile) / 8;
+    const dim3 jgrid((ch + kThreads - 1) / kThreads, (unsigned)tiles);
+    if (p.tile == 256)
+      hipLaunchKernelGGL((ffn_join_kernel<OP, ACT, 256>), jgrid, dim3(kThreads), 0, st, a, p.s.M, nr, nc, nb, p.splits);
+    else
+      hipLaunchKernelGGL((ffn_join_kernel<OP, ACT, 128>), jgrid, dim3(kThreads), 0, st, a, p.s.M, nr, nc, nb, p.splits);
+  } else if (p.tile == 256) {
+    if (OP == FFN_DOWN && a.res)
+      hipLaunchKernelGGL((ffn256_kernel<OP, OP == FFN_DOWN ? 1 : ACT, false>), grid, block, 0, st, a, p.s.M, p.s.K, nr,
+                         nc, nb, 1);
+    else
+      hipLaunchKernelGGL((ffn256_kernel<OP, ACT, false>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, 1);
+  } else {
+    hipLaunchKernelGGL((ffn128_kernel<OP, ACT, false>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, 1);
   }
   return hipGetLastError();
 }
@@ -484,7 +484,7 @@ hipError_t launch(const mok_ffn_args& a, const Plan& p, hipStream_t st) {
 
 size_t mok_ffn_part_bytes(const mok_ffn_args& a, mok_ffn_op op) {
   const Plan p = plan_of(a, op);
-  return p.splits > 1 ? (size_t)p.splits * p.nr * p.nc * p.s.batch * 65536 : 0;
+  return p.splits > 1 ? (size_t)p.splits * p.nr * p.nc * p.s.batch * p.tile * p.tile * 4 : 0;
 }
 
 hipError_t mok_launch_ffn(const mok_ffn_args& a, mok_ffn_op op, int act, hipStream_t st) {

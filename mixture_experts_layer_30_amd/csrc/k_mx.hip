@@ -15,28 +15,9 @@ using namespace mok;
 namespace {
 
 // ------------------------------------------------------------------ quantize
-// Scale byte of a block: clamp(floor(log2 amax) - 2 + 127, 0, 254), 0 for zeros
-// (2: the exponent of the largest E2M1 value, 6 = 1.5 * 2^2).
-MOK_DEV int mxfp4_scale_byte(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  if (b == 0) return 0;
-  const int field = (int)(b >> 23);
-  const int e = field > 0 ? field - 127 : (31 - __clz((int)b)) - 149;
-  return max(0, min(254, e - 2 + 127));
-}
-
-// E2M1 code of q, nearest value of 0, 0.5, 1, 1.5, 2, 3, 4, 6, ties to the even
-// code, saturating at 6: the code counts the midpoints that |q| has passed.
-MOK_DEV uint32_t e2m1_encode(float q) {
-  const float a = fabsf(q);
-  const uint32_t m = (uint32_t)(a > 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a > 1.25f) +
-                     (uint32_t)(a >= 1.75f) + (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.0f);
-  return m | ((__float_as_uint(q) >> 28) & 8u);
-}
-MOK_DEV float e2m1_decode(uint32_t c) {
-  const uint32_t m = c & 7u;
-  const uint32_t bits = m >= 2 ? ((126u + (m >> 1)) << 23) | ((m & 1u) << 22) : (m ? 0x3F000000u : 0u);
-  return __uint_as_float(bits | ((c & 8u) << 28));
+// E8M0 scale as a float: 2^(s - 127), NaN for 255
+MOK_DEV float e8m0(int s) {
+  return __uint_as_float(s == 255 ? 0x7FC00000u : s == 0 ? 0x00400000u : (uint32_t)s << 23);
 }
 
 // bits of the largest magnitude of a block held by four adjacent lanes, eight
@@ -49,40 +30,54 @@ MOK_DEV uint32_t block_max_bits(const float v[8]) {
   return max(m, (uint32_t)__shfl_xor((int)m, 2));
 }
 
-// Four adjacent lanes per block, eight elements each: 16-byte loads along the
-// row, the block's largest magnitude over the four lanes, 4 bytes of codes per
-// lane. A block that holds a NaN or an infinity, which the format cannot, gets
-// the NaN scale 255: it reads back, and multiplies, as NaN.
+// Four adjacent lanes per block, eight elements each: 16-byte loads along the row, the
+// block's largest magnitude over the four lanes, 4 bytes of codes per lane. The scale
+// byte is clamp(floor(log2 amax) - 2 + 127, 0, 254) (2: the exponent of the largest E2M1
+// value, 6 = 1.5 * 2^2), which from the exponent field f of a bf16 amax is max(f - 2, 0),
+// 0 for zeros and subnormals too. The codes are the hardware's (v_cvt_scalef32_pk_fp4_bf16:
+// value / 2^(s-127) to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6, ties to the even code,
+// saturating, sign kept): equal to the definition on gfx950 for every bf16 value at every
+// scale. A block that holds a NaN or an infinity, which the format cannot, gets the NaN
+// scale 255: it reads back, and multiplies, as NaN.
+// Bound by memory: 16384 x 7168 in TODO us; seven comparisons per element in place
+// of the conversion took 80 us.
 __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const bf16_t* __restrict__ src, int64_t n8,
                                                             uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= n8) return;                         // n8 is a multiple of 4: whole blocks leave
   const uint4 raw = reinterpret_cast<const uint4*>(src)[idx];
-  float v[8];
-  unpack_bf16x8(raw, v);
-  const uint32_t m = block_max_bits(v);
-  const bool nan = m >= 0x7F800000u;
-  const int sc = nan ? 255 : mxfp4_scale_byte(__uint_as_float(m));
-  const float inv = mx_inv_scale(sc);
-  uint32_t w = 0;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) w |= e2m1_encode(v[u] * inv) << (4 * u);
+  const auto mag = [](uint32_t v) { return __builtin_bit_cast(u16x2, v & 0x7FFF7FFFu); };
+  const u16x2 m2 = __builtin_elementwise_max(__builtin_elementwise_max(mag(raw.x), mag(raw.y)),
+                                             __builtin_elementwise_max(mag(raw.z), mag(raw.w)));
+  int m = max((int)m2[0], (int)m2[1]);
+  m = max(m, __shfl_xor(m, 1));
+  m = max(m, __shfl_xor(m, 2));
+  const bool nan = m >= 0x7F80;
+  const int sc = nan ? 255 : max((m >> 7) - 2, 0);
+  const float x = e8m0(nan ? 127 : sc);
+  const auto pair = [](uint32_t v) { return __builtin_bit_cast(bf16x2_t, v); };
+  uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(0u, pair(raw.x), x, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(raw.y), x, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(raw.z), x, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(raw.w), x, 3);
   reinterpret_cast<uint32_t*>(q)[idx] = nan ? 0u : w;
   if ((idx & 3) == 0) scales[idx >> 2] = (uint8_t)sc;
 }
 
+// code * 2^(s-127), exact in bf16 (v_cvt_scalef32_pk_bf16_fp4); 16384 x 7168 in TODO us
 __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __restrict__ q,
                                                               const uint8_t* __restrict__ scales, int64_t n8,
                                                               bf16_t* __restrict__ dst) {
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= n8) return;
   const uint32_t w = reinterpret_cast<const uint32_t*>(q)[idx];
-  const int sc = scales[idx >> 2];
-  const float x = sc == 255 ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, sc - 127);
-  float v[8];
-#pragma unroll
-  for (int u = 0; u < 8; ++u) v[u] = e2m1_decode((w >> (4 * u)) & 15u) * x;
-  reinterpret_cast<uint4*>(dst)[idx] = pack_bf16x8(v);
+  const float x = e8m0(scales[idx >> 2]);
+  const auto bits = [](bf16x2_t v) { return __builtin_bit_cast(uint32_t, v); };
+  reinterpret_cast<uint4*>(dst)[idx] = make_uint4(bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, x, 0)),
+                                                  bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, x, 1)),
+                                                  bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, x, 2)),
+                                                  bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, x, 3)));
 }
 
 // MXFP8 rows (E4M3, the scale rule of the layer's quantizer) of a bf16 or fp32
@@ -229,27 +224,21 @@ MOK_DEV void mx_store8(const mok_mx_args& a, bool vec, int r, int c, float v[8])
   }
 }
 
-// 32 columns from c on of row r of h = act(g) * u, as E4M3 codes and a scale
+// Eight columns from c on of row r of h = act(g) * u as E4M3 codes; four adjacent lanes
+// hold a block, and the first writes its scale.
 template <int ACT>
-MOK_DEV void mx_gate32(const mok_mx_args& a, int r, int c, const float g[32], const float u[32]) {
-  float h[32];
-  uint32_t m = 0;
+MOK_DEV void mx_gate8(const mok_mx_args& a, int r, int c, const float g[8], const float u[8]) {
+  float h[8];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    h[i] = gate_act<ACT>(g[i]) * u[i];
-    m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-  }
+  for (int i = 0; i < 8; ++i) h[i] = gate_act<ACT>(g[i]) * u[i];
+  const uint32_t m = block_max_bits(h);
   const bool nan = m >= 0x7F800000u;
   const int sc = nan ? 255 : mx_scale_byte(__uint_as_float(m));
   const float inv = mx_inv_scale(sc);
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i] = nan ? 0u : e4m3_pack4(h[4 * i] * inv, h[4 * i + 1] * inv, h[4 * i + 2] * inv, h[4 * i + 3] * inv);
-  uint4* d = reinterpret_cast<uint4*>(a.hq + (int64_t)r * a.N + c);
-  d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  a.hs[(int64_t)r * (a.N / 32) + c / 32] = (uint8_t)sc;
+  const uint32_t lo = e4m3_pack4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+  const uint32_t hi = e4m3_pack4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv);
+  *reinterpret_cast<uint2*>(a.hq + (int64_t)r * a.N + c) = nan ? make_uint2(0, 0) : make_uint2(lo, hi);
+  if ((c & 31) == 0) a.hs[(int64_t)r * (a.N / 32) + c / 32] = (uint8_t)sc;
 }
 
 template <bool GLU>
@@ -330,12 +319,14 @@ __global__ __launch_bounds__(kThreads, 2) void mx128_kernel(mok_mx_args a, bool 
       reinterpret_cast<float4*>(p)[idx] =
           *reinterpret_cast<const float4*>(lds + (idx >> 5) * kPitch128 + (idx & 31) * 16);
   } else if constexpr (GLU) {
-    const int r = (int)threadIdx.x >> 1, c = ((int)threadIdx.x & 1) * 32;
-    if (r < nrows && n0 + c < a.N) {
-      float g[32], u[32];
-      load_f32<32>(lds + r * kPitch128 + c * 8, g);
-      load_f32<32>(lds + r * kPitch128 + c * 8 + 128, u);
-      mx_gate32<ACT>(a, m0 + r, n0 + c, g, u);
+    for (int idx = threadIdx.x; idx < nrows * 8; idx += kThreads) {
+      const int r = idx >> 3, c = (idx & 7) * 8;
+      if (n0 + c >= a.N) continue;               // (N a multiple of 128: whole blocks)
+      float g[8], u[8];
+      const uint8_t* p = lds + r * kPitch128 + ((c >> 5) * 64 + (c & 31)) * 4;
+      load_f32<8>(p, g);
+      load_f32<8>(p + 128, u);
+      mx_gate8<ACT>(a, m0 + r, n0 + c, g, u);
     }
   } else {
     for (int idx = threadIdx.x; idx < nrows * 16; idx += kThreads) {
@@ -347,34 +338,24 @@ __global__ __launch_bounds__(kThreads, 2) void mx128_kernel(mok_mx_args a, bool 
   }
 }
 
-template <bool GLU, int ACT>
+template <bool GLU, int ACT, int TS>
 __global__ __launch_bounds__(kThreads) void mx_join_kernel(mok_mx_args a, bool vec, int nr, int nc, int splits) {
+  constexpr int NC = GLU ? TS / 2 : TS, CH = NC / 8;
   const int tiles = nr * nc, t = (int)blockIdx.y;
   int row, col;
-  dense_tile(t, nr, nc, 8, row, col);
+  dense_tile(t, nr, nc, TS == 256 ? 4 : 8, row, col);
   const int idx = (int)blockIdx.x * kThreads + (int)threadIdx.x;
-  constexpr int W = GLU ? 32 : 8, CH = mx_cols<GLU>() / W;
-  const int r = idx / CH, c = (idx % CH) * W;
-  if (r >= min(128, a.M - row * 128)) return;
-  const int gc = col * mx_cols<GLU>() + c;
-  if (gc >= a.N) return;
-  const float* p = a.part + (int64_t)t * 16384 + r * 128 + (GLU ? 2 * c : c);
-  float v[W], u[W];
-#pragma unroll
-  for (int q = 0; q < W; ++q) v[q] = u[q] = 0.f;
-  for (int s = 0; s < splits; ++s, p += (int64_t)tiles * 16384) {
-    float q[W];
-    load_f32<W>(p, q);
-#pragma unroll
-    for (int x = 0; x < W; ++x) v[x] += q[x];
-    if constexpr (GLU) {
-      load_f32<W>(p + 32, q);
-#pragma unroll
-      for (int x = 0; x < W; ++x) u[x] += q[x];
-    }
+  const int r = idx / CH, c = (idx % CH) * 8, gc = col * NC + c;
+  if (r >= min(TS, a.M - row * TS) || gc >= a.N) return;
+  const float* p = a.part + (int64_t)t * TS * TS + r * TS + (GLU ? (c >> 5) * 64 + (c & 31) : c);
+  float v[8], u[8];
+  sum_splits(p, (int64_t)tiles * TS * TS, splits, v);
+  if constexpr (GLU) {
+    sum_splits(p + 32, (int64_t)tiles * TS * TS, splits, u);
+    mx_gate8<ACT>(a, row * TS + r, gc, v, u);
+  } else {
+    mx_store8(a, vec, row * TS + r, gc, v);
   }
-  if constexpr (GLU) mx_gate32<ACT>(a, row * 128 + r, gc, v, u);
-  else mx_store8(a, vec, row * 128 + r, gc, v);
 }
 
 // ------------------------------------------------------------------ product, 256 x 256 tile
@@ -402,19 +383,19 @@ MOK_DEV f32x16_t mx_mma(const i32x8_t& b, const i32x8_t& a, const f32x16_t& c, i
 }
 
 template <bool A8, bool GLU, class LA, class LB>
-MOK_DEV void mx_pp_loop(uint8_t* lds, const LA& la, const LB& lb, const CopyScales16& ls, int K, Acc<4, 2>& acc) {
+MOK_DEV void mx_pp_loop(uint8_t* lds, const LA& la, const LB& lb, const CopyScales16& ls, int K, int j0, int ns,
+                        Acc<4, 2>& acc) {
   using X = MxPp<A8>;
   const int grp = pp_group(), c = pp_col(), l = lane_id(), lr = l & 31, hl = l >> 5;
-  const int ns = (K + X::SK - 1) / X::SK;
   const bool third = !grp || X::kD1 == 3;        // a third buffer of this group's half of A
   const uint32_t base = lds_addr(lds), oa = grp * 3 * X::kHA, last = (third ? 2 : 1) * X::kHA;
   const uint32_t sdst = base + X::kOffS + (grp ? 0 : 4096) + c * 1024;   // A's rows, then B's
   acc.zero();
-  ls.dma(0, sdst);
-  lb.dma(0, base + X::kOffB + grp * X::kHB);
-  la.dma(0, base + oa);
-  if (third && ns > 1) {
-    la.dma(1, base + oa + X::kHA);
+  ls.dma(j0 / X::kPer, sdst + ((j0 / X::kPer) & 1) * X::kS);
+  lb.dma(j0, base + X::kOffB + grp * X::kHB);
+  la.dma(j0, base + oa);
+  if (third && ns > j0 + 1) {
+    la.dma(j0 + 1, base + oa + X::kHA);
     wait_vm_lds<4>();
   } else {
     wait_vm_lds<0>();
@@ -494,16 +475,17 @@ MOK_DEV void mx_pp_loop(uint8_t* lds, const LA& la, const LB& lb, const CopyScal
   };
   const int ahead = third ? 2 : 1;               // A of s + ahead is copied during s
   uint32_t s0 = 0, sn = last;                    // A's buffers of s and s + ahead
-  for (int s = 0; s < ns; ++s) {
+  for (int s = j0; s < ns; ++s) {
+    const int par = (s - j0) & 1;
     const uint8_t* ta = lds + oa + s0;
-    const uint8_t* tb = lds + X::kOffB + ((s & 1) * 2 + (c >> 1)) * X::kHB;
+    const uint8_t* tb = lds + X::kOffB + (par * 2 + (c >> 1)) * X::kHB;
     const uint8_t* ts = lds + X::kOffS + ((s / X::kPer) & 1) * X::kS;
     const bool more = s + ahead < ns;
     read(ta, tb, ts, s, 0);
-    // (the other buffer of scales was last read for slot s - 1)
-    if (s % X::kPer == 0 && (s + X::kPer) < ns)
+    // (the other buffer of scales was last read for slot s - 1, or not yet)
+    if ((s % X::kPer == 0 || s == j0) && (s / X::kPer + 1) * X::kPer < ns)
       ls.dma(s / X::kPer + 1, sdst + ((s / X::kPer + 1) & 1) * X::kS);
-    if (s + 1 < ns) lb.dma(s + 1, base + X::kOffB + (((s + 1) & 1) * 2 + grp) * X::kHB);
+    if (s + 1 < ns) lb.dma(s + 1, base + X::kOffB + ((par ^ 1) * 2 + grp) * X::kHB);
     barrier_lds_only();
     multiply(std::integral_constant<int, 0>{});
     barrier_lds();
@@ -522,20 +504,26 @@ MOK_DEV void mx_pp_loop(uint8_t* lds, const LA& la, const LB& lb, const CopyScal
 }
 
 // VAR: the gate's kind, or 1 = with a residual
-template <bool A8, bool GLU, int VAR>
-__global__ __launch_bounds__(kPpThreads, 1) void mx256_kernel(mok_mx_args a, bool vec, int nr, int nc) {
+template <bool A8, bool GLU, int VAR, bool SPLIT>
+__global__ __launch_bounds__(kPpThreads, 1) void mx256_kernel(mok_mx_args a, bool vec, int nr, int nc, int splits) {
   using X = MxPp<A8>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[X::kLds];
-  const int t = dense_index((int64_t)nr * nc);
-  if (t < 0) return;
+  const int tiles = nr * nc, ix = dense_index((int64_t)tiles * splits);
+  if (ix < 0) return;
+  const int split = SPLIT ? ix / tiles : 0, t = SPLIT ? ix % tiles : ix;
   int row, col;
   dense_tile(t, nr, nc, 4, row, col);
+  const int ns = (a.K + X::SK - 1) / X::SK;
+  const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
+  const int j1 = SPLIT ? (int)((int64_t)ns * (split + 1) / splits) : ns;
   const int m0 = row * 256, n0 = col * (GLU ? 128 : 256), nrows = min(256, a.M - m0);
   Acc<4, 2> acc;
   const int g = pp_group();
   mx_pp_loop<A8, GLU>(lds, mx_copy_a<A8>(a, m0 + 128 * g), mx_copy_b<A8, GLU>(a, n0 + mx_cols<GLU>() * g),
-                      mx_copy_s16<GLU>(a, m0, n0), a.K, acc);
-  if constexpr (GLU) {
+                      mx_copy_s16<GLU>(a, m0, n0), a.K, j0, j1, acc);
+  if constexpr (SPLIT) {
+    pp_store32(lds, acc, nrows, a.part + ((int64_t)split * tiles + t) * 65536);
+  } else if constexpr (GLU) {
     // a lane holds 16 of the 32 columns of a block of h, lane l ^ 32 the others. Codes go
     // through LDS (128 bytes a row, 16-byte chunk c of row r at c ^ (r & 7))
 #pragma unroll
@@ -710,15 +698,18 @@ hipError_t launch_few(const mok_mx_args& a, hipStream_t st) {
 struct Plan {
   int tile, nr, nc, splits;                      // tile 0: few rows
 };
+// (slots of 128, of 256)
+constexpr dense_cost kCost8 = {7.7f, 1.62f, 8.3f, 1.39f, 0.4f, 3.9f, 4.9e6f};
+constexpr dense_cost kCost4 = {11.7f, 1.70f, 10.0f, 1.21f, 0.57f, 2.4f, 2.9e6f};
+
 Plan plan_of(const mok_mx_args& a, bool glu) {
   if (mok_mx_few(a.M)) return Plan{0, 0, 0, 1};
-  const auto rows = [&](int t) { return (a.M + t - 1) / t; };
-  const auto cols = [&](int t) { return ((glu ? 2 : 1) * (int64_t)a.N + t - 1) / t; };
-  if (rows(256) * cols(256) >= 256) return Plan{256, rows(256), (int)cols(256), 1};
-  const int64_t n = rows(128) * cols(128), slots = a.K / (a.a8 ? 128 : 256);
-  int64_t sp = n > 0 ? 512 / n : 1;
-  sp = sp < slots / 4 ? sp : slots / 4;
-  return Plan{128, rows(128), (int)cols(128), sp < 1 ? 1 : (int)sp};
+  Plan p;
+  const int64_t cols = (glu ? 2 : 1) * (int64_t)a.N;
+  dense_plan(a.M, cols, 1, a.K / (a.a8 ? 128 : 256), a.a8 ? kCost8 : kCost4, &p.tile, &p.splits);
+  p.nr = (a.M + p.tile - 1) / p.tile;
+  p.nc = (int)((cols + p.tile - 1) / p.tile);
+  return p;
 }
 
 template <bool A8, bool GLU, int ACT>
@@ -727,17 +718,26 @@ hipError_t launch(const mok_mx_args& a, const Plan& p, hipStream_t st) {
   if (tiles * p.splits > (1 << 30)) return hipErrorInvalidValue;
   if (tiles == 0) return hipSuccess;
   const bool vec = a.ldd % 8 == 0 && ((uintptr_t)a.d | (uintptr_t)a.res) % 16 == 0;
-  const dim3 grid(dense_grid(tiles * p.splits)), block(kThreads);
-  if (p.tile == 256) {
-    if (!GLU && a.res) hipLaunchKernelGGL((mx256_kernel<A8, GLU, GLU ? ACT : 1>), grid, dim3(kPpThreads), 0, st, a, vec, p.nr, p.nc);
-    else hipLaunchKernelGGL((mx256_kernel<A8, GLU, ACT>), grid, dim3(kPpThreads), 0, st, a, vec, p.nr, p.nc);
-  } else if (p.splits == 1) {
-    hipLaunchKernelGGL((mx128_kernel<A8, GLU, ACT, false>), grid, block, 0, st, a, vec, p.nr, p.nc, 1);
+  const dim3 grid(dense_grid(tiles * p.splits)), block(p.tile == 256 ? kPpThreads : kThreads);
+  const int nr = p.nr, nc = p.nc;
+  if (p.splits > 1) {
+    if (p.tile == 256)
+      hipLaunchKernelGGL((mx256_kernel<A8, GLU, 0, true>), grid, block, 0, st, a, vec, nr, nc, p.splits);
+    else
+      hipLaunchKernelGGL((mx128_kernel<A8, GLU, 0, true>), grid, block, 0, st, a, vec, nr, nc, p.splits);
+    const int ch = p.tile * (GLU ? p.tile / 2 : p.tile) / 8;
+    const dim3 jgrid((ch + kThreads - 1) / kThreads, (unsigned)tiles);
+    if (p.tile == 256)
+      hipLaunchKernelGGL((mx_join_kernel<GLU, ACT, 256>), jgrid, dim3(kThreads), 0, st, a, vec, nr, nc, p.splits);
+    else
+      hipLaunchKernelGGL((mx_join_kernel<GLU, ACT, 128>), jgrid, dim3(kThreads), 0, st, a, vec, nr, nc, p.splits);
+  } else if (p.tile == 256) {
+    if (!GLU && a.res)
+      hipLaunchKernelGGL((mx256_kernel<A8, GLU, GLU ? ACT : 1, false>), grid, block, 0, st, a, vec, nr, nc, 1);
+    else
+      hipLaunchKernelGGL((mx256_kernel<A8, GLU, ACT, false>), grid, block, 0, st, a, vec, nr, nc, 1);
   } else {
-    hipLaunchKernelGGL((mx128_kernel<A8, GLU, ACT, true>), grid, block, 0, st, a, vec, p.nr, p.nc, p.splits);
-    const int ch = 128 * (GLU ? 2 : 16);
-    hipLaunchKernelGGL((mx_join_kernel<GLU, ACT>), dim3(ch / kThreads, (unsigned)tiles), block, 0, st, a, vec, p.nr,
-                       p.nc, p.splits);
+    hipLaunchKernelGGL((mx128_kernel<A8, GLU, ACT, false>), grid, block, 0, st, a, vec, nr, nc, 1);
   }
   return hipGetLastError();
 }
@@ -781,7 +781,7 @@ hipError_t mok_launch_mxfp8_rows(const void* src, bool f32, int64_t ld, int64_t 
 
 size_t mok_mx_part_bytes(const mok_mx_args& a, bool glu) {
   const Plan p = plan_of(a, glu);
-  return p.splits > 1 ? (size_t)p.splits * p.nr * p.nc * 65536 : 0;
+  return p.splits > 1 ? (size_t)p.splits * p.nr * p.nc * p.tile * p.tile * 4 : 0;
 }
 
 bool mok_mx_few(int M) { return M <= kMxFewRows; }
