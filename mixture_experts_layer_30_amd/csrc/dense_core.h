@@ -501,8 +501,8 @@ MOK_DEV void dense_tile(int i, int nr, int nc, int grp, int& row, int& col) {
 // Tile and split of a product of M x N (x batch) over `slots` slots of K: the least
 // estimated time. A pass of 256 workgroups of 256 x 256 tiles (one a CU), or of 512 of
 // 128 x 128 (two a CU), takes a fixed part (launch, first copies, epilogue) and a part
-// per slot, of which a 128 x 128 tile with a CU to itself needs the share `alone`;
-// partial sums add a launch and the traffic of writing and reading them. With the
+// per slot, of which a 128 x 128 tile with a CU to itself needs the share `alone`; all
+// slots take at least as long as reading the operands; partial sums add a launch and the traffic of writing and reading them. With the
 // constants fitted to 280 shapes of 65 to 8192 rows, each timed with both tiles and up
 // to 8 splits, the choice was within 1% of the fastest in the mean and 20% at worst.
 struct dense_cost {
@@ -510,6 +510,7 @@ struct dense_cost {
   float join, rate;                              // us, bytes per us
 };
 inline float dense_plan(int64_t M, int64_t N, int batch, int64_t slots, const dense_cost& c, int* tile, int* splits) {
+  const float read = (float)(M + N * batch) * slots * 128 / 4.6e6f;   // the operands once, 4.6 TB/s
   float best = 0.f;
   *tile = 128;
   *splits = 1;
@@ -517,8 +518,8 @@ inline float dense_plan(int64_t M, int64_t N, int batch, int64_t slots, const de
     const int64_t n = ((M + ts - 1) / ts) * ((N + ts - 1) / ts) * batch, fill = ts == 256 ? 256 : 512;
     for (int64_t s = 1; s == 1 || (n * s <= fill && slots >= 4 * s); ++s) {
       const int64_t passes = (n * s + fill - 1) / fill, per = (slots + s - 1) / s;
-      float t = ts == 256 ? passes * (c.fix256 + per * c.slot256)
-                          : passes * c.fix128 + per * c.slot128 * (n * s <= 256 ? c.alone : (float)passes);
+      float t = ts == 256 ? passes * per * c.slot256 : per * c.slot128 * (n * s <= 256 ? c.alone : (float)passes);
+      t = passes * (ts == 256 ? c.fix256 : c.fix128) + (t > read ? t : read);
       if (s > 1) t += c.join + (float)s * M * N * batch * 8 / c.rate;
       if (best == 0.f || t < best) {
         best = t;
