@@ -268,3 +268,62 @@ def test_binding_refuses():
     refused(ctx=torch.empty((T, I), dtype=torch.bfloat16, device="cuda"))
     refused(w=(w[0], w[1], w[2].t()))
     refused(w=w[:2])
+
+
+def test_offsets_past_32_bits():
+    """Two billion elements of x, y, dy and dx: the last tokens' outputs and the weight gradients, whose sums run
+    over all tokens."""
+    import torch
+    T, H, I = 1_100_003, 2048, 16
+    assert T * H > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    dy = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    w = tuple((torch.randn(s, generator=g, device="cuda") * s[1] ** -0.5).bfloat16() for s in ((I, H), (I, H), (H, I)))
+    ws = F.get_ffn_workspace(T, H, I)
+    y = F.run_ffn_forward(ws, x, w)
+    dx, dwg, dwu, dwd = F.run_ffn_backward(ws, x, w, dy)
+    torch.cuda.synchronize()
+    t = slice(T - 300, T)
+    c = [f64(v) for v in (x[t], *w, dy[t])]
+    r = do.ffn_forward(*c[:4], "silu")
+    assert_within(f64(y[t]), r["y"], forward_bounds(r, *c[:4], "silu")["y"], "y")
+    a, b = f64(ws.ctx[t])[:, :I], f64(ws.ctx[t])[:, I:]
+    r = do.ffn_backward(c[0], a, b, *c[1:], "silu")
+    assert_within(f64(dx[t]), r["dx"], backward_bounds(r, c[0], a, b, *c[1:], "silu")["dx"], "dx")
+    # the sums over all tokens in double, by chunks, with their magnitudes for the bound: h, da, db are
+    # rounded to bf16 (2^-8) after the gate (2^-15 of terms up to 1 + |a| / 4 of |dh b|), T terms in fp32
+    ref = {k: torch.zeros(s, dtype=torch.float64, device="cuda") for k, s in
+           (("dwg", (I, H)), ("dwu", (I, H)), ("dwd", (H, I)))}
+    mag = {k: v.clone() for k, v in ref.items()}
+    wd = w[2].double()
+    for k in range(0, T, 1 << 17):
+        q = slice(k, min(T, k + (1 << 17)))
+        xc, dc, ab = x[q].double(), dy[q].double(), ws.ctx[q].double()
+        a, b = ab[:, :I], ab[:, I:]
+        s = torch.sigmoid(a)
+        dh = dc @ wd
+        da, db, h = dh * b * s * (1 + a * (1 - s)), dh * a * s, a * s * b
+        for n, u, v, loose in (("dwg", da, xc, (dh * b).abs() * (1 + a.abs())), ("dwu", db, xc, db.abs()),
+                               ("dwd", dc, h, None)):
+            ref[n] += u.t() @ v
+            mag[n] += (u.abs() + (2.0 ** -7 * loose if loose is not None else 0)).t() @ v.abs()
+    for n, t in (("dwg", dwg), ("dwu", dwu), ("dwd", dwd)):
+        allowed = (2.0 ** -7 + (T + 8) * 2.0 ** -24) * mag[n] + 2.0 ** -8 * ref[n].abs()
+        assert bool(((t.double() - ref[n]).abs() <= allowed).all()), n
+        # and far closer in the mean: errors of either sign over a million tokens
+        assert float((t.double() - ref[n]).norm() / ref[n].norm()) < 2.0 ** -7, n
+
+
+def test_another_current_device_is_not_touched():
+    """The call runs on its tensors' device; tensors of two devices are refused (needs two GPUs to say more)."""
+    import torch
+    T, H, I = 4, 256, 128
+    ws = F.get_ffn_workspace(T, H, I)
+    c = {k: bf(v) for k, v in case(T, H, I).items()}
+    before = torch.cuda.current_device()
+    F.run_ffn_forward(ws, c["x"], (c["wg"], c["wu"], c["wd"]))
+    assert torch.cuda.current_device() == before
+    with pytest.raises(mok.MokError):
+        mok.ffn_forward(ws.problem, c["x"], (c["wg"], c["wu"], c["wd"]), torch.empty_like(c["x"]),
+                        ws.workspace.cpu())

@@ -274,3 +274,37 @@ def test_4bit_chain_in_a_graph(T):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((y, q, s, out), want)), k
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 512, 1024), (150, 512, 1024), (4100, 4100, 256)])
+def test_mxfp8_rows_times_mxfp4_weights(M, N, K):
+    """The layer's own MXFP8 quantizer on the activations, the 4-bit one on the weights, and their product."""
+    import torch
+    g = np.random.default_rng(M)
+    x = bf(g.normal(size=(M, K)) * np.exp2(g.integers(-3, 4, size=K)))
+    w = bf(g.normal(size=(N, K)) * K ** -0.5)
+    q = torch.empty((M, K), dtype=torch.uint8, device="cuda")
+    s = torch.empty((M, K // 32), dtype=torch.uint8, device="cuda")
+    mok.mxfp8_quantize(x, q, s)
+    qw, sw = F.mxfp4_quantize(w)
+    d = F.run_mx_matmul(F.get_mx_matmul_workspace(M, N, K, mok.MOK_MXFP8), q, s, qw, sw)
+    torch.cuda.synchronize()
+    av, bv = do.mxfp8_round(f64(x)), do.mxfp4_values(qw.cpu().numpy(), sw.cpu().numpy())
+    ref, e = av @ bv.T, mx_dot(av, bv, True)
+    assert_within(f64(d), ref, e + HALF * (np.abs(ref) + e) + 1e-38, "d")
+
+
+def test_calls_are_traced():
+    """The launches of these calls appear in the tracer under their names."""
+    import torch
+    x = torch.randn((40, 256), device="cuda").bfloat16()
+    w = F.quantize_ffn_weights_mxfp4(*(torch.randn((256, 256), device="cuda").bfloat16() for _ in range(3)))
+    ws = F.get_ffn_workspace(40, 256, 256, dtype=mok.MOK_MXFP4, training=False)
+    mok.trace_enable(True)
+    try:
+        F.run_ffn_forward(ws, x, w)
+        F.mxfp4_dequantize(*F.mxfp4_quantize(x))
+        seen = mok.trace_collect()
+    finally:
+        mok.trace_enable(False)
+    assert set(seen) == {"ffn_quantize_x", "ffn_gateup_mxfp4", "ffn_down_mxfp4", "mxfp4_quantize", "mxfp4_dequantize"}
