@@ -244,8 +244,7 @@ def forward_fused(problem, topk_ids, schedule, x, topk_w, weights, y, workspace,
                                    schedule.numel() * schedule.element_size(), _ptr(x), _ptr(topk_w),
                                    ctypes.byref(w), _ptr(y), _ptr(fwd_ctx), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(), _stream(stream)),
-           "mok_forward_fused", "mok_mxfp4_quantize", "mok_mxfp4_dequantize", "mok_mx_matmul_workspace",
-           "mok_mx_matmul", "mok_ffn_buffer_sizes", "mok_ffn_forward", "mok_ffn_backward")
+           "mok_forward_fused")
 
 
 def backward(problem, schedule, fwd_ctx, x, topk_w, weights, dy, dx, dw_gate, dw_up, dw_down,
