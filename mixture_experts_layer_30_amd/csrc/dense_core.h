@@ -1,7 +1,6 @@
 // Tile machinery of the dense products (k_ffn.hip, k_mx.hip): operand copies
-// for matrices that no schedule gathers, with tails in K, a 128 x 128 tile and
-// row epilogues. The 256 x 256 bf16 tile runs the main loop of gemm_core.h on
-// the copies defined here.
+// for matrices that no schedule gathers, with tails in K, main loops of 128 x 128
+// and 256 x 256 tiles, products of few rows, the choice among them, and the gates.
 //
 // LDS slots hold 64 bf16 (128 MX elements) of K per row. The layouts are those
 // of gemm_core.h: 128-byte rows [rows][128 B] for K-contiguous operands,
@@ -161,59 +160,103 @@ struct CopyT {
 };
 
 // ------------------------------------------------------------------ 128 x 128 tile
-// Four wavefronts of 64 x 64 (2 x 2 fragments of 32 x 32). Two slots of 32 KiB
-// leave room for two workgroups on a CU, each multiplying while the other waits.
+// Four wavefronts of 64 x 64 (2 x 2 fragments of 32 x 32), and two ways to fill a CU:
+//  S = 2: two slots of LDS and two workgroups a CU, each multiplying while the other
+//         waits; for more than 256 tiles (with S = 4 those take 10% longer, mean of 200).
+//  S = 4: one workgroup a CU, with four more wavefronts that only copy, three slots
+//         ahead. A wavefront that copies waits for the address unit, and the multiplying
+//         ones then do not: a bf16 slot takes 0.58 us, with four wavefronts doing both
+//         and two slots 0.83 us, and with four slots 0.95 us.
 using G128 = Geo<128, 128, 2, 2>;
 constexpr int kPitch128 = 128 * 4 + 16;          // fp32 staging of the tile
-constexpr int kLds128 = 128 * kPitch128;         // 67584 B, above the two slots' 65536 B
+constexpr int kLds128 = 128 * kPitch128;         // 67584 B, above two slots' 65536 B
+template <int S>
+constexpr int kThreads128 = S == 2 ? 256 : 512;
+template <int S, int SLOT>
+constexpr int lds128() { return S * SLOT > kLds128 ? S * SLOT : kLds128; }
 
-// bf16 product over slots [j0, j1)
-template <class LA, class LB>
-MOK_DEV void loop128(uint8_t* lds, const LA& la, const LB& lb, int j0, int j1, Acc<2, 2>& acc) {
-  constexpr int kSlot = 32768, kB = 16384, kD = LA::kDma + LB::kDma;
-  const uint32_t base = lds_addr(lds);
-  acc.zero();
-  const auto issue = [&](int j, int s) {
-    la.dma(j, base + s * kSlot);
-    lb.dma(j, base + s * kSlot + kB);
-  };
-  if (j0 < j1) issue(j0, 0);
-  if (j0 + 1 < j1) issue(j0 + 1, 1);
-  for (int j = j0; j < j1; ++j) {
-    const int s = (j - j0) & 1;
-    if (j + 1 < j1) wait_vm_lds<kD>();
-    else wait_vm_lds<0>();
+// slots [j0, j1): issue(j, buffer) starts a wavefront's kD copies of slot j, compute(buffer)
+// multiplies (S = 4: wavefronts 0 to 3)
+template <int S, int kD, class Issue, class Compute>
+MOK_DEV void ring128(int j0, int j1, Issue&& issue, Compute&& compute) {
+  if constexpr (S == 2) {
+    if (j0 < j1) issue(j0, 0);
+    if (j0 + 1 < j1) issue(j0 + 1, 1);
+    for (int j = j0; j < j1; ++j) {
+      const int s = (j - j0) & 1;
+      if (j + 1 < j1) wait_vm_lds<kD>();
+      else wait_vm_lds<0>();
+      barrier_lds();
+      compute(s);
+      barrier_lds_only();
+      if (j + 2 < j1) issue(j + 2, s);
+    }
+  } else if (wave_id() >= 4) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (j0 + k < j1) issue(j0 + k, k);
+    for (int j = j0; j < j1; ++j) {
+      // slot j has arrived when at most the two slots after it are outstanding; behind the
+      // barrier everyone is done with slot j - 1, whose buffer slot j + 3 takes
+      if (j + 2 < j1) wait_vm_lds<2 * kD>();
+      else wait_vm_lds<0>();
+      barrier_lds();
+      if (j + 3 < j1) issue(j + 3, (j - j0 + 3) & 3);
+    }
     barrier_lds();
-    const uint8_t* ta = lds + s * kSlot;
-    const uint8_t* tb = ta + kB;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      bf16x8_t a[2], b[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        a[i] = LA::frag(ta, G128::wm() * 64 + 32 * i, ks >> 1, ks & 1);
-        b[i] = LB::frag(tb, G128::wn() * 64 + 32 * i, ks >> 1, ks & 1);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-          acc.c[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[n], acc.c[i][n], 0, 0, 0);
+  } else {
+    for (int j = j0; j < j1; ++j) {
+      barrier_lds_only();                        // (with the reads of slot j - 1 complete)
+      compute((j - j0) & 3);
     }
     barrier_lds_only();
-    if (j + 2 < j1) issue(j + 2, s);
   }
 }
 
+// bf16 product over slots [j0, j1)
+template <int S, class LA, class LB>
+MOK_DEV void loop128(uint8_t* lds, const LA& la, const LB& lb, int j0, int j1, Acc<2, 2>& acc) {
+  constexpr int kSlot = 32768, kB = 16384;
+  const uint32_t base = lds_addr(lds);
+  acc.zero();
+  ring128<S, LA::kDma + LB::kDma>(
+      j0, j1,
+      [&](int j, int s) {
+        la.dma(j, base + s * kSlot);
+        lb.dma(j, base + s * kSlot + kB);
+      },
+      [&](int s) {
+        const uint8_t* ta = lds + s * kSlot;
+        const uint8_t* tb = ta + kB;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          bf16x8_t a[2], b[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            a[i] = LA::frag(ta, G128::wm() * 64 + 32 * i, ks >> 1, ks & 1);
+            b[i] = LB::frag(tb, G128::wn() * 64 + 32 * i, ks >> 1, ks & 1);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              acc.c[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[n], acc.c[i][n], 0, 0, 0);
+        }
+      });
+}
+
 // stage the fp32 tile in LDS (the slots are free: every loop ends in a barrier)
+template <int S>
 MOK_DEV void stage128(uint8_t* lds, const Acc<2, 2>& acc) {
+  if (S == 2 || wave_id() < 4) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int q = 0; q < 16; ++q)
-        *reinterpret_cast<float*>(lds + G128::row(i, q) * kPitch128 + G128::col(n) * 4) = acc.c[i][n][q];
+        for (int q = 0; q < 16; ++q)
+          *reinterpret_cast<float*>(lds + G128::row(i, q) * kPitch128 + G128::col(n) * 4) = acc.c[i][n][q];
+  }
   barrier_lds_only();
 }
 
@@ -247,7 +290,9 @@ MOK_DEV void stage128(uint8_t* lds, const Acc<2, 2>& acc) {
 // than a slot, and no time goes into the waits. The last reads of slot s are complete
 // before the barrier of 4s+3, B of s+2 is written over them from 4s+4 on, A of s+3 from
 // 4s+6 on. (Copies between the matrix instructions of the multiplying group were 13 to
-// 40% slower, all of B in interval 4s TODO, two slots of each operand 5%.)
+// 40% slower, all of B in interval 4s and two slots of each operand 5% each.) A down
+// product of 4096 x 4096 x 8192 takes 203 us (1352 TFLOP/s; the library's 200 us). Bound
+// by power: the same matrix instructions alone, on random data, sustain 1801 TFLOP/s.
 constexpr int kPpThreads = 512;
 constexpr int kPpHalf = 16384;
 constexpr int kPpLds = 10 * kPpHalf;             // 160 KiB: 3 + 3 half slots of A, 2 + 2 of B
@@ -503,7 +548,7 @@ MOK_DEV void dense_tile(int i, int nr, int nc, int grp, int& row, int& col) {
 // 128 x 128 (two a CU), takes a fixed part (launch, first copies, epilogue) and a part
 // per slot, of which a 128 x 128 tile with a CU to itself needs the share `alone`; all
 // slots take at least as long as reading the operands; partial sums add a launch and the traffic of writing and reading them. With the
-// constants fitted to 280 shapes of 65 to 8192 rows, each timed with both tiles and up
+// constants fitted to 280 shapes of 33 to 8192 rows, each timed with both tiles and up
 // to 8 splits, the choice was within 1% of the fastest in the mean and 20% at worst.
 struct dense_cost {
   float fix256, slot256, fix128, slot128, alone; // us

@@ -111,11 +111,11 @@ template <int OP>
 MOK_DEV int acc_col(int c) { return OP == FFN_GATEUP ? (c >> 5) * 64 + (c & 31) : c; }
 
 // rows [0, nrows) of fp32 staging at pitch P -> finish8; row0/col0 of the tile
-template <int OP, int ACT>
+template <int OP, int ACT, int THREADS>
 MOK_DEV void finish_rows(const mok_ffn_args& a, const uint8_t* st, int pitch, int nrows, int row0, int col0,
                          int half) {
   constexpr int CH = out_cols<OP, 128>() / 8;
-  for (int idx = threadIdx.x; idx < nrows * CH; idx += kThreads) {
+  for (int idx = threadIdx.x; idx < nrows * CH; idx += THREADS) {
     const int r = idx / CH, c = (idx % CH) * 8;
     const uint8_t* p = st + r * pitch + acc_col<OP>(c) * 4;
     float v[8], w[8];
@@ -165,10 +165,10 @@ MOK_DEV auto copy_b(const mok_ffn_args& a, int n0) {
   }
 }
 
-template <int OP, int ACT, bool SPLIT>
-__global__ __launch_bounds__(kThreads, 2) void ffn128_kernel(mok_ffn_args a, int M, int K, int nr, int nc,
-                                                             int batch, int splits) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds128];
+template <int OP, int ACT, bool SPLIT, int S>
+__global__ __launch_bounds__(kThreads128<S>, S == 2 ? 2 : 1) void ffn128_kernel(mok_ffn_args a, int M, int K, int nr,
+                                                                                int nc, int batch, int splits) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[lds128<S, 32768>()];
   const int tiles = nr * nc * batch;
   const int i = dense_index((int64_t)tiles * splits);
   if (i < 0) return;
@@ -180,17 +180,17 @@ __global__ __launch_bounds__(kThreads, 2) void ffn128_kernel(mok_ffn_args a, int
   const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
   const int j1 = SPLIT ? (int)((int64_t)ns * (split + 1) / splits) : ns;
   Acc<2, 2> acc;
-  loop128(lds, copy_a<OP>(a, m0, half), copy_b<OP>(a, n0), j0, j1, acc);
-  stage128(lds, acc);
+  loop128<S>(lds, copy_a<OP>(a, m0, half), copy_b<OP>(a, n0), j0, j1, acc);
+  stage128<S>(lds, acc);
   const int nrows = min(128, M - m0);
   if constexpr (SPLIT) {
     // partial tile (split, t): 128 rows of 128 fp32
     float* p = a.part + ((int64_t)split * tiles + t) * 16384;
-    for (int idx = threadIdx.x; idx < nrows * 32; idx += kThreads)
+    for (int idx = threadIdx.x; idx < nrows * 32; idx += kThreads128<S>)
       reinterpret_cast<float4*>(p)[idx] =
           *reinterpret_cast<const float4*>(lds + (idx >> 5) * kPitch128 + (idx & 31) * 16);
   } else {
-    finish_rows<OP, ACT>(a, lds, kPitch128, nrows, m0, n0, half);
+    finish_rows<OP, ACT, kThreads128<S>>(a, lds, kPitch128, nrows, m0, n0, half);
   }
 }
 
@@ -432,7 +432,7 @@ struct Plan {
 };
 
 // (slots of 64)
-constexpr dense_cost kCost = {14.2f, 1.06f, 3.7f, 1.09f, 0.76f, 3.9f, 3.6e6f};
+constexpr dense_cost kCost = {13.0f, 2.11f, 2.2f, 1.62f, 0.36f, 3.5f, 2.65e6f};
 
 Plan plan_of(const mok_ffn_args& a, mok_ffn_op op) {
   Plan p;
@@ -455,13 +455,15 @@ hipError_t launch(const mok_ffn_args& a, const Plan& p, hipStream_t st) {
   const int64_t tiles = (int64_t)p.nr * p.nc * p.s.batch;
   if (tiles * p.splits > (1 << 30)) return hipErrorInvalidValue;
   if (tiles == 0) return hipSuccess;
-  const dim3 grid(dense_grid(tiles * p.splits)), block(p.tile == 256 ? kPpThreads : kThreads);
+  const dim3 grid(dense_grid(tiles * p.splits)), block(p.tile == 256 || tiles * p.splits <= 256 ? 512 : 256);
   const int nr = p.nr, nc = p.nc, nb = p.s.batch;
   if (p.splits > 1) {
     if (p.tile == 256)
       hipLaunchKernelGGL((ffn256_kernel<OP, 0, true>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, p.splits);
+    else if (tiles * p.splits <= 256)
+      hipLaunchKernelGGL((ffn128_kernel<OP, 0, true, 4>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, p.splits);
     else
-      hipLaunchKernelGGL((ffn128_kernel<OP, 0, true>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, p.splits);
+      hipLaunchKernelGGL((ffn128_kernel<OP, 0, true, 2>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, p.splits);
     const int ch = p.tile * (OP == FFN_GATEUP ? p.tile / 2 : p.tile) / 8;
     const dim3 jgrid((ch + kThreads - 1) / kThreads, (unsigned)tiles);
     if (p.tile == 256)
@@ -474,8 +476,10 @@ hipError_t launch(const mok_ffn_args& a, const Plan& p, hipStream_t st) {
                          nc, nb, 1);
     else
       hipLaunchKernelGGL((ffn256_kernel<OP, ACT, false>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, 1);
+  } else if (tiles <= 256) {
+    hipLaunchKernelGGL((ffn128_kernel<OP, ACT, false, 4>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, 1);
   } else {
-    hipLaunchKernelGGL((ffn128_kernel<OP, ACT, false>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, 1);
+    hipLaunchKernelGGL((ffn128_kernel<OP, ACT, false, 2>), grid, block, 0, st, a, p.s.M, p.s.K, nr, nc, nb, 1);
   }
   return hipGetLastError();
 }

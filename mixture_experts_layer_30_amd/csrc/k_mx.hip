@@ -39,8 +39,8 @@ MOK_DEV uint32_t block_max_bits(const float v[8]) {
 // saturating, sign kept): equal to the definition on gfx950 for every bf16 value at every
 // scale. A block that holds a NaN or an infinity, which the format cannot, gets the NaN
 // scale 255: it reads back, and multiplies, as NaN.
-// Bound by memory: 16384 x 7168 in TODO us; seven comparisons per element in place
-// of the conversion took 80 us.
+// Bound by memory: 16384 x 7168 in 58 us (5.1 TB/s); seven comparisons per element in
+// place of the conversion took 80 us.
 __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const bf16_t* __restrict__ src, int64_t n8,
                                                             uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
   typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
@@ -65,7 +65,8 @@ __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const bf16_t* __res
   if ((idx & 3) == 0) scales[idx >> 2] = (uint8_t)sc;
 }
 
-// code * 2^(s-127), exact in bf16 (v_cvt_scalef32_pk_bf16_fp4); 16384 x 7168 in TODO us
+// code * 2^(s-127), exact in bf16 (v_cvt_scalef32_pk_bf16_fp4); 16384 x 7168 in 52 us
+// (5.7 TB/s)
 __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __restrict__ q,
                                                               const uint8_t* __restrict__ scales, int64_t n8,
                                                               bf16_t* __restrict__ dst) {
@@ -115,7 +116,6 @@ struct MxTile {
   static constexpr int RBA = 128, RBB = SK / 2;
   static constexpr int kA = 128 * RBA, kB = 128 * RBB, kS = SK / 128 * 1024;
   static constexpr int kSlot = kA + kB + kS;
-  static constexpr int kLds = 2 * kSlot > kLds128 ? 2 * kSlot : kLds128;
 };
 
 // Scale words (four blocks of 32, one word per 128 of K) of 64 rows: lane l copies those
@@ -145,25 +145,18 @@ MOK_DEV int scale_at(int r) {
   return GLU ? (r & ~127) | ((r >> 5) & 1) << 6 | ((r >> 6) & 1) << 5 | (r & 31) : r;
 }
 
-template <bool A8, bool GLU, class LA, class LB, class LS>
+template <bool A8, bool GLU, int S, class LA, class LB, class LS>
 MOK_DEV void mx_loop128(uint8_t* lds, const LA& la, const LB& lb, const LS& ls, int j0, int j1, Acc<2, 2>& acc) {
   using X = MxTile<A8>;
-  constexpr int kD = LA::kDma + LB::kDma + LS::kDma;
   const uint32_t base = lds_addr(lds);
   const int l = lane_id(), lr = l & 31, hl = l >> 5;
   acc.zero();
   const auto issue = [&](int j, int s) {
     la.dma(j, base + s * X::kSlot);
     lb.dma(j, base + s * X::kSlot + X::kA);
-    ls.dma(j, base + s * X::kSlot + X::kA + X::kB + wave_id() * 256, 1024);
+    ls.dma(j, base + s * X::kSlot + X::kA + X::kB + copy_wave() * 256, 1024);
   };
-  if (j0 < j1) issue(j0, 0);
-  if (j0 + 1 < j1) issue(j0 + 1, 1);
-  for (int j = j0; j < j1; ++j) {
-    const int s = (j - j0) & 1;
-    if (j + 1 < j1) wait_vm_lds<kD>();
-    else wait_vm_lds<0>();
-    barrier_lds();
+  ring128<S, LA::kDma + LB::kDma + LS::kDma>(j0, j1, issue, [&](int s) {
     const uint8_t* ta = lds + s * X::kSlot;
     const uint8_t* tb = ta + X::kA;
     const uint32_t* sc = reinterpret_cast<const uint32_t*>(tb + X::kB);
@@ -198,9 +191,7 @@ MOK_DEV void mx_loop128(uint8_t* lds, const LA& la, const LB& lb, const LS& ls, 
           acc.c[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[i], b[n], acc.c[i][n], A8 ? 0 : 4, 4, 0,
                                                                         as[i], 0, bs[n]);
     }
-    barrier_lds_only();
-    if (j + 2 < j1) issue(j + 2, s);
-  }
+  });
 }
 
 // ------------------------------------------------------------------ epilogues
@@ -297,10 +288,11 @@ MOK_DEV auto mx_copy_s16(const mok_mx_args& a, int m0, int n0) {
   return CopyScales16((GLU && (c & 1) ? a.sb2 : a.sb) + n0 * ks, a.N - n0, a.K);
 }
 
-template <bool A8, bool GLU, int ACT, bool SPLIT>
-__global__ __launch_bounds__(kThreads, 2) void mx128_kernel(mok_mx_args a, bool vec, int nr, int nc, int splits) {
+template <bool A8, bool GLU, int ACT, bool SPLIT, int S>
+__global__ __launch_bounds__(kThreads128<S>, S == 2 ? 2 : 1) void mx128_kernel(mok_mx_args a, bool vec, int nr,
+                                                                               int nc, int splits) {
   using X = MxTile<A8>;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[X::kLds];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[lds128<S, X::kSlot>()];
   const int tiles = nr * nc, i = dense_index((int64_t)tiles * splits);
   if (i < 0) return;
   const int split = SPLIT ? i / tiles : 0, t = SPLIT ? i % tiles : i;
@@ -311,15 +303,16 @@ __global__ __launch_bounds__(kThreads, 2) void mx128_kernel(mok_mx_args a, bool 
   const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
   const int j1 = SPLIT ? (int)((int64_t)ns * (split + 1) / splits) : ns;
   Acc<2, 2> acc;
-  mx_loop128<A8, GLU>(lds, mx_copy_a<A8>(a, m0), mx_copy_b<A8, GLU>(a, n0), mx_copy_s<A8, GLU>(a, m0, n0), j0, j1, acc);
-  stage128(lds, acc);
+  mx_loop128<A8, GLU, S>(lds, mx_copy_a<A8>(a, m0), mx_copy_b<A8, GLU>(a, n0), mx_copy_s<A8, GLU>(a, m0, n0), j0, j1,
+                         acc);
+  stage128<S>(lds, acc);
   if constexpr (SPLIT) {
     float* p = a.part + ((int64_t)split * tiles + t) * 16384;
-    for (int idx = threadIdx.x; idx < nrows * 32; idx += kThreads)
+    for (int idx = threadIdx.x; idx < nrows * 32; idx += kThreads128<S>)
       reinterpret_cast<float4*>(p)[idx] =
           *reinterpret_cast<const float4*>(lds + (idx >> 5) * kPitch128 + (idx & 31) * 16);
   } else if constexpr (GLU) {
-    for (int idx = threadIdx.x; idx < nrows * 8; idx += kThreads) {
+    for (int idx = threadIdx.x; idx < nrows * 8; idx += kThreads128<S>) {
       const int r = idx >> 3, c = (idx & 7) * 8;
       if (n0 + c >= a.N) continue;               // (N a multiple of 128: whole blocks)
       float g[8], u[8];
@@ -329,7 +322,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx128_kernel(mok_mx_args a, bool 
       mx_gate8<ACT>(a, m0 + r, n0 + c, g, u);
     }
   } else {
-    for (int idx = threadIdx.x; idx < nrows * 16; idx += kThreads) {
+    for (int idx = threadIdx.x; idx < nrows * 16; idx += kThreads128<S>) {
       const int r = idx >> 4, c = (idx & 15) * 8;
       float v[8];
       load_f32<8>(lds + r * kPitch128 + c * 4, v);
@@ -699,8 +692,8 @@ struct Plan {
   int tile, nr, nc, splits;                      // tile 0: few rows
 };
 // (slots of 128, of 256)
-constexpr dense_cost kCost8 = {7.7f, 1.62f, 8.3f, 1.39f, 0.4f, 3.9f, 4.9e6f};
-constexpr dense_cost kCost4 = {11.7f, 1.70f, 10.0f, 1.21f, 0.57f, 2.4f, 2.9e6f};
+constexpr dense_cost kCost8 = {10.1f, 1.80f, 10.5f, 1.36f, 0.28f, 3.5f, 6.7e6f};
+constexpr dense_cost kCost4 = {17.3f, 1.85f, 8.7f, 1.25f, 0.31f, 2.2f, 2.8e6f};
 
 Plan plan_of(const mok_mx_args& a, bool glu) {
   if (mok_mx_few(a.M)) return Plan{0, 0, 0, 1};
@@ -718,13 +711,15 @@ hipError_t launch(const mok_mx_args& a, const Plan& p, hipStream_t st) {
   if (tiles * p.splits > (1 << 30)) return hipErrorInvalidValue;
   if (tiles == 0) return hipSuccess;
   const bool vec = a.ldd % 8 == 0 && ((uintptr_t)a.d | (uintptr_t)a.res) % 16 == 0;
-  const dim3 grid(dense_grid(tiles * p.splits)), block(p.tile == 256 ? kPpThreads : kThreads);
+  const dim3 grid(dense_grid(tiles * p.splits)), block(p.tile == 256 || tiles * p.splits <= 256 ? 512 : 256);
   const int nr = p.nr, nc = p.nc;
   if (p.splits > 1) {
     if (p.tile == 256)
       hipLaunchKernelGGL((mx256_kernel<A8, GLU, 0, true>), grid, block, 0, st, a, vec, nr, nc, p.splits);
+    else if (tiles * p.splits <= 256)
+      hipLaunchKernelGGL((mx128_kernel<A8, GLU, 0, true, 4>), grid, block, 0, st, a, vec, nr, nc, p.splits);
     else
-      hipLaunchKernelGGL((mx128_kernel<A8, GLU, 0, true>), grid, block, 0, st, a, vec, nr, nc, p.splits);
+      hipLaunchKernelGGL((mx128_kernel<A8, GLU, 0, true, 2>), grid, block, 0, st, a, vec, nr, nc, p.splits);
     const int ch = p.tile * (GLU ? p.tile / 2 : p.tile) / 8;
     const dim3 jgrid((ch + kThreads - 1) / kThreads, (unsigned)tiles);
     if (p.tile == 256)
@@ -736,8 +731,10 @@ hipError_t launch(const mok_mx_args& a, const Plan& p, hipStream_t st) {
       hipLaunchKernelGGL((mx256_kernel<A8, GLU, GLU ? ACT : 1, false>), grid, block, 0, st, a, vec, nr, nc, 1);
     else
       hipLaunchKernelGGL((mx256_kernel<A8, GLU, ACT, false>), grid, block, 0, st, a, vec, nr, nc, 1);
+  } else if (tiles <= 256) {
+    hipLaunchKernelGGL((mx128_kernel<A8, GLU, ACT, false, 4>), grid, block, 0, st, a, vec, nr, nc, 1);
   } else {
-    hipLaunchKernelGGL((mx128_kernel<A8, GLU, ACT, false>), grid, block, 0, st, a, vec, nr, nc, 1);
+    hipLaunchKernelGGL((mx128_kernel<A8, GLU, ACT, false, 2>), grid, block, 0, st, a, vec, nr, nc, 1);
   }
   return hipGetLastError();
 }
