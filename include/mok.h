@@ -366,8 +366,8 @@ mok_status mok_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t
  * with its scales [rows][K/32]; products on the scaled matrix instructions,
  * summed in fp32 in a fixed order, one rounding to bf16. A block of scale 255
  * makes its row of D (or, in B, its column) NaN. K a multiple of 128 and at
- * most 2^20 (MOK_ERR_UNSUPPORTED otherwise); M, N >= 0, any value up to 2^30;
- * a and b 16-byte, scales 4-byte aligned; D may start and step anywhere.
+ * most 2^20 (MOK_ERR_UNSUPPORTED otherwise); M, N >= 0, any value up to 2^30
+ * with ceil(M/128) * ceil(N/128) <= 2^23 (MOK_ERR_UNSUPPORTED); a and b 16-byte, scales 4-byte aligned; D may start and step anywhere.
  * Columns N .. ld_d-1 of D are not touched. */
 typedef struct {
   int64_t M, N, K;
@@ -376,7 +376,9 @@ typedef struct {
 } mok_mx_problem;
 
 /* [host] Workspace bytes of mok_mx_matmul (0 for many shapes; not monotonic in
- * M: few rows are split along K to fill the device). */
+ * M: few rows are split along K to fill the device). The workspace is scratch
+ * of one call at a time: calls that may overlap (on two streams, in graphs
+ * replayed side by side) take one each. */
 mok_status mok_mx_matmul_workspace(const mok_mx_problem* problem, size_t* workspace_bytes);
 
 mok_status mok_mx_matmul(const mok_mx_problem* problem, const uint8_t* a, const uint8_t* a_scales,
@@ -406,8 +408,8 @@ typedef struct {
   int64_t ld_x, ld_y;
 } mok_ffn_problem;
 
-/* [host] Bytes of the caller's buffers: workspace (scratch of either call, not
- * monotonic in T) and ctx, what the forward saves for the backward: the
+/* [host] Bytes of the caller's buffers: workspace (scratch of either call, one
+ * call at a time as mok_mx_matmul's, not monotonic in T) and ctx, what the forward saves for the backward: the
  * pre-activations [T][2I] bf16, a in columns [0, I), b in [I, 2I) (MOK_MXFP4:
  * 0). */
 mok_status mok_ffn_buffer_sizes(const mok_ffn_problem* problem, size_t* workspace_bytes, size_t* ctx_bytes);
@@ -415,13 +417,14 @@ mok_status mok_ffn_buffer_sizes(const mok_ffn_problem* problem, size_t* workspac
 /* residual NULL = none, and may be y itself (y += block(x)): the routed
  * layer's output goes in here and the shared expert is added before the one
  * rounding. ctx NULL for inference. Columns H .. ld_y-1 of y are not touched.
- * x and y may be NULL when T = 0. */
+ * y may be x. x and y may be NULL when T = 0. */
 mok_status mok_ffn_forward(const mok_ffn_problem* problem, const void* x, const mok_weights* weights,
                            const void* residual, void* y, void* ctx, void* workspace, size_t workspace_bytes,
                            void* stream);
 
 /* Gradients of <dy, y> from the forward's x and ctx: dx [T][H], dw_gate, dw_up
  * [I][H], dw_down [H][I] (bf16, overwritten; the residual's gradient is dy).
+ * dx may be x or dy (at the same row pitch).
  * With T = 0 the weight gradients are zeros and the other pointers may be NULL.
  * MOK_MXFP4: MOK_ERR_UNSUPPORTED. */
 mok_status mok_ffn_backward(const mok_ffn_problem* problem, const void* ctx, const void* x,

@@ -583,6 +583,13 @@ inline float few_time(int64_t M, int64_t rows, int64_t K) {
 }
 inline unsigned dense_grid(int64_t n) { return (unsigned)((n + kXcds - 1) / kXcds * kXcds); }
 
+// A launch takes fewer than 2^32 threads along x: `blocks` workgroups as rows of 2^22.
+inline dim3 flat_grid(int64_t blocks) {
+  const int64_t row = (int64_t)1 << 22;
+  return blocks <= row ? dim3((unsigned)blocks) : dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
+}
+MOK_DEV int64_t flat_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // ------------------------------------------------------------------ gates
 // act(a) and its derivative; KIND 0: SiLU a*s(a), 1: GELU in its tanh form,
 // a/2 (1 + tanh u) = a*s(2u), u = sqrt(2/pi)(a + 0.044715 a^3), with the logistic s.

@@ -12,12 +12,13 @@ using namespace mok;
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxK = (int64_t)1 << 20, kMaxTiles = (int64_t)1 << 28;
+constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxK = (int64_t)1 << 20, kMaxTiles = (int64_t)1 << 23;
 constexpr int64_t kMaxPitch = (int64_t)1 << 22;  // row pitch of x, y, dy, dx in elements (copies: 32-bit offsets)
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// rows x cols in 128 x 128 tiles, within what a launch can number
+// rows x cols in 128 x 128 tiles, of 256 threads each, within one launch (2^32 threads; tiles of
+// 256 x 256 have 512 threads and are split into no more than 512)
 bool tiles_fit(int64_t rows, int64_t cols) { return cdiv(rows, 128) * cdiv(cols, 128) <= kMaxTiles; }
 
 struct Ffn {

@@ -44,7 +44,7 @@ MOK_DEV uint32_t block_max_bits(const float v[8]) {
 __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const bf16_t* __restrict__ src, int64_t n8,
                                                             uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
   typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t idx = flat_block() * 256 + threadIdx.x;
   if (idx >= n8) return;                         // n8 is a multiple of 4: whole blocks leave
   const uint4 raw = reinterpret_cast<const uint4*>(src)[idx];
   const auto mag = [](uint32_t v) { return __builtin_bit_cast(u16x2, v & 0x7FFF7FFFu); };
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const bf16_t* __res
 __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __restrict__ q,
                                                               const uint8_t* __restrict__ scales, int64_t n8,
                                                               bf16_t* __restrict__ dst) {
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t idx = flat_block() * 256 + threadIdx.x;
   if (idx >= n8) return;
   const uint32_t w = reinterpret_cast<const uint32_t*>(q)[idx];
   const float x = e8m0(scales[idx >> 2]);
@@ -88,7 +88,7 @@ template <class T>
 __global__ __launch_bounds__(256) void mxfp8_rows_kernel(const T* __restrict__ src, int64_t ld, int64_t n8,
                                                         int k8, uint8_t* __restrict__ q,
                                                         uint8_t* __restrict__ scales) {
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t idx = flat_block() * 256 + threadIdx.x;
   if (idx >= n8) return;
   const int64_t r = idx / k8, c = idx - r * k8;
   float v[8];
@@ -597,7 +597,8 @@ __global__ __launch_bounds__(kFewThreads) void mx_few_kernel(mok_mx_args a) {
   constexpr int U = 4;                           // steps per batch: one scale word per lane group
   __shared__ __attribute__((aligned(16))) float red[kFewWaves * NT * 256];
   const int l = lane_id(), lr = l & 15, g = l >> 4;
-  const int c0 = (int)blockIdx.x * (GLU ? 8 : 16);
+  const int c0 = (int)flat_block() * (GLU ? 8 : 16);
+  if (c0 >= a.N) return;                         // (the last row of a flat grid)
   const int64_t kb = a.K / 2, ks = a.K / 32;
   const uint8_t* wp;
   const uint8_t* wsp;
@@ -681,7 +682,7 @@ __global__ __launch_bounds__(kFewThreads) void mx_few_kernel(mok_mx_args a) {
 
 template <bool A8, bool GLU, int ACT>
 hipError_t launch_few(const mok_mx_args& a, hipStream_t st) {
-  const dim3 grid(GLU ? a.N / 8 : (a.N + 15) / 16), block(kFewThreads);
+  const dim3 grid = flat_grid(GLU ? a.N / 8 : (a.N + 15) / 16), block(kFewThreads);
   if (a.M <= 16) hipLaunchKernelGGL((mx_few_kernel<A8, GLU, ACT, 1>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((mx_few_kernel<A8, GLU, ACT, 2>), grid, block, 0, st, a);
   return hipGetLastError();
@@ -708,7 +709,6 @@ Plan plan_of(const mok_mx_args& a, bool glu) {
 template <bool A8, bool GLU, int ACT>
 hipError_t launch(const mok_mx_args& a, const Plan& p, hipStream_t st) {
   const int64_t tiles = (int64_t)p.nr * p.nc;
-  if (tiles * p.splits > (1 << 30)) return hipErrorInvalidValue;
   if (tiles == 0) return hipSuccess;
   const bool vec = a.ldd % 8 == 0 && ((uintptr_t)a.d | (uintptr_t)a.res) % 16 == 0;
   const dim3 grid(dense_grid(tiles * p.splits)), block(p.tile == 256 || tiles * p.splits <= 256 ? 512 : 256);
@@ -745,9 +745,8 @@ hipError_t mok_launch_mxfp4_quantize(const bf16_t* src, int64_t rows, int64_t K,
                                      hipStream_t st) {
   const int64_t n8 = rows * (K / 8);
   if (n8 <= 0) return hipSuccess;
-  const int64_t grid = (n8 + 255) / 256;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(mxfp4_quantize_kernel, dim3((unsigned)grid), dim3(256), 0, st, src, n8, q, scales);
+  const dim3 grid = flat_grid((n8 + 255) / 256);
+  hipLaunchKernelGGL(mxfp4_quantize_kernel, grid, dim3(256), 0, st, src, n8, q, scales);
   return hipGetLastError();
 }
 
@@ -755,9 +754,8 @@ hipError_t mok_launch_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, 
                                        bf16_t* dst, hipStream_t st) {
   const int64_t n8 = rows * (K / 8);
   if (n8 <= 0) return hipSuccess;
-  const int64_t grid = (n8 + 255) / 256;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(mxfp4_dequantize_kernel, dim3((unsigned)grid), dim3(256), 0, st, q, scales, n8, dst);
+  const dim3 grid = flat_grid((n8 + 255) / 256);
+  hipLaunchKernelGGL(mxfp4_dequantize_kernel, grid, dim3(256), 0, st, q, scales, n8, dst);
   return hipGetLastError();
 }
 
@@ -765,14 +763,13 @@ hipError_t mok_launch_mxfp8_rows(const void* src, bool f32, int64_t ld, int64_t 
                                  uint8_t* scales, hipStream_t st) {
   const int64_t n8 = rows * (K / 8);
   if (n8 <= 0) return hipSuccess;
-  const int64_t grid = (n8 + 255) / 256;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid = flat_grid((n8 + 255) / 256);
   if (f32)
-    hipLaunchKernelGGL(mxfp8_rows_kernel<float>, dim3((unsigned)grid), dim3(256), 0, st, static_cast<const float*>(src),
-                       ld, n8, (int)(K / 8), q, scales);
+    hipLaunchKernelGGL(mxfp8_rows_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(src), ld, n8,
+                       (int)(K / 8), q, scales);
   else
-    hipLaunchKernelGGL(mxfp8_rows_kernel<bf16_t>, dim3((unsigned)grid), dim3(256), 0, st,
-                       static_cast<const bf16_t*>(src), ld, n8, (int)(K / 8), q, scales);
+    hipLaunchKernelGGL(mxfp8_rows_kernel<bf16_t>, grid, dim3(256), 0, st, static_cast<const bf16_t*>(src), ld, n8,
+                       (int)(K / 8), q, scales);
   return hipGetLastError();
 }
 

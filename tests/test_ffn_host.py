@@ -73,7 +73,7 @@ def test_ffn_calls_refuse_before_any_launch():
 
 @pytest.mark.parametrize("kw,status", [
     (dict(M=-1), INV), (dict(N=-1), INV), (dict(K=0), INV), (dict(K=160), UNS), (dict(a_dtype=0), INV),
-    (dict(ld_d=99), INV), (dict(K=1 << 21), UNS), (dict(M=1 << 30, N=1 << 30), UNS),
+    (dict(ld_d=99), INV), (dict(K=1 << 21), UNS), (dict(M=1 << 30, N=1 << 30), UNS), (dict(M=1 << 30, N=129), UNS),
 ])
 def test_mx_problems_refused(kw, status):
     p = dict(M=10, N=100, K=256, a_dtype=mok.MOK_MXFP4)

@@ -270,6 +270,25 @@ def test_binding_refuses():
     refused(w=w[:2])
 
 
+@pytest.mark.parametrize("T,H,I", [(3, 256, 128), (200, 256, 128), (2500, 2048, 768), (4100, 2048, 768)])
+def test_outputs_in_place_of_inputs(T, H, I):
+    """y over x (as residual too), dx over x and over dy: the same bits as in buffers of their own."""
+    import torch
+    c = {k: bf(v) for k, v in case(T, H, I).items()}
+    w = (c["wg"], c["wu"], c["wd"])
+    ws = F.get_ffn_workspace(T, H, I)
+    y = F.run_ffn_forward(ws, c["x"], w, residual=c["x"])
+    dx, *dw = F.run_ffn_backward(ws, c["x"], w, c["dy"])
+    over = c["x"].clone()
+    F.run_ffn_forward(ws, over, w, residual=over, y=over)
+    assert torch.equal(over, y)
+    for over in ("x", "dy"):
+        a = dict(x=c["x"].clone(), dy=c["dy"].clone())
+        g = [torch.empty_like(t) for t in dw]
+        mok.ffn_backward(ws.problem, ws.ctx, a["x"], w, a["dy"], a[over], *g, ws.workspace)
+        assert torch.equal(a[over], dx) and all(torch.equal(p, q) for p, q in zip(g, dw)), over
+
+
 def test_offsets_past_32_bits():
     """Two billion elements of x, y, dy and dx: the last tokens' outputs and the weight gradients, whose sums run
     over all tokens."""

@@ -308,3 +308,46 @@ def test_calls_are_traced():
     finally:
         mok.trace_enable(False)
     assert set(seen) == {"ffn_quantize_x", "ffn_gateup_mxfp4", "ffn_down_mxfp4", "mxfp4_quantize", "mxfp4_dequantize"}
+
+
+def test_quantize_more_than_one_row_of_workgroups():
+    """2^35 + 3 * 2^20 elements: more threads than a launch holds along one axis. Every row is one of a few, so the
+    codes of all rows are known from theirs."""
+    import torch
+    K, rows = 1 << 20, (1 << 15) + 3
+    free, _ = torch.cuda.mem_get_info()
+    if free < 100 << 30:
+        pytest.skip("needs 100 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    few = torch.randn((5, K), generator=g, device="cuda").bfloat16()
+    src = torch.empty((rows, K), dtype=torch.bfloat16, device="cuda")
+    for i in range(5):
+        src[i::5] = few[i]
+    q, s = F.mxfp4_quantize(src)
+    qf, sf = F.mxfp4_quantize(few)
+    src.zero_()
+    mok.mxfp4_dequantize(q, s, src)
+    back = F.mxfp4_dequantize(qf, sf)
+    for i in range(5):
+        for j in range(i, rows, 5 * 512):
+            e = slice(j, min(j + 5 * 512, rows), 5)
+            assert bool((q[e] == qf[i]).all()) and bool((s[e] == sf[i]).all()) and bool((src[e] == back[i]).all()), j
+
+
+def test_matmul_more_than_one_row_of_workgroups():
+    """2^27 + 40 rows of B with one row of A: every row of B is one of 77, and so is every column of D."""
+    import torch
+    N, K, P = (1 << 27) + 40, 128, 77
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    a = torch.randint(0, 256, (1, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    sa = torch.randint(120, 134, (1, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    bp = torch.randint(0, 256, (P, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    sp = torch.randint(120, 134, (P, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    rep = -(-N // P)
+    b, sb = (t.repeat(rep, 1)[:N].contiguous() for t in (bp, sp))
+    one = F.run_mx_matmul(F.get_mx_matmul_workspace(1, P, K, mok.MOK_MXFP4), a, sa, bp, sp)
+    d = F.run_mx_matmul(F.get_mx_matmul_workspace(1, N, K, mok.MOK_MXFP4), a, sa, b, sb)
+    assert bool((d == one.repeat(1, rep)[:, :N]).all())
