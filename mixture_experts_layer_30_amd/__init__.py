@@ -305,21 +305,29 @@ def router_backward(problem, schedule, x, w_router, topk_ids, topk_w, d_topk_w, 
 # These calls check their tensors (device, type, shape, row layout) and run on
 # the tensors' device: with the caller's stream, or that device's current one.
 
-_types = None
+_torch = None
 
 
-def _want(what, t, dtype, shape, rows=False, device=None):
-    """t is a device tensor of this type and shape, contiguous (rows=True: with
-    contiguous elements within a row, rows at any pitch)."""
-    global _types
-    if _types is None:
+def _device_of(t):
+    """The index of t's GPU (-1: none), at which the call's other tensors have to be."""
+    global _torch
+    if _torch is None:
         import torch
-        _types = {"bf16": torch.bfloat16, "u8": torch.uint8}
-    if not t.is_cuda or (device is not None and t.device != device):
+        _torch = torch
+    return t.get_device()
+
+
+def _want(what, t, dtype, shape, index, rows=False):
+    """t is a tensor of GPU `index` of this type and shape, contiguous (rows=True: with
+    contiguous elements within a row, rows at any pitch)."""
+    dtype = _torch.bfloat16 if dtype == "bf16" else _torch.uint8
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index != -1 and t.is_contiguous():
+        return
+    if not t.is_cuda or t.get_device() != index:
         raise MokError(MOK_ERR_INVALID_ARG, f"{what}: not on the call's GPU ({t.device})")
-    if t.dtype is not _types[dtype] or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise MokError(MOK_ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, wanted {dtype} {tuple(shape)}")
-    if not t.is_contiguous() and not (rows and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
+    if not (rows and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
         raise MokError(MOK_ERR_INVALID_ARG, f"{what}: strides {t.stride()}")
 
 
@@ -328,25 +336,23 @@ def _pitch(t):
     return 0 if t.is_contiguous() else t.stride(0)
 
 
-def _scratch(workspace, device):
+def _scratch(workspace, index):
     """(pointer, bytes) of a workspace tensor or None."""
     if workspace is None:
         return None, 0
-    if workspace.device != device or not workspace.is_contiguous():
-        raise MokError(MOK_ERR_INVALID_ARG, f"workspace: not contiguous memory of {device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise MokError(MOK_ERR_INVALID_ARG, f"workspace: not contiguous memory of GPU {index}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
-def _run(what, t, stream, fn, *args):
-    """fn(*args, stream) on the device of t: the caller's stream, or that device's current one."""
-    import torch
-    index = t.device.index
-    # (the raw handle: torch.cuda.current_stream builds a Stream object, 3 us a call)
-    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
-    if index == torch.cuda.current_device():
+def _run(what, index, stream, fn, *args):
+    """fn(*args, stream) on GPU `index`: the caller's stream, or that device's current one."""
+    # (the raw handles: torch.cuda.current_stream builds a Stream object, 3 us a call)
+    st = _torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if index == _torch._C._cuda_getDevice():
         status = fn(*args, st)
     else:
-        with torch.cuda.device(index):
+        with _torch.cuda.device(index):
             status = fn(*args, st)
     if status != MOK_OK:
         raise MokError(status, what)
@@ -360,20 +366,22 @@ def _rows_K(src):
 def mxfp4_quantize(src, q, scales, stream=None):
     """src [..., K] bf16 -> q [..., K/2] uint8 (two E2M1 codes a byte), scales [..., K/32] uint8 (E8M0)."""
     rows, K = _rows_K(src)
-    _want("src", src, "bf16", src.shape)
-    _want("q", q, "u8", (*src.shape[:-1], K // 2), device=src.device)
-    _want("scales", scales, "u8", (*src.shape[:-1], K // 32), device=src.device)
-    _run("mok_mxfp4_quantize", src, stream, lib().mok_mxfp4_quantize, src.data_ptr(), rows, K, q.data_ptr(),
+    dev = _device_of(src)
+    _want("src", src, "bf16", src.shape, dev)
+    _want("q", q, "u8", (*src.shape[:-1], K // 2), dev)
+    _want("scales", scales, "u8", (*src.shape[:-1], K // 32), dev)
+    _run("mok_mxfp4_quantize", dev, stream, lib().mok_mxfp4_quantize, src.data_ptr(), rows, K, q.data_ptr(),
          scales.data_ptr())
 
 
 def mxfp4_dequantize(q, scales, dst, stream=None):
     """The bf16 values dst [..., K] of the codes q [..., K/2] and scales [..., K/32]."""
     rows, K = _rows_K(dst)
-    _want("dst", dst, "bf16", dst.shape)
-    _want("q", q, "u8", (*dst.shape[:-1], K // 2), device=dst.device)
-    _want("scales", scales, "u8", (*dst.shape[:-1], K // 32), device=dst.device)
-    _run("mok_mxfp4_dequantize", dst, stream, lib().mok_mxfp4_dequantize, q.data_ptr(), scales.data_ptr(), rows, K,
+    dev = _device_of(dst)
+    _want("dst", dst, "bf16", dst.shape, dev)
+    _want("q", q, "u8", (*dst.shape[:-1], K // 2), dev)
+    _want("scales", scales, "u8", (*dst.shape[:-1], K // 32), dev)
+    _run("mok_mxfp4_dequantize", dev, stream, lib().mok_mxfp4_dequantize, q.data_ptr(), scales.data_ptr(), rows, K,
          dst.data_ptr())
 
 
@@ -392,14 +400,14 @@ def mx_matmul(problem, a, a_scales, b, b_scales, d, workspace, stream=None):
     """d [M][N] bf16 = A . B^T: a [M][K] (MXFP8) or [M][K/2] (MXFP4) uint8, b [N][K/2] uint8, scales
     [rows][K/32] uint8. The row pitch of d is taken from the tensor (problem.ld_d is ignored)."""
     M, N, K = problem.M, problem.N, problem.K
-    dev = d.device
-    _want("d", d, "bf16", (M, N), rows=True)
-    _want("a", a, "u8", (M, K if problem.a_dtype == MOK_MXFP8 else K // 2), device=dev)
-    _want("a_scales", a_scales, "u8", (M, K // 32), device=dev)
-    _want("b", b, "u8", (N, K // 2), device=dev)
-    _want("b_scales", b_scales, "u8", (N, K // 32), device=dev)
+    dev = _device_of(d)
+    _want("d", d, "bf16", (M, N), dev, rows=True)
+    _want("a", a, "u8", (M, K if problem.a_dtype == MOK_MXFP8 else K // 2), dev)
+    _want("a_scales", a_scales, "u8", (M, K // 32), dev)
+    _want("b", b, "u8", (N, K // 2), dev)
+    _want("b_scales", b_scales, "u8", (N, K // 32), dev)
     p = MxProblem(M, N, K, _pitch(d), problem.a_dtype)
-    _run("mok_mx_matmul", d, stream, lib().mok_mx_matmul, ctypes.byref(p), a.data_ptr(), a_scales.data_ptr(),
+    _run("mok_mx_matmul", dev, stream, lib().mok_mx_matmul, ctypes.byref(p), a.data_ptr(), a_scales.data_ptr(),
          b.data_ptr(), b_scales.data_ptr(), d.data_ptr(), *_scratch(workspace, dev))
 
 
@@ -422,10 +430,10 @@ def _ffn_weights(problem, weights, device):
         raise MokError(MOK_ERR_INVALID_ARG, "weights: (w_gate, w_up, w_down[, s_gate, s_up, s_down])")
     t, div = ("u8", 2) if mx else ("bf16", 1)
     for n, w, shape in zip(("w_gate", "w_up", "w_down"), weights, ((I, H // div), (I, H // div), (H, I // div))):
-        _want(n, w, t, shape, device=device)
+        _want(n, w, t, shape, device)
     if mx:
         for n, w, shape in zip(("s_gate", "s_up", "s_down"), weights[3:], ((I, H // 32), (I, H // 32), (H, I // 32))):
-            _want(n, w, "u8", shape, device=device)
+            _want(n, w, "u8", shape, device)
     return _weights(*weights[:6 if mx else 3])
 
 
@@ -438,38 +446,38 @@ def ffn_forward(problem, x, weights, y, workspace, residual=None, ctx=None, stre
     may have any row pitch that is a multiple of 8 (taken from the tensors). weights: (w_gate, w_up, w_down)
     bf16, or MXFP4 codes with (s_gate, s_up, s_down)."""
     T, H = problem.T, problem.H
-    dev = x.device
-    _want("x", x, "bf16", (T, H), rows=True)
-    _want("y", y, "bf16", (T, H), rows=True, device=dev)
+    dev = _device_of(x)
+    _want("x", x, "bf16", (T, H), dev, rows=True)
+    _want("y", y, "bf16", (T, H), dev, rows=True)
     if residual is not None:
-        _want("residual", residual, "bf16", (T, H), rows=True, device=dev)
+        _want("residual", residual, "bf16", (T, H), dev, rows=True)
         if _pitch(residual) != _pitch(y):
             raise MokError(MOK_ERR_INVALID_ARG, "residual: another row pitch than y")
     if ctx is not None:
-        _want("ctx", ctx, "bf16", (T, 2 * problem.I), device=dev)
+        _want("ctx", ctx, "bf16", (T, 2 * problem.I), dev)
     w = _ffn_weights(problem, weights, dev)
     p = _ffn_call(problem, _pitch(x), _pitch(y))
-    _run("mok_ffn_forward", x, stream, lib().mok_ffn_forward, ctypes.byref(p), x.data_ptr(), ctypes.byref(w),
+    _run("mok_ffn_forward", dev, stream, lib().mok_ffn_forward, ctypes.byref(p), x.data_ptr(), ctypes.byref(w),
          _ptr(residual), y.data_ptr(), _ptr(ctx), *_scratch(workspace, dev))
 
 
 def ffn_backward(problem, ctx, x, weights, dy, dx, dw_gate, dw_up, dw_down, workspace, stream=None):
     """Gradients of <dy, y>; x and dx share one row pitch, dy may have another."""
     T, H, I = problem.T, problem.H, problem.I
-    dev = x.device
+    dev = _device_of(x)
     if ctx is None:
         raise MokError(MOK_ERR_INVALID_ARG, "ctx: no context was saved by a forward")
-    _want("x", x, "bf16", (T, H), rows=True)
-    _want("dy", dy, "bf16", (T, H), rows=True, device=dev)
-    _want("dx", dx, "bf16", (T, H), rows=True, device=dev)
-    _want("ctx", ctx, "bf16", (T, 2 * I), device=dev)
+    _want("x", x, "bf16", (T, H), dev, rows=True)
+    _want("dy", dy, "bf16", (T, H), dev, rows=True)
+    _want("dx", dx, "bf16", (T, H), dev, rows=True)
+    _want("ctx", ctx, "bf16", (T, 2 * I), dev)
     for n, t, shape in (("dw_gate", dw_gate, (I, H)), ("dw_up", dw_up, (I, H)), ("dw_down", dw_down, (H, I))):
-        _want(n, t, "bf16", shape, device=dev)
+        _want(n, t, "bf16", shape, dev)
     if _pitch(x) != _pitch(dx):
         raise MokError(MOK_ERR_INVALID_ARG, "dx: another row pitch than x")
     w = _ffn_weights(problem, weights, dev)
     p = _ffn_call(problem, _pitch(x), _pitch(dy))
-    _run("mok_ffn_backward", x, stream, lib().mok_ffn_backward, ctypes.byref(p), ctx.data_ptr(), x.data_ptr(),
+    _run("mok_ffn_backward", dev, stream, lib().mok_ffn_backward, ctypes.byref(p), ctx.data_ptr(), x.data_ptr(),
          ctypes.byref(w), dy.data_ptr(), dx.data_ptr(), dw_gate.data_ptr(), dw_up.data_ptr(), dw_down.data_ptr(),
          *_scratch(workspace, dev))
 
