@@ -585,10 +585,11 @@ __global__ __launch_bounds__(kPpThreads, 1) void mx256_kernel(mok_mx_args a, boo
 // rows (E2M1) are the first operand, 16 rows of A the second; lane l supplies row
 // l % 16 with the 32 weights from 32 g on (g = l / 16, 16 bytes), of E4M3 the 16 bytes
 // from 16 g on and those 64 further, and the scale of block g (checked on gfx950).
-// The rows of A are quantized by a launch of their own: every workgroup quantizing
-// them as it reads them took 9 us more at 16 rows of 7168 (256 workgroups repeat
-// the work) against 2.5 us for the launch. So h, of which a workgroup makes 8
-// columns and a block has 32, goes out as fp32.
+// The rows of A are quantized by a launch of their own, which takes 2.5 us: every
+// workgroup quantizing them as it reads them (256 or more repeat the work, on two or four
+// times the bytes) took 9 us more for x at 16 rows of 7168, and for h at rows of 2048 2 us
+// more at one row and 5 us at 16. So h, of which a workgroup makes 8 columns and a block has 32,
+// goes out as fp32.
 constexpr int kMxFewRows = 32;
 
 template <bool A8, bool GLU, int ACT, int NT>
