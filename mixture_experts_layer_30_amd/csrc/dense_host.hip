@@ -98,16 +98,26 @@ FfnWs fwd_ws(const Ffn& r) {
 FfnBwdWs bwd_ws(const Ffn& r) {
   FfnBwdWs w;
   const mok_ffn_args a = ffn_args(r);
-  size_t o = 0, part = 0;
+  size_t o = 0, part;
   w.h = o;    o = align_up(o + (size_t)r.T * r.I * 2);
   w.dab = o;  o = align_up(o + (size_t)r.T * a.Ip * 4);
-  for (mok_ffn_op op : {FFN_DH, FFN_DWD, FFN_DWGU, FFN_DX}) part = std::max(part, mok_ffn_part_bytes(a, op));
+  part = std::max(mok_ffn_part_bytes(a, FFN_DH), mok_ffn_grads_part_bytes(a));
   w.part = o; o = align_up(o + part);
   w.total = o;
   return w;
 }
 size_t ffn_ws_bytes(const Ffn& r) { return std::max(fwd_ws(r).total, r.mx ? (size_t)0 : bwd_ws(r).total); }
 size_t ffn_ctx_bytes(const Ffn& r) { return r.mx ? 0 : (size_t)r.T * 2 * r.I * 2; }
+
+// whether rows of H elements share memory: T rows at a of pitch lda, and at b of pitch ldb
+// (rows of one pitch that lie side by side do not)
+bool rows_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t T, int64_t H) {
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(b)) / 2;
+  if (T <= 0 || d >= (T - 1) * ldb + H || -d >= (T - 1) * lda + H) return false;
+  if (lda != ldb) return true;
+  const int64_t m = (d % lda + lda) % lda;
+  return m < H || m > lda - H;
+}
 
 mok_status ffn_weights(const Ffn& r, const mok_weights* w) {
   if (!w || !w->w_gate || !w->w_up || !w->w_down) return MOK_ERR_INVALID_ARG;
@@ -210,6 +220,8 @@ mok_status mok_ffn_backward(const mok_ffn_problem* problem, const void* ctx, con
   for (const void* p : {ctx, x, dy, (const void*)dx, (const void*)dw_gate, (const void*)dw_up, (const void*)dw_down,
                         (const void*)workspace})
     if (!aligned(p, 16)) return MOK_ERR_INVALID_ARG;
+  if (rows_overlap(dx, r.ldx, x, r.ldx, r.T, r.H) || rows_overlap(dx, r.ldx, dy, r.ldy, r.T, r.H))
+    return MOK_ERR_INVALID_ARG;
   const FfnBwdWs W = bwd_ws(r);
   if (r.T > 0 && (!workspace || workspace_bytes < ffn_ws_bytes(r))) return MOK_ERR_BUFFER_TOO_SMALL;
   if ((s = check_device()) != MOK_OK) return s;
@@ -233,9 +245,7 @@ mok_status mok_ffn_backward(const mok_ffn_problem* problem, const void* ctx, con
     MOK_RUN("ffn_bwd_dh", mok_launch_ffn(a, FFN_DH, r.act, st));
   }
   // (no tokens: the sums over them are empty, and the weight gradients zeros)
-  MOK_RUN("ffn_bwd_dwd", mok_launch_ffn(a, FFN_DWD, r.act, st));
-  MOK_RUN("ffn_bwd_dwgu", mok_launch_ffn(a, FFN_DWGU, r.act, st));
-  if (r.T > 0) MOK_RUN("ffn_bwd_dx", mok_launch_ffn(a, FFN_DX, r.act, st));
+  MOK_RUN("ffn_bwd_grads", mok_launch_ffn_grads(a, st));
   return MOK_OK;
 }
 

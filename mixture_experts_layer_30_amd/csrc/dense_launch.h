@@ -34,9 +34,14 @@ enum mok_ffn_op { FFN_GATEUP, FFN_DOWN, FFN_DH, FFN_DWD, FFN_DWGU, FFN_DX, FFN_O
 
 // bytes of partial tiles that `op` needs at this shape (0: not split)
 size_t mok_ffn_part_bytes(const mok_ffn_args& a, mok_ffn_op op);
-// the product `op` with its epilogue (and, where it is split along K, the sum
+// the product `op` (not those of mok_launch_ffn_grads) with its epilogue (and, where it is split along K, the sum
 // of its partial tiles); act: mok_activation, used by FFN_GATEUP and FFN_DH
 hipError_t mok_launch_ffn(const mok_ffn_args& a, mok_ffn_op op, int act, hipStream_t st);
+
+// dWd, dWg, dWu and dx together, once FFN_DH has made h and dab; with no tokens
+// the weight gradients are zeros and there is no dx
+size_t mok_ffn_grads_part_bytes(const mok_ffn_args& a);
+hipError_t mok_launch_ffn_grads(const mok_ffn_args& a, hipStream_t st);
 
 // ---------------------------------------------------------------- MX formats
 hipError_t mok_launch_mxfp4_quantize(const bf16_t* src, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,

@@ -10,6 +10,8 @@
 // ascending order), so results are bitwise reproducible. Rounded to bf16: y, the
 // saved a and b, and the operands of the next product, h, da and db (the matrix
 // cores take bf16): each adds at most 2^-8 relative to its element.
+#include <utility>
+
 #include "dense_core.h"
 #include "dense_launch.h"
 
@@ -165,27 +167,25 @@ MOK_DEV auto copy_b(const mok_ffn_args& a, int n0) {
   }
 }
 
-template <int OP, int ACT, bool SPLIT, int S>
-__global__ __launch_bounds__(kThreads128<S>, S == 2 ? 2 : 1) void ffn128_kernel(mok_ffn_args a, int M, int K, int nr,
-                                                                                int nc, int batch, int splits) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[lds128<S, 32768>()];
-  const int tiles = nr * nc * batch;
-  const int i = dense_index((int64_t)tiles * splits);
-  if (i < 0) return;
-  const int split = SPLIT ? i / tiles : 0, t = SPLIT ? i % tiles : i, half = t / (nr * nc);
+// tile i of the product, counted over its splits along K; split in two or more, to partial
+// tiles (split, tile) of fp32 rows at `part`
+template <int OP, int ACT, int S>
+MOK_DEV void tile128(const mok_ffn_args& a, uint8_t* lds, float* part, int i, int M, int K, int nr, int nc, int batch,
+                     int splits) {
+  const int tiles = nr * nc * batch, split = splits > 1 ? i / tiles : 0, t = splits > 1 ? i % tiles : i;
+  const int half = t / (nr * nc);
   int row, col;
   dense_tile(t - half * nr * nc, nr, nc, kGroup<128>, row, col);
   const int m0 = row * 128, n0 = col * out_cols<OP, 128>();
   const int ns = (K + 63) / 64;
-  const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
-  const int j1 = SPLIT ? (int)((int64_t)ns * (split + 1) / splits) : ns;
+  const int j0 = splits > 1 ? (int)((int64_t)ns * split / splits) : 0;
+  const int j1 = splits > 1 ? (int)((int64_t)ns * (split + 1) / splits) : ns;
   Acc<2, 2> acc;
   loop128<S>(lds, copy_a<OP>(a, m0, half), copy_b<OP>(a, n0), j0, j1, acc);
   stage128<S>(lds, acc);
   const int nrows = min(128, M - m0);
-  if constexpr (SPLIT) {
-    // partial tile (split, t): 128 rows of 128 fp32
-    float* p = a.part + ((int64_t)split * tiles + t) * 16384;
+  if (splits > 1) {
+    float* p = part + ((int64_t)split * tiles + t) * 16384;
     for (int idx = threadIdx.x; idx < nrows * 32; idx += kThreads128<S>)
       reinterpret_cast<float4*>(p)[idx] =
           *reinterpret_cast<const float4*>(lds + (idx >> 5) * kPitch128 + (idx & 31) * 16);
@@ -193,24 +193,37 @@ __global__ __launch_bounds__(kThreads128<S>, S == 2 ? 2 : 1) void ffn128_kernel(
     finish_rows<OP, ACT, kThreads128<S>>(a, lds, kPitch128, nrows, m0, n0, half);
   }
 }
+template <int OP, int ACT, bool SPLIT, int S>
+__global__ __launch_bounds__(kThreads128<S>, S == 2 ? 2 : 1) void ffn128_kernel(mok_ffn_args a, int M, int K, int nr,
+                                                                                int nc, int batch, int splits) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[lds128<S, 32768>()];
+  if constexpr (SPLIT) __builtin_assume(splits > 1);
+  const int i = dense_index((int64_t)nr * nc * batch * splits);
+  if (i >= 0) tile128<OP, ACT, S>(a, lds, a.part, i, M, K, nr, nc, batch, SPLIT ? splits : 1);
+}
 
-// sums of the partial tiles of TS x TS, and the epilogue; one workgroup per 256 chunks of
-// eight output columns
+// Sums of the partial tiles of TS x TS, and the epilogue: chunk idx of eight output columns of
+// tile t. One workgroup takes 256 chunks.
 template <int OP, int ACT, int TS>
-__global__ __launch_bounds__(kThreads) void ffn_join_kernel(mok_ffn_args a, int M, int nr, int nc, int batch,
-                                                            int splits) {
+MOK_DEV void join_tile(const mok_ffn_args& a, const float* part, int t, int idx, int M, int nr, int nc, int batch,
+                       int splits) {
   constexpr int CH = out_cols<OP, TS>() / 8;
-  const int tiles = nr * nc * batch, t = (int)blockIdx.y, half = t / (nr * nc);
+  const int tiles = nr * nc * batch, half = t / (nr * nc);
   int row, col;
   dense_tile(t - half * nr * nc, nr, nc, kGroup<TS>, row, col);
-  const int idx = (int)blockIdx.x * kThreads + (int)threadIdx.x;
   const int r = idx / CH, c = (idx % CH) * 8;
   if (r >= min(TS, M - row * TS)) return;
-  const float* p = a.part + (int64_t)t * TS * TS + r * TS + acc_col<OP>(c);
+  const float* p = part + (int64_t)t * TS * TS + r * TS + acc_col<OP>(c);
   float v[8], w[8];
   sum_splits(p, (int64_t)tiles * TS * TS, splits, v);
   if constexpr (OP == FFN_GATEUP) sum_splits(p + 32, (int64_t)tiles * TS * TS, splits, w);
   finish8<OP, ACT>(a, row * TS + r, col * out_cols<OP, TS>() + c, half, v, w);
+}
+template <int OP, int ACT, int TS>
+__global__ __launch_bounds__(kThreads) void ffn_join_kernel(mok_ffn_args a, int M, int nr, int nc, int batch,
+                                                            int splits) {
+  join_tile<OP, ACT, TS>(a, a.part, (int)blockIdx.y, (int)blockIdx.x * kThreads + (int)threadIdx.x, M, nr, nc, batch,
+                         splits);
 }
 
 // Epilogue of a 256 x 256 tile (the main loop ends in a barrier: LDS is free). VAR: the
@@ -316,25 +329,86 @@ MOK_DEV void finish256(const mok_ffn_args& a, uint8_t* lds, Acc<4, 2>& acc, int 
   }
 }
 
-template <int OP, int VAR, bool SPLIT>
-__global__ __launch_bounds__(kPpThreads, 1) void ffn256_kernel(mok_ffn_args a, int M, int K, int nr, int nc,
-                                                               int batch, int splits) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kPpLds];
-  const int tiles = nr * nc * batch;
-  const int ix = dense_index((int64_t)tiles * splits);
-  if (ix < 0) return;
-  const int split = SPLIT ? ix / tiles : 0, t = SPLIT ? ix % tiles : ix, half = t / (nr * nc);
+template <int OP, int VAR>
+MOK_DEV void tile256(const mok_ffn_args& a, uint8_t* lds, float* part, int i, int M, int K, int nr, int nc, int batch,
+                     int splits) {
+  const int tiles = nr * nc * batch, split = splits > 1 ? i / tiles : 0, t = splits > 1 ? i % tiles : i;
+  const int half = t / (nr * nc);
   int row, col;
   dense_tile(t - half * nr * nc, nr, nc, kGroup<256>, row, col);
   const int ns = (K + 63) / 64;
-  const int j0 = SPLIT ? (int)((int64_t)ns * split / splits) : 0;
-  const int j1 = SPLIT ? (int)((int64_t)ns * (split + 1) / splits) : ns;
+  const int j0 = splits > 1 ? (int)((int64_t)ns * split / splits) : 0;
+  const int j1 = splits > 1 ? (int)((int64_t)ns * (split + 1) / splits) : ns;
   const int m0 = row * 256, n0 = col * out_cols<OP, 256>();
   const int nrows = min(256, M - m0), g = pp_group();
   Acc<4, 2> acc;
   pp_loop(lds, copy_a<OP>(a, m0 + 128 * g, half), copy_b<OP>(a, n0 + out_cols<OP, 128>() * g), j0, j1, acc);
-  if constexpr (SPLIT) pp_store32(lds, acc, nrows, a.part + ((int64_t)split * tiles + t) * 65536);
+  if (splits > 1) pp_store32(lds, acc, nrows, part + ((int64_t)split * tiles + t) * 65536);
   else finish256<OP, VAR>(a, lds, acc, nrows, m0, n0, half);
+}
+template <int OP, int VAR, bool SPLIT>
+__global__ __launch_bounds__(kPpThreads, 1) void ffn256_kernel(mok_ffn_args a, int M, int K, int nr, int nc,
+                                                               int batch, int splits) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kPpLds];
+  if constexpr (SPLIT) __builtin_assume(splits > 1);
+  const int i = dense_index((int64_t)nr * nc * batch * splits);
+  if (i >= 0) tile256<OP, VAR>(a, lds, a.part, i, M, K, nr, nc, batch, SPLIT ? splits : 1);
+}
+
+// ------------------------------------------------------------------ dWd, dWg and dWu, dx in one launch
+// The three products that follow dh need nothing of each other. Launched one after the
+// other, each ends with CUs that wait for its last tiles; here the workgroups of the next
+// fill them. The products go in descending time of a workgroup, so that the last ones are the short
+// ones (the other way round up to 16% slower), and of two equal ones dWd first, whose operands
+// dh's launch has just read and written (dWg and dWu first: 2 to 4% slower). Against one launch
+// each, the whole backward: 51 -> 31 us at T = 777 of 1000 x 712, 39 -> 23 at 4096 of
+// 256 x 256, 114 -> 101 at 4093 of 2048 x 768, 1174 -> 1116 at 16384 of 4096 x 1536; equal at 64
+// and at 16384 of 7168 x 2048.
+struct GradsPart {
+  int op, M, K, nr, nc, batch, splits;
+  int n, per;                                    // workgroups, and per XCD
+  int joins;                                     // tiles with partial sums
+  int64_t part;                                  // theirs, in floats
+};
+struct GradsPlan {
+  int tile, blocks, joins;
+  int64_t part;
+  GradsPart p[3];
+};
+template <int TS, int S>
+constexpr int grads_lds() { return TS == 256 ? kPpLds : lds128<S, 32768>(); }
+template <int TS, int S>
+__global__ __launch_bounds__(TS == 256 ? kPpThreads : kThreads128<S>, TS == 128 && S == 2 ? 2 : 1) void
+ffn_grads_kernel(mok_ffn_args a, GradsPlan g) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[grads_lds<TS, S>()];
+  int k = (int)blockIdx.x / kXcds, r = 0;
+  if (k >= g.p[0].per) { k -= g.p[0].per; r = 1; }
+  if (r == 1 && k >= g.p[1].per) { k -= g.p[1].per; r = 2; }
+  const GradsPart q = r == 0 ? g.p[0] : r == 1 ? g.p[1] : g.p[2];
+  const int i = ((int)blockIdx.x % kXcds) * q.per + k;
+  if (k >= q.per || i >= q.n) return;
+  float* part = a.part + q.part;
+  if constexpr (TS == 256) {
+    if (q.op == FFN_DWGU) tile256<FFN_DWGU, 0>(a, lds, part, i, q.M, q.K, q.nr, q.nc, q.batch, q.splits);
+    else if (q.op == FFN_DWD) tile256<FFN_DWD, 0>(a, lds, part, i, q.M, q.K, q.nr, q.nc, 1, q.splits);
+    else tile256<FFN_DX, 0>(a, lds, part, i, q.M, q.K, q.nr, q.nc, 1, q.splits);
+  } else {
+    if (q.op == FFN_DWGU) tile128<FFN_DWGU, 0, S>(a, lds, part, i, q.M, q.K, q.nr, q.nc, q.batch, q.splits);
+    else if (q.op == FFN_DWD) tile128<FFN_DWD, 0, S>(a, lds, part, i, q.M, q.K, q.nr, q.nc, 1, q.splits);
+    else tile128<FFN_DX, 0, S>(a, lds, part, i, q.M, q.K, q.nr, q.nc, 1, q.splits);
+  }
+}
+template <int TS>
+__global__ __launch_bounds__(kThreads) void ffn_grads_join_kernel(mok_ffn_args a, GradsPlan g) {
+  int t = (int)blockIdx.y, r = 0;
+  if (t >= g.p[0].joins) { t -= g.p[0].joins; r = 1; }
+  if (r == 1 && t >= g.p[1].joins) { t -= g.p[1].joins; r = 2; }
+  const GradsPart q = r == 0 ? g.p[0] : r == 1 ? g.p[1] : g.p[2];
+  const int idx = (int)blockIdx.x * kThreads + (int)threadIdx.x;
+  const float* part = a.part + q.part;
+  if (q.op == FFN_DWGU) join_tile<FFN_DWGU, 0, TS>(a, part, t, idx, q.M, q.nr, q.nc, q.batch, q.splits);
+  else if (q.op == FFN_DWD) join_tile<FFN_DWD, 0, TS>(a, part, t, idx, q.M, q.nr, q.nc, 1, q.splits);
+  else join_tile<FFN_DX, 0, TS>(a, part, t, idx, q.M, q.nr, q.nc, 1, q.splits);
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -483,6 +557,81 @@ hipError_t launch(const mok_ffn_args& a, const Plan& p, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Tile and splits of the three together, by the constants of dense_plan: for each tile and
+// each longest chunk of K (in slots) the time of all workgroups over the CUs, the half of a
+// shortest one by which the CUs end apart, and the partial sums.
+GradsPlan grads_plan(const mok_ffn_args& a) {
+  constexpr mok_ffn_op kOps[3] = {FFN_DWD, FFN_DWGU, FFN_DX};
+  constexpr int kChunks[] = {1 << 30, 192, 128, 96, 64, 48, 32, 24, 16, 12, 8, 6, 4};
+  Shape sh[3];
+  float read = 0.f;
+  for (int i = 0; i < 3; ++i) {
+    sh[i] = shape_of(a, kOps[i]);
+    read += (float)(sh[i].M + (int64_t)sh[i].N * sh[i].batch) * ((sh[i].K + 63) / 64) * 128 / 4.6e6f;
+  }
+  GradsPlan best;
+  float least = 0.f, took[3] = {0.f, 0.f, 0.f};
+  best.tile = 0;
+  for (int ts = 256; ts >= 128; ts -= 128)
+    for (int chunk : kChunks) {
+      GradsPlan g;
+      float d[3], sum = 0.f, join = 0.f, longest = 0.f, shortest = 0.f;
+      int64_t count = 0;
+      g.tile = ts;
+      g.joins = 0;
+      g.part = 0;
+      for (int i = 0; i < 3; ++i) {
+        GradsPart& q = g.p[i];
+        const int slots = (sh[i].K + 63) / 64;
+        q.op = kOps[i];
+        q.M = sh[i].M; q.K = sh[i].K; q.batch = sh[i].batch;
+        q.nr = (int)(((int64_t)q.M + ts - 1) / ts);
+        q.nc = (sh[i].N + ts - 1) / ts;
+        q.splits = chunk >= slots ? 1 : (slots + chunk - 1) / chunk;
+        if (q.splits > slots / 4) q.splits = slots / 4 > 1 ? slots / 4 : 1;
+        q.n = q.nr * q.nc * q.batch * q.splits;
+        q.per = (q.n + kXcds - 1) / kXcds;
+        q.joins = q.splits > 1 ? q.nr * q.nc * q.batch : 0;
+        q.part = g.part;
+        g.joins += q.joins;
+        if (q.joins) g.part += (int64_t)q.n * ts * ts;
+        if (q.joins) join += (float)q.splits * q.M * sh[i].N * q.batch * 8 / kCost.rate;
+        count += q.n;
+      }
+      if (g.joins && count > 1024) continue;     // (bounds the partial tiles)
+      const bool alone = ts == 256 || count <= 256;
+      for (int i = 0; i < 3; ++i) {
+        const GradsPart& q = g.p[i];
+        const int per = ((q.K + 63) / 64 + q.splits - 1) / q.splits;
+        d[i] = ts == 256 ? kCost.fix256 + per * kCost.slot256
+                         : kCost.fix128 + per * kCost.slot128 * (alone ? kCost.alone : 1.f);
+        if (q.n == 0) continue;
+        sum += q.n * d[i];
+        if (d[i] > longest) longest = d[i];
+        if (shortest == 0.f || d[i] < shortest) shortest = d[i];
+      }
+      const int cap = alone ? 256 : 512;
+      float t = count <= cap ? longest : sum / cap + 0.5f * shortest;
+      if (t < longest) t = longest;
+      if (t < read) t = read;
+      if (g.joins) t += kCost.join + join;
+      if (best.tile == 0 || t < least) {
+        best = g;
+        least = t;
+        for (int i = 0; i < 3; ++i) took[i] = d[i];
+      }
+    }
+  for (int i = 0; i < 2; ++i)                    // longest first
+    for (int j = 0; j < 2 - i; ++j)
+      if (took[j] < took[j + 1]) {
+        std::swap(took[j], took[j + 1]);
+        std::swap(best.p[j], best.p[j + 1]);
+      }
+  best.blocks = 0;
+  for (const GradsPart& q : best.p) best.blocks += q.per * kXcds;
+  return best;
+}
+
 }  // namespace
 
 size_t mok_ffn_part_bytes(const mok_ffn_args& a, mok_ffn_op op) {
@@ -496,9 +645,26 @@ hipError_t mok_launch_ffn(const mok_ffn_args& a, mok_ffn_op op, int act, hipStre
     case FFN_GATEUP: return act == 0 ? launch<FFN_GATEUP, 0>(a, p, st) : launch<FFN_GATEUP, 1>(a, p, st);
     case FFN_DOWN: return launch<FFN_DOWN, 0>(a, p, st);
     case FFN_DH: return act == 0 ? launch<FFN_DH, 0>(a, p, st) : launch<FFN_DH, 1>(a, p, st);
-    case FFN_DWD: return launch<FFN_DWD, 0>(a, p, st);
-    case FFN_DWGU: return launch<FFN_DWGU, 0>(a, p, st);
-    case FFN_DX: return launch<FFN_DX, 0>(a, p, st);
     default: return hipErrorInvalidValue;
   }
+}
+
+size_t mok_ffn_grads_part_bytes(const mok_ffn_args& a) { return (size_t)grads_plan(a).part * 4; }
+
+hipError_t mok_launch_ffn_grads(const mok_ffn_args& a, hipStream_t st) {
+  const GradsPlan g = grads_plan(a);
+  const int count = g.p[0].n + g.p[1].n + g.p[2].n;
+  const dim3 grid((unsigned)g.blocks);
+  if (g.tile == 256)
+    hipLaunchKernelGGL((ffn_grads_kernel<256, 0>), grid, dim3(kPpThreads), 0, st, a, g);
+  else if (count <= 256)
+    hipLaunchKernelGGL((ffn_grads_kernel<128, 4>), grid, dim3(kThreads128<4>), 0, st, a, g);
+  else
+    hipLaunchKernelGGL((ffn_grads_kernel<128, 2>), grid, dim3(kThreads128<2>), 0, st, a, g);
+  if (g.joins) {
+    const dim3 jgrid((unsigned)(g.tile * g.tile / 8 / kThreads), (unsigned)g.joins);
+    if (g.tile == 256) hipLaunchKernelGGL((ffn_grads_join_kernel<256>), jgrid, dim3(kThreads), 0, st, a, g);
+    else hipLaunchKernelGGL((ffn_grads_join_kernel<128>), jgrid, dim3(kThreads), 0, st, a, g);
+  }
+  return hipGetLastError();
 }

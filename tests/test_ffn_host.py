@@ -62,13 +62,40 @@ def test_ffn_calls_refuse_before_any_launch():
     assert fwd(p=m, n=nm, w=wm, ctx=FAKE) == UNS
     assert fwd(p=m, n=nm - 1, w=wm) == SMALL
 
-    def bwd(p=p, ctx=FAKE, x=FAKE, w=w, dy=FAKE, dx=FAKE, g=FAKE, u=FAKE, d=FAKE, n=ws):
+    far = ctypes.c_void_p(0x100000000)
+
+    def bwd(p=p, ctx=FAKE, x=FAKE, w=w, dy=FAKE, dx=far, g=FAKE, u=FAKE, d=FAKE, n=ws):
         return L.mok_ffn_backward(ctypes.byref(p), ctx, x, ctypes.byref(w), dy, dx, g, u, d, FAKE, n, None)
 
     for k in ("ctx", "x", "dy", "dx", "g", "u", "d"):
         assert bwd(**{k: None}) == INV, k
         assert bwd(**{k: odd}) == INV, k
     assert bwd(n=16) == SMALL and bwd(p=m, w=wm) == UNS
+
+
+def test_dx_that_overlaps_x_or_dy_is_refused():
+    L = mok.lib()
+    w = mok.Weights(0x1000, 0x1000, 0x1000)
+    T, H = 5, 64
+
+    def bwd(dx, x=1 << 32, dy=1 << 33, ld_x=0, ld_y=0, T=T):
+        p = mok.make_ffn_problem(T, H, 64, ld_x=ld_x, ld_y=ld_y)
+        v = ctypes.c_void_p
+        return L.mok_ffn_backward(ctypes.byref(p), FAKE, v(x), ctypes.byref(w), v(dy), v(dx), FAKE, FAKE, FAKE, FAKE,
+                                  16, None)
+
+    for base in ("x", "dy"):
+        at = {"x": 1 << 32, "dy": 1 << 33}[base]
+        for off in (0, 16, -16, 2 * T * H - 16, -(2 * T * H - 16)):
+            assert bwd(at + off) == INV, (base, off)
+        for off in (2 * T * H, -2 * T * H):
+            assert bwd(at + off) == SMALL, (base, off)
+    # rows of 160: x in columns 0 .. 63, dx beside it, or across the next row's start
+    assert [bwd((1 << 32) + 2 * c, ld_x=160) for c in (56, 64, 96, 104, -64, -96, 152, 160)] == [
+        INV, SMALL, SMALL, INV, SMALL, SMALL, INV, INV]
+    assert bwd((1 << 33) + 2 * 64, ld_x=160) == INV            # another pitch than dy's: taken to overlap
+    assert bwd((1 << 33) + 2 * 64, ld_x=160, ld_y=160) == SMALL
+    assert bwd((1 << 32) + 2 * 64, ld_x=160, T=1) == SMALL
 
 
 @pytest.mark.parametrize("kw,status", [

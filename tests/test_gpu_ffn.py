@@ -30,10 +30,11 @@ def case(T, H, I, seed=0):
 
 
 # one token to a few thousand; sizes below a tile, of whole tiles, just past them, of a single 8; the
-# products of the last rows run as 256 x 256 tiles, those of the others as 128 x 128, split along K or not
+# products of the last rows run as 256 x 256 tiles (the weight gradients of the very last split along K),
+# those of the others as 128 x 128, split along K or not
 SHAPES = [(1, 8, 8), (1, 256, 512), (2, 1000, 712), (16, 2048, 768), (17, 264, 520), (32, 1024, 136), (33, 264, 520),
           (64, 7168, 256), (128, 128, 128), (129, 136, 72), (257, 8, 2048), (300, 2048, 768), (513, 4096, 8),
-          (777, 1000, 712), (1031, 520, 264), (4100, 520, 2056), (2049, 2312, 1096)]
+          (777, 1000, 712), (1031, 520, 264), (4100, 520, 2056), (2049, 2312, 1096), (4671, 3032, 64)]
 
 
 @pytest.mark.parametrize("T,H,I", SHAPES)
@@ -272,7 +273,8 @@ def test_binding_refuses():
 
 @pytest.mark.parametrize("T,H,I", [(3, 256, 128), (200, 256, 128), (2500, 2048, 768), (4100, 2048, 768)])
 def test_outputs_in_place_of_inputs(T, H, I):
-    """y over x (as residual too), dx over x and over dy: the same bits as in buffers of their own."""
+    """y over x (as residual too): the same bits as in a buffer of its own. dx beside x in the same rows is fine;
+    any overlap with x or dy, which are read while it is written, is refused."""
     import torch
     c = {k: bf(v) for k, v in case(T, H, I).items()}
     w = (c["wg"], c["wu"], c["wd"])
@@ -282,11 +284,22 @@ def test_outputs_in_place_of_inputs(T, H, I):
     over = c["x"].clone()
     F.run_ffn_forward(ws, over, w, residual=over, y=over)
     assert torch.equal(over, y)
-    for over in ("x", "dy"):
-        a = dict(x=c["x"].clone(), dy=c["dy"].clone())
-        g = [torch.empty_like(t) for t in dw]
-        mok.ffn_backward(ws.problem, ws.ctx, a["x"], w, a["dy"], a[over], *g, ws.workspace)
-        assert torch.equal(a[over], dx) and all(torch.equal(p, q) for p, q in zip(g, dw)), over
+
+    def back(x, dy, dx):
+        g = [torch.full_like(t, float("nan")) for t in dw]
+        mok.ffn_backward(ws.problem, ws.ctx, x, w, dy, dx, *g, ws.workspace)
+        return g
+
+    for kw in (dict(x=c["x"], dy=c["dy"], dx=c["x"]), dict(x=c["x"], dy=c["dy"], dx=c["dy"])):
+        with pytest.raises(mok.MokError) as e:
+            back(**kw)
+        assert e.value.status == mok.MOK_ERR_INVALID_ARG
+    wide = torch.zeros((T, 2 * H), dtype=torch.bfloat16, device="cuda")
+    wide[:, :H] = c["x"]
+    g = back(wide[:, :H], c["dy"], wide[:, H:])
+    assert torch.equal(wide[:, H:], dx) and all(torch.equal(p, q) for p, q in zip(g, dw))
+    with pytest.raises(mok.MokError):
+        back(wide[:, :H], c["dy"], wide[:, 8:H + 8])
 
 
 def test_offsets_past_32_bits():
