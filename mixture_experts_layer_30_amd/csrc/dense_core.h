@@ -549,7 +549,7 @@ MOK_DEV void dense_tile(int i, int nr, int nc, int grp, int& row, int& col) {
 // per slot, of which a 128 x 128 tile with a CU to itself needs the share `alone`; all
 // slots take at least as long as reading the operands; partial sums add a launch and the traffic of writing and reading them. With the
 // constants fitted to 280 shapes of 33 to 8192 rows, each timed with both tiles and up
-// to 8 splits, the choice was within 1% of the fastest in the mean and 20% at worst.
+// to 8 splits, the choice was within 1% of the fastest in the mean and 18% at worst.
 struct dense_cost {
   float fix256, slot256, fix128, slot128, alone; // us
   float join, rate;                              // us, bytes per us

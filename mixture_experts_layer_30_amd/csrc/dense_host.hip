@@ -222,6 +222,10 @@ mok_status mok_ffn_backward(const mok_ffn_problem* problem, const void* ctx, con
     if (!aligned(p, 16)) return MOK_ERR_INVALID_ARG;
   if (rows_overlap(dx, r.ldx, x, r.ldx, r.T, r.H) || rows_overlap(dx, r.ldx, dy, r.ldy, r.T, r.H))
     return MOK_ERR_INVALID_ARG;
+  const void* mats[] = {dw_gate, dw_up, dw_down, weights->w_gate, weights->w_up, weights->w_down};
+  for (int i = 0; i < 3; ++i)                    // no gradient over another, or over a weight
+    for (int j = i + 1; j < 6; ++j)
+      if (rows_overlap(mats[i], r.H, mats[j], r.H, r.I, r.H)) return MOK_ERR_INVALID_ARG;
   const FfnBwdWs W = bwd_ws(r);
   if (r.T > 0 && (!workspace || workspace_bytes < ffn_ws_bytes(r))) return MOK_ERR_BUFFER_TOO_SMALL;
   if ((s = check_device()) != MOK_OK) return s;

@@ -5,7 +5,7 @@
 //   dWd = dy^T h        dWg = da^T x              dWu = db^T x        dx = da Wg + db Wu
 //
 // Both projections, the gate and the product are one launch; so are dh with the
-// gate's backward, dWg with dWu, and the two terms of dx (one sum over 2I).
+// gate's backward, and the weight gradients with dx (its two terms one sum over 2I).
 // Sums are fp32 in ascending K (split products: fp32 partial sums, added in
 // ascending order), so results are bitwise reproducible. Rounded to bf16: y, the
 // saved a and b, and the operands of the next product, h, da and db (the matrix

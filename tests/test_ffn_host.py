@@ -62,15 +62,34 @@ def test_ffn_calls_refuse_before_any_launch():
     assert fwd(p=m, n=nm, w=wm, ctx=FAKE) == UNS
     assert fwd(p=m, n=nm - 1, w=wm) == SMALL
 
-    far = ctypes.c_void_p(0x100000000)
+    far, *grads = (ctypes.c_void_p(k << 32) for k in (1, 2, 3, 4))
 
-    def bwd(p=p, ctx=FAKE, x=FAKE, w=w, dy=FAKE, dx=far, g=FAKE, u=FAKE, d=FAKE, n=ws):
+    def bwd(p=p, ctx=FAKE, x=FAKE, w=w, dy=FAKE, dx=far, g=grads[0], u=grads[1], d=grads[2], n=ws):
         return L.mok_ffn_backward(ctypes.byref(p), ctx, x, ctypes.byref(w), dy, dx, g, u, d, FAKE, n, None)
 
     for k in ("ctx", "x", "dy", "dx", "g", "u", "d"):
         assert bwd(**{k: None}) == INV, k
         assert bwd(**{k: odd}) == INV, k
     assert bwd(n=16) == SMALL and bwd(p=m, w=wm) == UNS
+
+
+def test_weight_gradients_that_overlap_are_refused():
+    L = mok.lib()
+    p = mok.make_ffn_problem(4, 64, 32)
+    n = 2 * 64 * 32
+    v = ctypes.c_void_p
+
+    def bwd(**kw):
+        a = dict(g=1 << 32, u=2 << 32, d=3 << 32, wg=4 << 32, wu=5 << 32, wd=6 << 32)
+        a.update(kw)
+        w = mok.Weights(a["wg"], a["wu"], a["wd"])
+        return L.mok_ffn_backward(ctypes.byref(p), FAKE, v(7 << 32), ctypes.byref(w), v(8 << 32), v(9 << 32), v(a["g"]),
+                                  v(a["u"]), v(a["d"]), FAKE, 16, None)
+
+    assert bwd() == SMALL
+    for k, at in (("u", 1), ("d", 1), ("d", 2), ("g", 4), ("g", 5), ("g", 6), ("u", 5), ("d", 6)):
+        assert bwd(**{k: at << 32}) == INV and bwd(**{k: (at << 32) + n - 16}) == INV, (k, at)
+        assert bwd(**{k: (at << 32) + n}) == SMALL and bwd(**{k: (at << 32) - n}) == SMALL, (k, at)
 
 
 def test_dx_that_overlaps_x_or_dy_is_refused():
@@ -81,8 +100,8 @@ def test_dx_that_overlaps_x_or_dy_is_refused():
     def bwd(dx, x=1 << 32, dy=1 << 33, ld_x=0, ld_y=0, T=T):
         p = mok.make_ffn_problem(T, H, 64, ld_x=ld_x, ld_y=ld_y)
         v = ctypes.c_void_p
-        return L.mok_ffn_backward(ctypes.byref(p), FAKE, v(x), ctypes.byref(w), v(dy), v(dx), FAKE, FAKE, FAKE, FAKE,
-                                  16, None)
+        return L.mok_ffn_backward(ctypes.byref(p), FAKE, v(x), ctypes.byref(w), v(dy), v(dx), v(5 << 32), v(6 << 32),
+                                  v(7 << 32), FAKE, 16, None)
 
     for base in ("x", "dy"):
         at = {"x": 1 << 32, "dy": 1 << 33}[base]
