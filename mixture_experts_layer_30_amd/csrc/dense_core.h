@@ -607,7 +607,9 @@ MOK_DEV void gate_act_grad(float a, float& act, float& dact) {
   } else {
     const float s = sigmoidf_(1.5957691216057308f * (a + 0.044715f * a * a * a));
     act = a * s;
-    dact = s + act * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * a * a);
+    // (from |a| = 16 on act or 1 - s is 0 in fp32: a*a, which passes the largest number at 1.8e19, is held there)
+    const float p = __builtin_amdgcn_fmed3f(a, -16.0f, 16.0f);
+    dact = s + act * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * p * p);
   }
 }
 

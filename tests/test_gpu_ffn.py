@@ -359,3 +359,29 @@ def test_another_current_device_is_not_touched():
     with pytest.raises(mok.MokError):
         mok.ffn_forward(ws.problem, c["x"], (c["wg"], c["wu"], c["wd"]), torch.empty_like(c["x"]),
                         ws.workspace.cpu())
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_gates_far_out(kind):
+    """Saved pre-activations up to bf16's largest: from |a| = 200 on both gates are a or 0 in fp32 and their
+    derivatives 1 or 0. Identities for x, w_gate and w_down and powers of two elsewhere make dx, dw_gate and dw_up
+    one product each without a rounding; dw_down, a sum of up to 64 terms of up to 0.5 * 0.5 * 3.3e38 and none
+    below 0, may pass the largest number, and is no NaN."""
+    import torch
+    n = 64
+    g = torch.Generator(device="cuda").manual_seed(11)
+    eye = torch.eye(n, device="cuda").bfloat16()
+    zero = torch.zeros_like(eye)
+    dy = torch.exp2(-torch.randint(1, 5, (n, n), generator=g, device="cuda").float()).bfloat16()
+    far = torch.tensor([200.0, 1e3, 1e10, 1.8e19, 2e19, 4e19, 6e19, 1e25, 1e38, 3.3e38], device="cuda").bfloat16()
+    far = torch.cat([far, -far])
+    a = far[torch.randint(0, far.numel(), (n, n), generator=g, device="cuda")]
+    b = torch.full_like(a, 0.5)
+    ws = F.get_ffn_workspace(n, n, n, activation=ACT[kind])
+    ws.ctx = torch.cat([a, b], 1)
+    dx, dwg, dwu, dwd = F.run_ffn_backward(ws, eye, (eye, zero, eye), dy)
+    torch.cuda.synchronize()
+    on = a > 0
+    assert torch.equal(dwg.t(), torch.where(on, dy * b, zero)) and torch.equal(dx, torch.where(on, dy * b, zero))
+    assert torch.equal(dwu.t(), torch.where(on, dy * a, zero))
+    assert not dwd.isnan().any()
