@@ -167,6 +167,8 @@ mok_status mok_ffn_forward(const mok_ffn_problem* problem, const void* x, const 
   if (r.T > 0 && (!x || !y)) return MOK_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(ctx, 16) || !aligned(workspace, 16))
     return MOK_ERR_INVALID_ARG;
+  // (a workgroup reads the residual of its own part of y alone before it stores that)
+  if (residual && residual != y && rows_overlap(y, r.ldy, residual, r.ldy, r.T, r.H)) return MOK_ERR_INVALID_ARG;
   const FfnWs W = fwd_ws(r);
   if (r.T > 0 && (!workspace || workspace_bytes < ffn_ws_bytes(r))) return MOK_ERR_BUFFER_TOO_SMALL;
   if ((s = check_device()) != MOK_OK) return s;

@@ -166,3 +166,25 @@ def test_binding_refuses_tensors_off_the_gpu():
     with pytest.raises(mok.MokError) as e:
         mok.ffn_forward(p, x, w, x, torch.zeros(16, dtype=torch.uint8))
     assert e.value.status == INV
+
+
+def test_residual_that_overlaps_y_in_part_is_refused():
+    """y over another part of the residual's rows: one workgroup would overwrite what another still reads."""
+    L = mok.lib()
+    w = mok.Weights(4 << 32, 5 << 32, 6 << 32)
+    wm = mok.Weights(*(k << 32 for k in range(4, 10)))
+    T, H, y = 5, 128, 1 << 32
+
+    def fwd(res, ld_y=0, dtype=mok.MOK_BF16):
+        p = mok.make_ffn_problem(T, H, 128, dtype, ld_y=ld_y)
+        n, _ = mok.ffn_buffer_sizes(p)
+        v = ctypes.c_void_p
+        return L.mok_ffn_forward(ctypes.byref(p), v(2 << 32), ctypes.byref(wm if dtype == mok.MOK_MXFP4 else w), v(res),
+                                 v(y), None, v(3 << 32), n, None)
+
+    for dtype in (mok.MOK_BF16, mok.MOK_MXFP4):
+        for off in (16, -16, 2 * H, -2 * H, 2 * T * H - 16, 16 - 2 * T * H):
+            assert fwd(y + off, dtype=dtype) == INV, off
+        # rows of 320: windows that share columns, and one that reaches over the next row's start
+        for c in (8, 120, -8, 200, 320, 328):
+            assert fwd(y + 2 * c, 320, dtype) == INV, c

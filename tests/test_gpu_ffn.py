@@ -385,3 +385,23 @@ def test_gates_far_out(kind):
     assert torch.equal(dwg.t(), torch.where(on, dy * b, zero)) and torch.equal(dx, torch.where(on, dy * b, zero))
     assert torch.equal(dwu.t(), torch.where(on, dy * a, zero))
     assert not dwd.isnan().any()
+
+
+@pytest.mark.parametrize("T,H,I", [(3, 256, 128), (200, 256, 128), (4100, 2048, 768)])
+def test_residual_beside_y(T, H, I):
+    """The residual in the same rows as y, or right behind it, is no overlap: the bits of separate buffers. A
+    window that shares columns with y is refused."""
+    import torch
+    c = {k: bf(v) for k, v in case(T, H, I, 6).items()}
+    w = (c["wg"], c["wu"], c["wd"])
+    ws = F.get_ffn_workspace(T, H, I, training=False)
+    want = F.run_ffn_forward(ws, c["x"], w, residual=c["res"])
+    wide = torch.zeros((T, 2 * H), dtype=torch.bfloat16, device="cuda")
+    flat = torch.zeros((2 * T, H), dtype=torch.bfloat16, device="cuda")
+    for y, res in ((wide[:, :H], wide[:, H:]), (wide[:, H:], wide[:, :H]), (flat[:T], flat[T:]), (flat[T:], flat[:T])):
+        res.copy_(c["res"])
+        F.run_ffn_forward(ws, c["x"], w, residual=res, y=y)
+        assert torch.equal(y, want) and torch.equal(res, c["res"])
+    with pytest.raises(mok.MokError) as e:
+        F.run_ffn_forward(ws, c["x"], w, residual=wide[:, 8:H + 8], y=wide[:, :H])
+    assert e.value.status == mok.MOK_ERR_INVALID_ARG
