@@ -417,8 +417,11 @@ mok_status mok_ffn_buffer_sizes(const mok_ffn_problem* problem, size_t* workspac
 /* residual NULL = none, and may be y itself (y += block(x)): the routed
  * layer's output goes in here and the shared expert is added before the one
  * rounding. Any other overlap of the two is refused (MOK_ERR_INVALID_ARG; rows
- * side by side in one matrix do not overlap). ctx NULL for inference. Columns H .. ld_y-1 of y are not touched.
- * y may be x. x and y may be NULL when T = 0. */
+ * side by side in one matrix do not overlap). y may be x. ctx NULL for
+ * inference. Columns H .. ld_y-1 of y are not touched. y, ctx and the workspace
+ * share no memory with the weights or each other, nor ctx and the workspace
+ * with x or the residual (MOK_ERR_INVALID_ARG; rows with a pitch count from
+ * their first to their last element). x and y may be NULL when T = 0. */
 mok_status mok_ffn_forward(const mok_ffn_problem* problem, const void* x, const mok_weights* weights,
                            const void* residual, void* y, void* ctx, void* workspace, size_t workspace_bytes,
                            void* stream);

@@ -119,6 +119,33 @@ bool rows_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_
   return m < H || m > lda - H;
 }
 
+struct Span {
+  const void* p;
+  size_t n;                                      // bytes (rows with a pitch: from the first to the last)
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && (x < y ? y - x < a.n : x - y < b.n);
+}
+Span rows_span(const void* p, int64_t T, int64_t H, int64_t ld) { return {p, (size_t)((T - 1) * ld + H) * 2}; }
+
+// whether memory that a forward writes (y, ctx, the workspace) is also memory of another
+// operand of it that it reads or writes; y over x or the residual is not looked at here
+bool fwd_overlap(const Ffn& r, const void* x, const mok_weights& w, const void* res, const void* y, const void* ctx,
+                 const void* ws, size_t ws_bytes) {
+  const size_t m = (size_t)r.H * r.I, wb = r.mx ? m / 2 : m * 2, sb = r.mx ? m / 32 : 0;
+  const Span sy = rows_span(y, r.T, r.H, r.ldy), sc = {ctx, ffn_ctx_bytes(r)}, sw = {ws, ws_bytes};
+  for (const Span& o : {sy, sc, sw})
+    for (const Span& i : {Span{w.w_gate, wb}, Span{w.w_up, wb}, Span{w.w_down, wb}, Span{sb ? w.s_gate : nullptr, sb},
+                          Span{sb ? w.s_up : nullptr, sb}, Span{sb ? w.s_down : nullptr, sb}})
+      if (overlap(o, i)) return true;
+  const Span sx = rows_span(x, r.T, r.H, r.ldx), sr = rows_span(res, r.T, r.H, r.ldy);
+  for (const Span& o : {sc, sw})
+    for (const Span& i : {sx, sr, sy})
+      if (overlap(o, i)) return true;
+  return overlap(sc, sw);
+}
+
 mok_status ffn_weights(const Ffn& r, const mok_weights* w) {
   if (!w || !w->w_gate || !w->w_up || !w->w_down) return MOK_ERR_INVALID_ARG;
   if (!aligned(w->w_gate, 16) || !aligned(w->w_up, 16) || !aligned(w->w_down, 16)) return MOK_ERR_INVALID_ARG;
@@ -170,7 +197,9 @@ mok_status mok_ffn_forward(const mok_ffn_problem* problem, const void* x, const 
   // (a workgroup reads the residual of its own part of y alone before it stores that)
   if (residual && residual != y && rows_overlap(y, r.ldy, residual, r.ldy, r.T, r.H)) return MOK_ERR_INVALID_ARG;
   const FfnWs W = fwd_ws(r);
-  if (r.T > 0 && (!workspace || workspace_bytes < ffn_ws_bytes(r))) return MOK_ERR_BUFFER_TOO_SMALL;
+  const size_t need = ffn_ws_bytes(r);
+  if (r.T > 0 && (!workspace || workspace_bytes < need)) return MOK_ERR_BUFFER_TOO_SMALL;
+  if (r.T > 0 && fwd_overlap(r, x, *weights, residual, y, ctx, workspace, need)) return MOK_ERR_INVALID_ARG;
   if ((s = check_device()) != MOK_OK) return s;
   if (r.T == 0) return MOK_OK;
   hipStream_t st = (hipStream_t)stream;

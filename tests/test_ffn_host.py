@@ -188,3 +188,35 @@ def test_residual_that_overlaps_y_in_part_is_refused():
         # rows of 320: windows that share columns, and one that reaches over the next row's start
         for c in (8, 120, -8, 200, 320, 328):
             assert fwd(y + 2 * c, 320, dtype) == INV, c
+
+
+@pytest.mark.parametrize("dtype", [mok.MOK_BF16, mok.MOK_MXFP4])
+def test_forward_outputs_over_other_operands_are_refused(dtype):
+    """y over the weights, ctx over anything, the workspace over anything: one launch would read what another
+    workgroup of it, or the launch before, has overwritten. At the first byte of the other operand and at its last 16."""
+    L = mok.lib()
+    mx = dtype == mok.MOK_MXFP4
+    T, H, I = 5, 128, 256
+    p = mok.make_ffn_problem(T, H, I, dtype)
+    n, nctx = mok.ffn_buffer_sizes(p)
+    v = ctypes.c_void_p
+    size = dict(x=2 * T * H, y=2 * T * H, res=2 * T * H, ctx=nctx, ws=n)
+    size.update({k: H * I // 2 if mx else 2 * H * I for k in ("wg", "wu", "wd")})
+    if mx:
+        size.update({k: H * I // 32 for k in ("sg", "su", "sd")})
+    where = {k: (i + 1) << 32 for i, k in enumerate(size)}
+
+    def fwd(**kw):
+        a = dict(where, **kw)
+        w = mok.Weights(a["wg"], a["wu"], a["wd"], *((a["sg"], a["su"], a["sd"]) if mx else ()))
+        return L.mok_ffn_forward(ctypes.byref(p), v(a["x"]), ctypes.byref(w), v(a["res"]), v(a["y"]),
+                                 None if mx else v(a["ctx"]), v(a["ws"]), n, None)
+
+    weights = [k for k in size if k[0] in "ws" and k != "ws"]
+    others = {"y": weights, "ws": ["x", "y", "res"] + weights}
+    if not mx:
+        others["ctx"] = ["x", "y", "res", "ws"] + weights
+    for out, ks in others.items():
+        for k in ks:
+            for at in (where[k], where[k] + size[k] - 16, where[k] - size[out] + 16):
+                assert fwd(**{out: at}) == INV, (out, k, at - where[k])
