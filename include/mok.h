@@ -428,9 +428,9 @@ mok_status mok_ffn_forward(const mok_ffn_problem* problem, const void* x, const 
 
 /* Gradients of <dy, y> from the forward's x and ctx: dx [T][H], dw_gate, dw_up
  * [I][H], dw_down [H][I] (bf16, overwritten; the residual's gradient is dy).
- * dx shares no memory with x or dy, and the weight gradients none with each
- * other or the weights (MOK_ERR_INVALID_ARG); nor may any output with another
- * input, or with the workspace.
+ * Neither an output nor the workspace shares memory with another operand
+ * (MOK_ERR_INVALID_ARG; rows of dx beside those of x or dy in one matrix do not
+ * overlap).
  * With T = 0 the weight gradients are zeros and the other pointers may be NULL.
  * MOK_MXFP4: MOK_ERR_UNSUPPORTED. */
 mok_status mok_ffn_backward(const mok_ffn_problem* problem, const void* ctx, const void* x,

@@ -146,6 +146,23 @@ bool fwd_overlap(const Ffn& r, const void* x, const mok_weights& w, const void* 
   return overlap(sc, sw);
 }
 
+// the same for what a backward writes: dx, the weight gradients and the workspace (dx over x or dy:
+// rows_overlap)
+bool bwd_overlap(const Ffn& r, const void* ctx, const void* x, const mok_weights& w, const void* dy, const void* dx,
+                 const void* dwg, const void* dwu, const void* dwd, const void* ws, size_t ws_bytes) {
+  const size_t m = (size_t)r.H * r.I * 2;
+  const Span sdx = rows_span(dx, r.T, r.H, r.ldx), sx = rows_span(x, r.T, r.H, r.ldx), sc = {ctx, ffn_ctx_bytes(r)},
+             sdy = rows_span(dy, r.T, r.H, r.ldy), sw = {ws, ws_bytes};
+  const Span grads[3] = {{dwg, m}, {dwu, m}, {dwd, m}}, weights[3] = {{w.w_gate, m}, {w.w_up, m}, {w.w_down, m}};
+  if (overlap(sdx, sc) || overlap(sw, sc) || overlap(sw, sx) || overlap(sw, sdy) || overlap(sw, sdx)) return true;
+  for (int i = 0; i < 3; ++i) {
+    if (overlap(sdx, weights[i]) || overlap(sw, weights[i])) return true;
+    for (const Span& o : {sx, sdy, sc, sdx, sw})
+      if (overlap(grads[i], o)) return true;
+  }
+  return false;
+}
+
 mok_status ffn_weights(const Ffn& r, const mok_weights* w) {
   if (!w || !w->w_gate || !w->w_up || !w->w_down) return MOK_ERR_INVALID_ARG;
   if (!aligned(w->w_gate, 16) || !aligned(w->w_up, 16) || !aligned(w->w_down, 16)) return MOK_ERR_INVALID_ARG;
@@ -258,7 +275,10 @@ mok_status mok_ffn_backward(const mok_ffn_problem* problem, const void* ctx, con
     for (int j = i + 1; j < 6; ++j)
       if (rows_overlap(mats[i], r.H, mats[j], r.H, r.I, r.H)) return MOK_ERR_INVALID_ARG;
   const FfnBwdWs W = bwd_ws(r);
-  if (r.T > 0 && (!workspace || workspace_bytes < ffn_ws_bytes(r))) return MOK_ERR_BUFFER_TOO_SMALL;
+  const size_t need = ffn_ws_bytes(r);
+  if (r.T > 0 && (!workspace || workspace_bytes < need)) return MOK_ERR_BUFFER_TOO_SMALL;
+  if (r.T > 0 && bwd_overlap(r, ctx, x, *weights, dy, dx, dw_gate, dw_up, dw_down, workspace, need))
+    return MOK_ERR_INVALID_ARG;
   if ((s = check_device()) != MOK_OK) return s;
   hipStream_t st = (hipStream_t)stream;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

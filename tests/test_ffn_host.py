@@ -220,3 +220,29 @@ def test_forward_outputs_over_other_operands_are_refused(dtype):
         for k in ks:
             for at in (where[k], where[k] + size[k] - 16, where[k] - size[out] + 16):
                 assert fwd(**{out: at}) == INV, (out, k, at - where[k])
+
+
+def test_backward_outputs_over_other_operands_are_refused():
+    """What the header forbids for dx, the weight gradients and the workspace, at the first byte of the other
+    operand and at its last 16."""
+    L = mok.lib()
+    T, H, I = 5, 128, 256
+    p = mok.make_ffn_problem(T, H, I)
+    n, nctx = mok.ffn_buffer_sizes(p)
+    v = ctypes.c_void_p
+    size = dict(x=2 * T * H, dy=2 * T * H, dx=2 * T * H, ctx=nctx, ws=n)
+    size.update({k: 2 * H * I for k in ("wg", "wu", "wd", "dwg", "dwu", "dwd")})
+    where = {k: (i + 1) << 32 for i, k in enumerate(size)}
+
+    def bwd(**kw):
+        a = dict(where, **kw)
+        w = mok.Weights(a["wg"], a["wu"], a["wd"])
+        return L.mok_ffn_backward(ctypes.byref(p), v(a["ctx"]), v(a["x"]), ctypes.byref(w), v(a["dy"]), v(a["dx"]),
+                                  v(a["dwg"]), v(a["dwu"]), v(a["dwd"]), v(a["ws"]), n, None)
+
+    for out in ("dx", "ws", "dwg", "dwu", "dwd"):
+        for k in size:
+            if k == out:
+                continue
+            for at in (where[k], where[k] + size[k] - 16, where[k] - size[out] + 16):
+                assert bwd(**{out: at}) == INV, (out, k, at - where[k])
