@@ -350,14 +350,15 @@ mok_status mok_router_backward(const mok_problem* problem, const mok_config* con
  * q = E2M1(v * 2^(127-s)), round to nearest even, saturating at 6, the sign of
  * a zero kept. A block with a NaN or an infinity gets scale 255 (NaN) and zero
  * codes. K must be a multiple of 32; rows >= 0; src 16-byte and q 4-byte
- * aligned; rows * K <= 2^38 (MOK_ERR_UNSUPPORTED). */
+ * aligned; rows * K <= 2^38 (MOK_ERR_UNSUPPORTED). src, q and scales share no
+ * memory (MOK_ERR_INVALID_ARG). */
 mok_status mok_mxfp4_quantize(const void* src, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
                               void* stream);
 
 /* The values the codes stand for: dst [rows][K] bf16 = E2M1 * 2^(s-127), exact
  * (a block of scale 255 is NaN; values above bf16's range, which the quantizer
  * never writes, become infinities). Sizes and limits as mok_mxfp4_quantize,
- * dst 16-byte aligned. */
+ * dst 16-byte aligned and apart from q and scales. */
 mok_status mok_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, void* dst,
                                 void* stream);
 
@@ -368,7 +369,9 @@ mok_status mok_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t
  * makes its row of D (or, in B, its column) NaN. K a multiple of 128 and at
  * most 2^20 (MOK_ERR_UNSUPPORTED otherwise); M, N >= 0, any value up to 2^30
  * with ceil(M/128) * ceil(N/128) <= 2^23 (MOK_ERR_UNSUPPORTED); a and b 16-byte, scales 4-byte aligned; D may start and step anywhere.
- * Columns N .. ld_d-1 of D are not touched. */
+ * Columns N .. ld_d-1 of D are not touched. Neither D (from its first to its
+ * last element) nor the workspace shares memory with another operand
+ * (MOK_ERR_INVALID_ARG). */
 typedef struct {
   int64_t M, N, K;
   int64_t ld_d;

@@ -125,7 +125,7 @@ struct Span {
 };
 bool overlap(const Span& a, const Span& b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && (x < y ? y - x < a.n : x - y < b.n);
+  return a.p && b.p && a.n && b.n && (x < y ? y - x < a.n : x - y < b.n);
 }
 Span rows_span(const void* p, int64_t T, int64_t H, int64_t ld) { return {p, (size_t)((T - 1) * ld + H) * 2}; }
 
@@ -310,6 +310,9 @@ mok_status mok_mxfp4_quantize(const void* src, int64_t rows, int64_t K, uint8_t*
   if (rows > 0 && (!src || !q || !scales)) return MOK_ERR_INVALID_ARG;
   if (!aligned(src, 16) || !aligned(q, 4)) return MOK_ERR_INVALID_ARG;
   if (K > ((int64_t)1 << 38) || rows > ((int64_t)1 << 38) / K) return MOK_ERR_UNSUPPORTED;
+  const size_t n = (size_t)rows * K;
+  const Span v = {src, n * 2}, c = {q, n / 2}, e = {scales, n / 32};
+  if (overlap(v, c) || overlap(v, e) || overlap(c, e)) return MOK_ERR_INVALID_ARG;
   mok_status s = check_device();
   if (s != MOK_OK) return s;
   hipStream_t st = (hipStream_t)stream;
@@ -324,6 +327,9 @@ mok_status mok_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t
   if (rows > 0 && (!dst || !q || !scales)) return MOK_ERR_INVALID_ARG;
   if (!aligned(dst, 16) || !aligned(q, 4)) return MOK_ERR_INVALID_ARG;
   if (K > ((int64_t)1 << 38) || rows > ((int64_t)1 << 38) / K) return MOK_ERR_UNSUPPORTED;
+  const size_t n = (size_t)rows * K;
+  const Span v = {dst, n * 2}, c = {q, n / 2}, e = {scales, n / 32};
+  if (overlap(v, c) || overlap(v, e)) return MOK_ERR_INVALID_ARG;
   mok_status s = check_device();
   if (s != MOK_OK) return s;
   hipStream_t st = (hipStream_t)stream;
@@ -351,6 +357,14 @@ mok_status mok_mx_matmul(const mok_mx_problem* problem, const uint8_t* a, const 
     return MOK_ERR_INVALID_ARG;
   const size_t need = mok_mx_part_bytes(p, false);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOK_ERR_BUFFER_TOO_SMALL;
+  if (p.M > 0 && p.N > 0) {
+    const size_t K = (size_t)p.K;
+    const Span sd = rows_span(d, p.M, p.N, p.ldd), sw = {workspace, need};
+    for (const Span& i : {Span{a, p.M * (p.a8 ? K : K / 2)}, Span{a_scales, p.M * (K / 32)}, Span{b, p.N * (K / 2)},
+                          Span{b_scales, p.N * (K / 32)}})
+      if (overlap(sd, i) || overlap(sw, i)) return MOK_ERR_INVALID_ARG;
+    if (overlap(sd, sw)) return MOK_ERR_INVALID_ARG;
+  }
   if ((s = check_device()) != MOK_OK) return s;
   if (p.M == 0 || p.N == 0) return MOK_OK;
   p.a = a; p.sa = a_scales; p.b = b; p.sb = b_scales;

@@ -246,3 +246,42 @@ def test_backward_outputs_over_other_operands_are_refused():
                 continue
             for at in (where[k], where[k] + size[k] - 16, where[k] - size[out] + 16):
                 assert bwd(**{out: at}) == INV, (out, k, at - where[k])
+
+
+def test_mx_outputs_over_their_operands_are_refused():
+    L = mok.lib()
+    v = ctypes.c_void_p
+    rows, K = 40, 256
+    size = dict(src=2 * rows * K, q=rows * K // 2, s=rows * K // 32)
+    where = {k: (i + 1) << 32 for i, k in enumerate(size)}
+
+    def quantize(**kw):
+        a = dict(where, **kw)
+        return L.mok_mxfp4_quantize(v(a["src"]), rows, K, v(a["q"]), v(a["s"]), None)
+
+    def dequantize(**kw):
+        a = dict(where, **kw)
+        return L.mok_mxfp4_dequantize(v(a["q"]), v(a["s"]), rows, K, v(a["src"]), None)
+
+    for f, outs in ((quantize, ("q", "s")), (dequantize, ("src",))):
+        for out in outs:
+            for k in size:
+                if k != out:
+                    for at in (where[k], where[k] + size[k] - 16, where[k] - size[out] + 16):
+                        assert f(**{out: at}) == INV, (f.__name__, out, k, at - where[k])
+    M, N = 300, 500
+    p = mok.make_mx_problem(M, N, 4096, mok.MOK_MXFP8)
+    n = mok.mx_matmul_workspace(p)
+    assert n > 0
+    size = dict(a=M * 4096, sa=M * 128, b=N * 2048, sb=N * 128, d=2 * M * N, ws=n)
+    where = {k: (i + 1) << 32 for i, k in enumerate(size)}
+
+    def matmul(**kw):
+        a = dict(where, **kw)
+        return L.mok_mx_matmul(ctypes.byref(p), *(v(a[k]) for k in size), n, None)
+
+    for out in ("d", "ws"):
+        for k in size:
+            if k != out:
+                for at in (where[k], where[k] + size[k] - 16, where[k] - size[out] + 16):
+                    assert matmul(**{out: at}) == INV, (out, k, at - where[k])
