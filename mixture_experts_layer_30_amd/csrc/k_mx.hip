@@ -701,7 +701,8 @@ Plan plan_of(const mok_mx_args& a, bool glu) {
   if (mok_mx_few(a.M)) return Plan{0, 0, 0, 1};
   Plan p;
   const int64_t cols = (glu ? 2 : 1) * (int64_t)a.N;
-  dense_plan(a.M, cols, 1, a.K / (a.a8 ? 128 : 256), a.a8 ? kCost8 : kCost4, &p.tile, &p.splits);
+  const int slot = a.a8 ? 128 : 256;             // of K; the last may be half full
+  dense_plan(a.M, cols, 1, (a.K + slot - 1) / slot, a.a8 ? kCost8 : kCost4, &p.tile, &p.splits);
   p.nr = (a.M + p.tile - 1) / p.tile;
   p.nc = (int)((cols + p.tile - 1) / p.tile);
   return p;

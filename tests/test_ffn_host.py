@@ -285,3 +285,16 @@ def test_mx_outputs_over_their_operands_are_refused():
             if k != out:
                 for at in (where[k], where[k] + size[k] - 16, where[k] - size[out] + 16):
                     assert matmul(**{out: at}) == INV, (out, k, at - where[k])
+
+
+@pytest.mark.parametrize("K", [4480, 6016, 8064])
+def test_a_half_slot_of_k_counts_as_one(K):
+    """MXFP4 products walk 256 of K at a time, the last time 128 where K is an odd multiple of 128: as many slots as
+    at K + 128, and so the same tiles and splits, which the partial tiles' bytes tell."""
+    split = 0
+    for M in (33, 57, 147, 300, 639, 1500):
+        for N in (131, 442, 717, 1418, 4096):
+            at = [mok.mx_matmul_workspace(mok.make_mx_problem(M, N, k, mok.MOK_MXFP4)) for k in (K, K + 128)]
+            assert at[0] == at[1], (M, N, at)
+            split += at[0] > 0
+    assert split
