@@ -409,10 +409,12 @@ typedef struct {
   int32_t dtype;                 /* MOK_BF16 or MOK_MXFP4 */
   int32_t activation;            /* mok_activation */
   int64_t ld_x, ld_y;
+  int32_t forward_only;          /* 1: no backward will be asked for, and the workspace is a forward's alone; else 0 */
 } mok_ffn_problem;
 
-/* [host] Bytes of the caller's buffers: workspace (scratch of either call, one
- * call at a time as mok_mx_matmul's, not monotonic in T) and ctx, what the forward saves for the backward: the
+/* [host] Bytes of the caller's buffers: workspace (scratch of either call, with
+ * forward_only of the forward; one call at a time as mok_mx_matmul's, not
+ * monotonic in T) and ctx, what the forward saves for the backward: the
  * pre-activations [T][2I] bf16, a in columns [0, I), b in [I, 2I) (MOK_MXFP4:
  * 0). */
 mok_status mok_ffn_buffer_sizes(const mok_ffn_problem* problem, size_t* workspace_bytes, size_t* ctx_bytes);
@@ -435,7 +437,7 @@ mok_status mok_ffn_forward(const mok_ffn_problem* problem, const void* x, const 
  * (MOK_ERR_INVALID_ARG; rows of dx beside those of x or dy in one matrix do not
  * overlap).
  * With T = 0 the weight gradients are zeros and the other pointers may be NULL.
- * MOK_MXFP4: MOK_ERR_UNSUPPORTED. */
+ * MOK_MXFP4: MOK_ERR_UNSUPPORTED. A forward_only problem: MOK_ERR_INVALID_ARG. */
 mok_status mok_ffn_backward(const mok_ffn_problem* problem, const void* ctx, const void* x,
                             const mok_weights* weights, const void* dy, void* dx, void* dw_gate, void* dw_up,
                             void* dw_down, void* workspace, size_t workspace_bytes, void* stream);

@@ -70,7 +70,8 @@ class MxProblem(ctypes.Structure):
 
 class FfnProblem(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("I", ctypes.c_int64), ("dtype", ctypes.c_int32),
-                ("activation", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64)]
+                ("activation", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("forward_only", ctypes.c_int32)]
 
 
 _lib = None
@@ -411,8 +412,9 @@ def mx_matmul(problem, a, a_scales, b, b_scales, d, workspace, stream=None):
          b.data_ptr(), b_scales.data_ptr(), d.data_ptr(), *_scratch(workspace, dev))
 
 
-def make_ffn_problem(T, H, I, dtype=MOK_BF16, activation=ACT_SILU, ld_x=0, ld_y=0) -> FfnProblem:
-    return FfnProblem(int(T), int(H), int(I), int(dtype), int(activation), int(ld_x), int(ld_y))
+def make_ffn_problem(T, H, I, dtype=MOK_BF16, activation=ACT_SILU, ld_x=0, ld_y=0, forward_only=False) -> FfnProblem:
+    """forward_only: for forwards alone, whose workspace is smaller; ffn_backward refuses such a problem."""
+    return FfnProblem(int(T), int(H), int(I), int(dtype), int(activation), int(ld_x), int(ld_y), int(forward_only))
 
 
 def ffn_buffer_sizes(problem):
@@ -438,7 +440,8 @@ def _ffn_weights(problem, weights, device):
 
 
 def _ffn_call(problem, ld_x, ld_y):
-    return FfnProblem(problem.T, problem.H, problem.I, problem.dtype, problem.activation, ld_x, ld_y)
+    return FfnProblem(problem.T, problem.H, problem.I, problem.dtype, problem.activation, ld_x, ld_y,
+                      problem.forward_only)
 
 
 def ffn_forward(problem, x, weights, y, workspace, residual=None, ctx=None, stream=None):

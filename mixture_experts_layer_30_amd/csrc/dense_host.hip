@@ -23,7 +23,7 @@ bool tiles_fit(int64_t rows, int64_t cols) { return cdiv(rows, 128) * cdiv(cols,
 
 struct Ffn {
   int64_t T, H, I, ldx, ldy;
-  bool mx;
+  bool mx, fwd_only;
   int act;
 };
 
@@ -31,7 +31,9 @@ mok_status resolve(const mok_ffn_problem* p, Ffn* r) {
   if (!p || p->T < 0 || p->H <= 0 || p->I <= 0) return MOK_ERR_INVALID_ARG;
   if (p->dtype != MOK_BF16 && p->dtype != MOK_MXFP8 && p->dtype != MOK_MXFP4) return MOK_ERR_INVALID_ARG;
   if (p->activation != MOK_ACT_SILU && p->activation != MOK_ACT_GELU_TANH) return MOK_ERR_INVALID_ARG;
+  if (p->forward_only != 0 && p->forward_only != 1) return MOK_ERR_INVALID_ARG;
   r->T = p->T; r->H = p->H; r->I = p->I;
+  r->fwd_only = p->forward_only != 0;
   if (p->dtype == MOK_MXFP8) return MOK_ERR_UNSUPPORTED;
   r->mx = p->dtype == MOK_MXFP4;
   r->act = p->activation;
@@ -106,7 +108,11 @@ FfnBwdWs bwd_ws(const Ffn& r) {
   w.total = o;
   return w;
 }
-size_t ffn_ws_bytes(const Ffn& r) { return std::max(fwd_ws(r).total, r.mx ? (size_t)0 : bwd_ws(r).total); }
+// (a backward's is up to thousands of times a forward's: 22 MB against 4 KB for one token of 7168 x 2048)
+size_t ffn_ws_bytes(const Ffn& r) {
+  const size_t fwd = fwd_ws(r).total;
+  return r.mx || r.fwd_only ? fwd : std::max(fwd, bwd_ws(r).total);
+}
 size_t ffn_ctx_bytes(const Ffn& r) { return r.mx ? 0 : (size_t)r.T * 2 * r.I * 2; }
 
 // whether rows of H elements share memory: T rows at a of pitch lda, and at b of pitch ldb
@@ -262,6 +268,7 @@ mok_status mok_ffn_backward(const mok_ffn_problem* problem, const void* ctx, con
   mok_status s = resolve(problem, &r);
   if (s != MOK_OK) return s;
   if (r.mx) return MOK_ERR_UNSUPPORTED;
+  if (r.fwd_only) return MOK_ERR_INVALID_ARG;
   if ((s = ffn_weights(r, weights)) != MOK_OK) return s;
   if (!dw_gate || !dw_up || !dw_down) return MOK_ERR_INVALID_ARG;
   if (r.T > 0 && (!ctx || !x || !dy || !dx)) return MOK_ERR_INVALID_ARG;

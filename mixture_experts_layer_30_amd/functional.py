@@ -164,8 +164,9 @@ class FfnWorkspace:
 
 
 def get_ffn_workspace(T, H, I, dtype=MOK_BF16, activation=ACT_SILU, device="cuda", training=True):
-    """Allocate the workspace and (training) the saved context of one dense block."""
-    problem = make_ffn_problem(T, H, I, dtype, activation)
+    """Allocate the workspace and (training) the saved context of one dense block; without training, the workspace
+    of forwards alone, and run_ffn_backward refuses it."""
+    problem = make_ffn_problem(T, H, I, dtype, activation, forward_only=not training)
     ws, cb = ffn_buffer_sizes(problem)
     ctx = torch.empty((T, 2 * I), dtype=torch.bfloat16, device=device) if training and dtype == MOK_BF16 else None
     return FfnWorkspace(problem, torch.empty(max(ws, 16), dtype=torch.uint8, device=device), ctx)

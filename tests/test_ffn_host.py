@@ -298,3 +298,26 @@ def test_a_half_slot_of_k_counts_as_one(K):
             assert at[0] == at[1], (M, N, at)
             split += at[0] > 0
     assert split
+
+
+def test_forwards_alone_need_no_workspace_for_a_backward():
+    """forward_only: h and the forward's own partial tiles. One token of 7168 x 2048 has 2048 values of h."""
+    L = mok.lib()
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    for T, H, I in ((1, 7168, 2048), (1, 4096, 1536), (16, 2048, 768), (16384, 7168, 2048)):
+        full, ctx = mok.ffn_buffer_sizes(mok.make_ffn_problem(T, H, I))
+        p = mok.make_ffn_problem(T, H, I, forward_only=True)
+        n, ctx1 = mok.ffn_buffer_sizes(p)
+        assert n == up(2 * T * I) and n < full and ctx1 == ctx, (T, H, I)
+        w = mok.Weights(4 << 32, 5 << 32, 6 << 32)
+        v = ctypes.c_void_p
+        assert L.mok_ffn_forward(ctypes.byref(p), v(1 << 32), ctypes.byref(w), None, v(2 << 32), None, v(3 << 32),
+                                 n - 1, None) == SMALL
+        # and is no problem for a backward
+        assert L.mok_ffn_backward(ctypes.byref(p), v(1 << 32), v(2 << 32), ctypes.byref(w), v(3 << 32), v(7 << 32),
+                                  v(8 << 32), v(9 << 32), v(10 << 32), v(11 << 32), 2 * full, None) == INV
+    m = [mok.make_ffn_problem(64, 256, 256, mok.MOK_MXFP4, forward_only=f) for f in (False, True)]
+    assert mok.ffn_buffer_sizes(m[0]) == mok.ffn_buffer_sizes(m[1])
+    with pytest.raises(mok.MokError) as e:
+        mok.ffn_buffer_sizes(mok.FfnProblem(64, 256, 256, mok.MOK_BF16, mok.ACT_SILU, 0, 0, 2))
+    assert e.value.status == INV

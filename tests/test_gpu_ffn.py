@@ -405,3 +405,26 @@ def test_residual_beside_y(T, H, I):
     with pytest.raises(mok.MokError) as e:
         F.run_ffn_forward(ws, c["x"], w, residual=wide[:, 8:H + 8], y=wide[:, :H])
     assert e.value.status == mok.MOK_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 4096, 1536), (40, 2048, 768), (300, 2048, 768), (4100, 520, 2056)])
+def test_workspace_of_forwards_alone(T, H, I):
+    """The smaller workspace gives the bits of the full one, and nothing behind it is written; with ctx too."""
+    import torch
+    c = {k: bf(v) for k, v in case(T, H, I, 7).items()}
+    w = (c["wg"], c["wu"], c["wd"])
+    full = F.get_ffn_workspace(T, H, I)
+    want = F.run_ffn_forward(full, c["x"], w, residual=c["res"])
+    p = F.get_ffn_workspace(T, H, I, training=False).problem
+    n, nctx = mok.ffn_buffer_sizes(p)
+    assert n < full.workspace.numel() and nctx == full.ctx.nbytes
+    mem = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    for ctx in (None, torch.zeros_like(full.ctx)):
+        y = torch.empty_like(want)
+        mok.ffn_forward(p, c["x"], w, y, mem[:n], residual=c["res"], ctx=ctx)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and bool((mem[n:] == 0x5A).all())
+    assert torch.equal(ctx, full.ctx)
+    with pytest.raises(mok.MokError) as e:
+        F.run_ffn_backward(F.FfnWorkspace(p, full.workspace, full.ctx), c["x"], w, c["dy"])
+    assert e.value.status == mok.MOK_ERR_INVALID_ARG
