@@ -589,14 +589,15 @@ GradsPlan grads_plan(const mok_ffn_args& a) {
         q.nc = (sh[i].N + ts - 1) / ts;
         q.splits = chunk >= slots ? 1 : (slots + chunk - 1) / chunk;
         if (q.splits > slots / 4) q.splits = slots / 4 > 1 ? slots / 4 : 1;
-        q.n = q.nr * q.nc * q.batch * q.splits;
-        q.per = (q.n + kXcds - 1) / kXcds;
+        const int64_t n = (int64_t)q.nr * q.nc * q.batch * q.splits;   // (may pass 32 bits where it is dropped below)
+        q.n = (int)n;
+        q.per = (int)((n + kXcds - 1) / kXcds);
         q.joins = q.splits > 1 ? q.nr * q.nc * q.batch : 0;
         q.part = g.part;
         g.joins += q.joins;
-        if (q.joins) g.part += (int64_t)q.n * ts * ts;
+        if (q.joins) g.part += n * ts * ts;
         if (q.joins) join += (float)q.splits * q.M * sh[i].N * q.batch * 8 / kCost.rate;
-        count += q.n;
+        count += n;
       }
       if (g.joins && count > 1024) continue;     // (bounds the partial tiles)
       const bool alone = ts == 256 || count <= 256;
