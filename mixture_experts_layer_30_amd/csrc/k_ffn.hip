@@ -599,7 +599,7 @@ GradsPlan grads_plan(const mok_ffn_args& a) {
         if (q.joins) join += (float)q.splits * q.M * sh[i].N * q.batch * 8 / kCost.rate;
         count += n;
       }
-      if (g.joins && count > 1024) continue;     // (bounds the partial tiles)
+      if (g.joins && count > 1024) continue;     // partial tiles take at most 1024 * 256 KiB
       const bool alone = ts == 256 || count <= 256;
       for (int i = 0; i < 3; ++i) {
         const GradsPart& q = g.p[i];

@@ -321,3 +321,18 @@ def test_forwards_alone_need_no_workspace_for_a_backward():
     with pytest.raises(mok.MokError) as e:
         mok.ffn_buffer_sizes(mok.FfnProblem(64, 256, 256, mok.MOK_BF16, mok.ACT_SILU, 0, 0, 2))
     assert e.value.status == INV
+
+
+def test_partial_tiles_are_bounded():
+    """Workgroups of a launch that is split along K are held to 1024 (weight gradients and dx) or 512 (the others), with
+    partial tiles of 256 x 256 fp32 at most: 256 MiB. Long T, small H and large I come closest."""
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    most = 0
+    for T, H, I in ((33653, 144, 4064), (73362, 128, 6208), (15901, 64, 24640), (140477, 80, 3056), (9598, 16, 29992),
+                    (1, 7168, 2048), (4096, 256, 512), (3559, 2560, 8), (8, 1 << 17, 8), (8, 8, 1 << 17),
+                    (1 << 18, 1 << 18, 1 << 18), (1 << 20, 128, 1 << 12), (1 << 24, 64, 64)):
+        ws, _ = mok.ffn_buffer_sizes(mok.make_ffn_problem(T, H, I))
+        part = ws - up(2 * T * I) - up(4 * T * (-(-I // 64) * 64))
+        assert part <= 1024 * 256 * 1024, (T, H, I, part)
+        most = max(most, part)
+    assert most > 600 * 64 * 1024
