@@ -351,3 +351,21 @@ def test_matmul_more_than_one_row_of_workgroups():
     one = F.run_mx_matmul(F.get_mx_matmul_workspace(1, P, K, mok.MOK_MXFP4), a, sa, bp, sp)
     d = F.run_mx_matmul(F.get_mx_matmul_workspace(1, N, K, mok.MOK_MXFP4), a, sa, b, sb)
     assert bool((d == one.repeat(1, rep)[:, :N]).all())
+
+
+@pytest.mark.parametrize("a_dtype", [mok.MOK_MXFP4, mok.MOK_MXFP8])
+@pytest.mark.parametrize("M,N,K", [(5, 77, 8192), (33, 300, 1152), (300, 300, 8192), (4100, 4097, 640)])
+def test_matmul_scales_that_cancel(M, N, K, a_dtype):
+    """Scale bytes over the whole range, of A large where those of B are small: each product of blocks is of ordinary
+    size, though the values of one side alone may pass fp32's range at either end."""
+    a, _, b, _, _, _ = operands(M, N, K, a_dtype, 5)
+    g = np.random.default_rng(M + N + K)
+    e = g.permutation(np.linspace(0, 254, K // 32).astype(int))
+    sa = np.clip(e + g.integers(-2, 3, (M, K // 32)), 0, 254).astype(np.uint8)
+    sb = np.clip(254 - e + g.integers(-2, 3, (N, K // 32)), 0, 254).astype(np.uint8)
+    av = (do.mxfp4_values if a_dtype == mok.MOK_MXFP4 else do.mxfp8_values)(a, sa)
+    bv = do.mxfp4_values(b, sb)
+    ws = F.get_mx_matmul_workspace(M, N, K, a_dtype)
+    d = F.run_mx_matmul(ws, u8(a), u8(sa), u8(b), u8(sb))
+    ref, err = av @ bv.T, mx_dot(av, bv, a_dtype == mok.MOK_MXFP8)
+    assert_within(f64(d), ref, err + HALF * (np.abs(ref) + err) + 1e-38, "d")
