@@ -261,8 +261,8 @@ MOK_DEV void stage128(uint8_t* lds, const Acc<2, 2>& acc) {
 }
 
 // ------------------------------------------------------------------ 256 x 256 tile
-// Eight wavefronts in two groups of four, one of each group on every SIMD. Group
-// g owns tile rows 128 g .. +127, its wavefront c columns 64 c .. +63 (4 x 2
+// Eight wavefronts in two groups of four, one of each group on every SIMD, that multiply in
+// turns (a published scheme, known as ping-pong). Group g owns tile rows 128 g .. +127, its wavefront c columns 64 c .. +63 (4 x 2
 // fragments, 128 accumulators a lane; the products are formed transposed, so that a
 // lane holds four adjacent columns of a row: element 4 q + e of fragment (i, n) is
 // row 32 i + l % 32, column 32 n + 8 q + 4 (l / 32) + e). The groups run half a step apart: in each
@@ -291,8 +291,8 @@ MOK_DEV void stage128(uint8_t* lds, const Acc<2, 2>& acc) {
 // before the barrier of 4s+3, B of s+2 is written over them from 4s+4 on, A of s+3 from
 // 4s+6 on. (Copies between the matrix instructions of the multiplying group were 13 to
 // 40% slower, all of B in interval 4s and two slots of each operand 5% each.) A down
-// product of 4096 x 4096 x 8192 takes 203 us (1352 TFLOP/s; the library's 200 us). Bound
-// by power: the same matrix instructions alone, on random data, sustain 1801 TFLOP/s.
+// product of 4096 x 4096 x 8192 takes 203 us (1352 TFLOP/s; the library's 200 us); the same
+// matrix instructions alone sustain 1801 TFLOP/s on random data, 2352 on constant data.
 constexpr int kPpThreads = 512;
 constexpr int kPpHalf = 16384;
 constexpr int kPpLds = 10 * kPpHalf;             // 160 KiB: 3 + 3 half slots of A, 2 + 2 of B
@@ -547,12 +547,16 @@ MOK_DEV void dense_tile(int i, int nr, int nc, int grp, int& row, int& col) {
 // estimated time. A pass of 256 workgroups of 256 x 256 tiles (one a CU), or of 512 of
 // 128 x 128 (two a CU), takes a fixed part (launch, first copies, epilogue) and a part
 // per slot, of which a 128 x 128 tile with a CU to itself needs the share `alone`; all
-// slots take at least as long as reading the operands; partial sums add a launch and the traffic of writing and reading them. With the
-// constants fitted to 280 shapes of 33 to 8192 rows, each timed with both tiles and up
-// to 8 splits, the choice was within 1% of the fastest in the mean and 18% at worst.
+// slots take at least as long as reading the operands; partial sums add a launch and the
+// traffic of writing and reading them. The constants are those that make the choice, not
+// the times, come out best over 280 shapes of 33 to 8192 rows, each timed with both tiles
+// and up to 8 splits: no single one of them is the time of its part (a lone MXFP4
+// tile took about 5 us and 0.5 to 0.6 a slot; here 8.7 and 0.39). There the choice
+// was within 1% of the fastest in the mean and 18% at worst; on 200 random products that were
+// not fitted (bf16 120, MXFP8 and MXFP4 times MXFP4 40 each) within 2% and 24%.
 struct dense_cost {
-  float fix256, slot256, fix128, slot128, alone; // us
-  float join, rate;                              // us, bytes per us
+  float fix256, slot256, fix128, slot128, alone; // (us)
+  float join, rate;                              // (us, bytes per us)
 };
 inline float dense_plan(int64_t M, int64_t N, int batch, int64_t slots, const dense_cost& c, int* tile, int* splits) {
   const float read = (float)(M + N * batch) * slots * 128 / 4.6e6f;   // the operands once, 4.6 TB/s
@@ -575,9 +579,12 @@ inline float dense_plan(int64_t M, int64_t N, int batch, int64_t slots, const de
   }
   return best;
 }
-// The same for few rows: a launch, the weights (`rows` of K elements) once, and x in every
-// workgroup of 16 weight rows, which each CU takes in at 37 bytes per ns (fitted to 1 to 64
-// rows of bf16 at 4096 x 7168, 7168 x 2048, 1536 x 2048 and 2048 x 768).
+// The same for few rows of bf16: a launch, the weights (`rows` of K elements) once, and x in
+// every workgroup of 16 weight rows, which each CU takes in at 37 bytes per ns (fitted to 1 to
+// 64 rows at 4096 x 7168, 7168 x 2048, 1536 x 2048 and 2048 x 768). Both ways, gate/up and down
+// of 7168 x 2048: one row 15.7 and 10.5 us against 19.3 and 12.0 as tiles, 16 rows 20.0 and 12.8
+// against 19.9 and 13.5, 64 rows 40.5 and 25.6 against 22.9 and 15.1; of 2048 x 768: 16 rows
+// 7.1 and 4.5 against 11.2 and 8.3, 64 rows 12.8 and 6.5 against 12.8 and 8.3.
 inline float few_time(int64_t M, int64_t rows, int64_t K) {
   return 2.5f + (float)rows * K * 2 / 4.6e6f + (float)M * K * 2 * ((rows / 16 + 255) / 256) / 37e3f;
 }

@@ -361,9 +361,9 @@ __global__ __launch_bounds__(kPpThreads, 1) void ffn256_kernel(mok_ffn_args a, i
 // fill them. The products go in descending time of a workgroup, so that the last ones are the short
 // ones (the other way round up to 16% slower), and of two equal ones dWd first, whose operands
 // dh's launch has just read and written (dWg and dWu first: 2 to 4% slower). Against one launch
-// each, the whole backward: 51 -> 31 us at T = 777 of 1000 x 712, 39 -> 23 at 4096 of
-// 256 x 256, 114 -> 101 at 4093 of 2048 x 768, 1174 -> 1116 at 16384 of 4096 x 1536; equal at 64
-// and at 16384 of 7168 x 2048.
+// each, the whole backward from a graph, both in one run: 51 -> 31 us at T = 777 of 1000 x 712,
+// 41 -> 23 at 4096 of 256 x 256, 116 -> 99 at 4093 of 2048 x 768, 1163 -> 1093 at 16384 of
+// 4096 x 1536, 59 -> 57 at 64 and 2433 -> 2409 at 16384 of 7168 x 2048.
 struct GradsPart {
   int op, M, K, nr, nc, batch, splits;
   int n, per;                                    // workgroups, and per XCD
@@ -557,7 +557,8 @@ hipError_t launch(const mok_ffn_args& a, const Plan& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Tile and splits of the three together, by the constants of dense_plan: for each tile and
+// Tile and splits of the three together, by the constants of dense_plan (weights that order the
+// choices, not times): for each tile and
 // each longest chunk of K (in slots) the time of all workgroups over the CUs, the half of a
 // shortest one by which the CUs end apart, and the partial sums.
 GradsPlan grads_plan(const mok_ffn_args& a) {
