@@ -372,7 +372,8 @@ mok_status mok_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t
  * of the 32. A block of scale 255
  * makes its row of D (or, in B, its column) NaN. K a multiple of 128 and at
  * most 2^20 (MOK_ERR_UNSUPPORTED otherwise); M, N >= 0, any value up to 2^30
- * with ceil(M/128) * ceil(N/128) <= 2^23 (MOK_ERR_UNSUPPORTED); a and b 16-byte, scales 4-byte aligned; D may start and step anywhere.
+ * with ceil(M/128) * ceil(N/128) <= 2^23 (MOK_ERR_UNSUPPORTED); a and b 16-byte,
+ * scales 4-byte aligned; D may start and step anywhere.
  * Columns N .. ld_d-1 of D are not touched. Neither D (from its first to its
  * last element) nor the workspace shares memory with another operand
  * (MOK_ERR_INVALID_ARG). */
