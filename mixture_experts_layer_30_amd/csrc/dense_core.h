@@ -263,9 +263,9 @@ MOK_DEV void stage128(uint8_t* lds, const Acc<2, 2>& acc) {
 // ------------------------------------------------------------------ 256 x 256 tile
 // Eight wavefronts in two groups of four, one of each group on every SIMD, that multiply in
 // turns (a published scheme, known as ping-pong). Group g owns tile rows 128 g .. +127, its
-// wavefront c columns 64 c .. +63 (4 x 2 fragments, 128 accumulators a lane; the products are formed transposed, so that a
-// lane holds four adjacent columns of a row: element 4 q + e of fragment (i, n) is
-// row 32 i + l % 32, column 32 n + 8 q + 4 (l / 32) + e). The groups run half a step apart: in each
+// wavefront c columns 64 c .. +63 (4 x 2 fragments, 128 accumulators a lane; the products are
+// formed transposed, so that a lane holds four adjacent columns of a row: element 4 q + e of
+// fragment (i, n) is row 32 i + l % 32, column 32 n + 8 q + 4 (l / 32) + e). The groups run half a step apart: in each
 // interval between two workgroup barriers one group reads fragments from LDS and
 // issues copies while the other multiplies, so a copy that waits for the address
 // unit or for the L1 never holds up a matrix instruction. (One wavefront per
