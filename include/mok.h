@@ -447,6 +447,69 @@ mok_status mok_ffn_backward(const mok_ffn_problem* problem, const void* ctx, con
                             const mok_weights* weights, const void* dy, void* dx, void* dw_gate, void* dw_up,
                             void* dw_down, void* workspace, size_t workspace_bytes, void* stream);
 
+/* MXFP8 values: dst [rows][K] bf16 = E4M3 * 2^(s-127) of codes q [rows][K] and
+ * scales [rows][K/32]. Exact for what mok_mxfp8_quantize and
+ * mok_mxfp8_quantize_transposed write; values below bf16's steps or above its
+ * range round to nearest even (to infinities). A block of scale 255 is NaN.
+ * K must be a multiple of 32; rows >= 0; q and dst 16-byte aligned;
+ * rows * K <= 2^38 (MOK_ERR_UNSUPPORTED). dst shares no memory with q or scales
+ * (MOK_ERR_INVALID_ARG). */
+mok_status mok_mxfp8_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, void* dst,
+                                void* stream);
+
+/* ---------------------------------------------------------------- norm
+ * Root-mean-square norm of the residual stream, in front of the router, the
+ * layer and the dense block:
+ *   z = x + residual, rounded to bf16 and kept as `sum` (without a residual
+ *       z = x), rstd[t] = 1 / sqrt(mean_h z[t][h]^2 + eps),
+ *   y[t][h] = z[t][h] * rstd[t] * weight[h]
+ * What is normed is the stream as it is stored: the same bits as a second call
+ * on `sum` gives, and what the backward reads. Sums are fp32 in a fixed order
+ * that depends on H alone, so a row's results do not depend on the rows beside
+ * it. y is written in bf16, or as the MXFP8 rows that mok_mx_matmul takes
+ * (codes q [T][H] with scales [T][H/32], quantized from y in fp32), or both.
+ * Any T >= 0; H a multiple of 8, with q of 32, at most 32768
+ * (MOK_ERR_UNSUPPORTED otherwise). x has row pitch ld_x; residual, sum, d_sum
+ * and dx ld_s; y and dy ld_y (elements, multiples of 8, 0 = H, at most 2^31).
+ * eps is a positive normal number. weight [H] is bf16 or fp32 (weight_f32), or
+ * NULL for ones. bf16 data and q are 16-byte aligned, fp32 data 16-byte, scales
+ * anyhow. A row with a NaN or an infinity gives NaN in its own row alone: an
+ * infinity makes rstd 0, so its place is NaN and the others are zeros (in MXFP8
+ * a block with a NaN is NaN). Rows whose sum of squares passes fp32's range
+ * come out as zeros. */
+typedef struct {
+  int64_t T, H;
+  int64_t ld_x, ld_s, ld_y;
+  float eps;
+  int32_t weight_f32;            /* 0: weight and its gradient in bf16, 1: in fp32 */
+} mok_norm_problem;
+
+/* residual and sum are both given or both NULL. y, or q with scales, or all
+ * three are given; rstd [T] fp32 (what the backward needs) may be NULL. sum may
+ * be x or residual, and y may be x or residual (the same first element and
+ * pitch, and not the same one as sum's); any other overlap of an output with
+ * another operand is refused (MOK_ERR_INVALID_ARG; rows side by side in one
+ * matrix do not overlap). Columns H .. ld-1 are not touched. */
+mok_status mok_norm_forward(const mok_norm_problem* problem, const void* x, const void* residual, const void* weight,
+                            void* y, void* sum, float* rstd, uint8_t* q, uint8_t* scales, void* stream);
+
+/* [host] Workspace bytes of mok_norm_backward: the partial sums of d_weight (at
+ * most 1024 rows of fp32). One call at a time, as mok_mx_matmul's. */
+mok_status mok_norm_workspace(const mok_norm_problem* problem, size_t* workspace_bytes);
+
+/* Gradients of <dy, y> from the forward's stored z (pitch ld_z elements, 0 = H:
+ * `sum`, or x without a residual) and rstd. With xh = z rstd and g = dy weight:
+ *   dx[t][h] = rstd (g - xh mean_h(g xh)) + d_sum[t][h]
+ *   d_weight[h] = sum_t dy[t][h] xh[t][h]
+ * dx is the gradient of x and of the residual alike; d_sum (may be NULL) is
+ * the gradient that reaches `sum` from further on. d_weight, in the weight's
+ * type, may be NULL, and has to be without a weight. T = 0 gives zeros in
+ * d_weight. dx may be d_sum or dy (same first element and pitch); any other
+ * overlap of dx, d_weight or the workspace with another operand is refused. */
+mok_status mok_norm_backward(const mok_norm_problem* problem, const void* dy, const void* z, int64_t ld_z,
+                             const float* rstd, const void* weight, const void* d_sum, void* dx, void* d_weight,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- tracing
  * Per-kernel timing for profiling ([MoK clip] How-to item 1: profile first to
  * see where the layer's time goes). While tracing is on, every kernel the

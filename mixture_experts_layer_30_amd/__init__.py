@@ -74,6 +74,11 @@ class FfnProblem(ctypes.Structure):
                 ("forward_only", ctypes.c_int32)]
 
 
+class NormProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_s", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64), ("eps", ctypes.c_float), ("weight_f32", ctypes.c_int32)]
+
+
 _lib = None
 
 EXPORTS = ("mok_version", "mok_status_string", "mok_buffer_sizes", "mok_get_schedule_layout",
@@ -81,7 +86,8 @@ EXPORTS = ("mok_version", "mok_status_string", "mok_buffer_sizes", "mok_get_sche
            "mok_router_forward", "mok_router_backward", "mok_trace_enable", "mok_trace_collect",
            "mok_mxfp8_quantize_transposed", "mok_probe_mfma", "mok_build_schedule_noalloc",
            "mok_forward_fused", "mok_mxfp4_quantize", "mok_mxfp4_dequantize", "mok_mx_matmul_workspace",
-           "mok_mx_matmul", "mok_ffn_buffer_sizes", "mok_ffn_forward", "mok_ffn_backward")
+           "mok_mx_matmul", "mok_ffn_buffer_sizes", "mok_ffn_forward", "mok_ffn_backward",
+           "mok_mxfp8_dequantize", "mok_norm_forward", "mok_norm_workspace", "mok_norm_backward")
 
 
 class TraceStat(ctypes.Structure):
@@ -148,6 +154,14 @@ def lib():
         L.mok_ffn_forward.argtypes = [P(FfnProblem), vp, P(Weights), vp, vp, vp, vp, sz, vp]
         L.mok_ffn_backward.restype = ctypes.c_int
         L.mok_ffn_backward.argtypes = [P(FfnProblem), vp, vp, P(Weights), vp, vp, vp, vp, vp, vp, sz, vp]
+        L.mok_mxfp8_dequantize.restype = ctypes.c_int
+        L.mok_mxfp8_dequantize.argtypes = [vp, vp, ctypes.c_int64, ctypes.c_int64, vp, vp]
+        L.mok_norm_forward.restype = ctypes.c_int
+        L.mok_norm_forward.argtypes = [P(NormProblem)] + [vp] * 9
+        L.mok_norm_workspace.restype = ctypes.c_int
+        L.mok_norm_workspace.argtypes = [P(NormProblem), P(sz)]
+        L.mok_norm_backward.restype = ctypes.c_int
+        L.mok_norm_backward.argtypes = [P(NormProblem), vp, vp, ctypes.c_int64, vp, vp, vp, vp, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -302,11 +316,12 @@ def router_backward(problem, schedule, x, w_router, topk_ids, topk_w, d_topk_w, 
            "mok_router_backward")
 
 
-# ---------------------------------------------------------------- MXFP4 and the dense block
+# ---------------------------------------------------------------- MXFP4, the dense block, the norm
 # These calls check their tensors (device, type, shape, row layout) and run on
 # the tensors' device: with the caller's stream, or that device's current one.
 
 _torch = None
+_types = {}
 
 
 def _device_of(t):
@@ -314,6 +329,7 @@ def _device_of(t):
     global _torch
     if _torch is None:
         import torch
+        _types.update(bf16=torch.bfloat16, u8=torch.uint8, f32=torch.float32, i32=torch.int32)
         _torch = torch
     return t.get_device()
 
@@ -321,7 +337,7 @@ def _device_of(t):
 def _want(what, t, dtype, shape, index, rows=False):
     """t is a tensor of GPU `index` of this type and shape, contiguous (rows=True: with
     contiguous elements within a row, rows at any pitch)."""
-    dtype = _torch.bfloat16 if dtype == "bf16" else _torch.uint8
+    dtype = _types[dtype]
     if t.dtype is dtype and t.shape == shape and t.get_device() == index != -1 and t.is_contiguous():
         return
     if not t.is_cuda or t.get_device() != index:
@@ -483,6 +499,86 @@ def ffn_backward(problem, ctx, x, weights, dy, dx, dw_gate, dw_up, dw_down, work
     _run("mok_ffn_backward", dev, stream, lib().mok_ffn_backward, ctypes.byref(p), ctx.data_ptr(), x.data_ptr(),
          ctypes.byref(w), dy.data_ptr(), dx.data_ptr(), dw_gate.data_ptr(), dw_up.data_ptr(), dw_down.data_ptr(),
          *_scratch(workspace, dev))
+
+
+def mxfp8_dequantize(q, scales, dst, stream=None):
+    """The bf16 values dst [..., K] of the E4M3 codes q [..., K] and scales [..., K/32]."""
+    rows, K = _rows_K(dst)
+    dev = _device_of(dst)
+    _want("dst", dst, "bf16", dst.shape, dev)
+    _want("q", q, "u8", dst.shape, dev)
+    _want("scales", scales, "u8", (*dst.shape[:-1], K // 32), dev)
+    _run("mok_mxfp8_dequantize", dev, stream, lib().mok_mxfp8_dequantize, q.data_ptr(), scales.data_ptr(), rows, K,
+         dst.data_ptr())
+
+
+# ---------------------------------------------------------------- norm
+def make_norm_problem(T, H, eps=1e-6, weight_f32=False, ld_x=0, ld_s=0, ld_y=0) -> NormProblem:
+    return NormProblem(int(T), int(H), int(ld_x), int(ld_s), int(ld_y), float(eps), int(weight_f32))
+
+
+def norm_workspace(problem):
+    """Workspace bytes of norm_backward; host only."""
+    n = ctypes.c_size_t()
+    _check(lib().mok_norm_workspace(ctypes.byref(problem), ctypes.byref(n)), "mok_norm_workspace")
+    return n.value
+
+
+def _norm_call(problem, ld_x, ld_s, ld_y):
+    return NormProblem(problem.T, problem.H, ld_x, ld_s, ld_y, problem.eps, problem.weight_f32)
+
+
+def norm_forward(problem, x, weight, y=None, residual=None, sum_out=None, rstd=None, q=None, scales=None, stream=None):
+    """z = x + residual -> sum_out [T][H] bf16, 1 / rms(z) -> rstd [T] fp32, z rstd weight -> y [T][H] bf16 and / or
+    MXFP8 rows q [T][H], scales [T][H/32] uint8. x, y, and residual with sum_out, may have any row pitch that is a
+    multiple of 8 (taken from the tensors). weight [H] in the problem's type, or None for ones."""
+    T, H = problem.T, problem.H
+    dev = _device_of(x)
+    _want("x", x, "bf16", (T, H), dev, rows=True)
+    if weight is not None:
+        _want("weight", weight, "f32" if problem.weight_f32 else "bf16", (H,), dev)
+    ld_y = ld_s = 0
+    if y is not None:
+        _want("y", y, "bf16", (T, H), dev, rows=True)
+        ld_y = _pitch(y)
+    if (residual is None) != (sum_out is None) or (q is None) != (scales is None):
+        raise MokError(MOK_ERR_INVALID_ARG, "residual with sum_out, and q with scales, come together")
+    if residual is not None:
+        _want("residual", residual, "bf16", (T, H), dev, rows=True)
+        _want("sum_out", sum_out, "bf16", (T, H), dev, rows=True)
+        ld_s = _pitch(residual)
+        if _pitch(sum_out) != ld_s:
+            raise MokError(MOK_ERR_INVALID_ARG, "sum_out: another row pitch than residual")
+    if rstd is not None:
+        _want("rstd", rstd, "f32", (T,), dev)
+    if q is not None:
+        _want("q", q, "u8", (T, H), dev)
+        _want("scales", scales, "u8", (T, H // 32), dev)
+    p = _norm_call(problem, _pitch(x), ld_s, ld_y)
+    _run("mok_norm_forward", dev, stream, lib().mok_norm_forward, ctypes.byref(p), x.data_ptr(), _ptr(residual),
+         _ptr(weight), _ptr(y), _ptr(sum_out), _ptr(rstd), _ptr(q), _ptr(scales))
+
+
+def norm_backward(problem, dy, z, rstd, weight, dx, dw, workspace, d_sum=None, stream=None):
+    """dx [T][H] bf16 (with d_sum added) and dw [H] in the weight's type, from the forward's stored stream z and rstd.
+    weight and dw may be None (ones; no gradient). d_sum and dx share one row pitch, dy and z may have others."""
+    T, H = problem.T, problem.H
+    dev = _device_of(dy)
+    for n, t in (("dy", dy), ("z", z), ("dx", dx)):
+        _want(n, t, "bf16", (T, H), dev, rows=True)
+    _want("rstd", rstd, "f32", (T,), dev)
+    wt = "f32" if problem.weight_f32 else "bf16"
+    if weight is not None:
+        _want("weight", weight, wt, (H,), dev)
+    if dw is not None:
+        _want("dw", dw, wt, (H,), dev)
+    if d_sum is not None:
+        _want("d_sum", d_sum, "bf16", (T, H), dev, rows=True)
+        if _pitch(d_sum) != _pitch(dx):
+            raise MokError(MOK_ERR_INVALID_ARG, "dx: another row pitch than d_sum")
+    p = _norm_call(problem, 0, _pitch(dx), _pitch(dy))
+    _run("mok_norm_backward", dev, stream, lib().mok_norm_backward, ctypes.byref(p), dy.data_ptr(), z.data_ptr(),
+         _pitch(z), rstd.data_ptr(), _ptr(weight), _ptr(d_sum), dx.data_ptr(), _ptr(dw), *_scratch(workspace, dev))
 
 
 def trace_enable(on=True):

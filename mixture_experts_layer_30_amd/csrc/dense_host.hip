@@ -15,8 +15,6 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxK = (int64_t)1 << 20, kMaxTiles = (int64_t)1 << 23;
 constexpr int64_t kMaxPitch = (int64_t)1 << 22;  // row pitch of x, y, dy, dx in elements (copies: 32-bit offsets)
 
-bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 // rows x cols in 128 x 128 tiles, of 256 threads each, within one launch (2^32 threads; tiles of
 // 256 x 256 have 512 threads and are split into no more than 512)
 bool tiles_fit(int64_t rows, int64_t cols) { return cdiv(rows, 128) * cdiv(cols, 128) <= kMaxTiles; }
@@ -114,26 +112,6 @@ size_t ffn_ws_bytes(const Ffn& r) {
   return r.mx || r.fwd_only ? fwd : std::max(fwd, bwd_ws(r).total);
 }
 size_t ffn_ctx_bytes(const Ffn& r) { return r.mx ? 0 : (size_t)r.T * 2 * r.I * 2; }
-
-// whether rows of H elements share memory: T rows at a of pitch lda, and at b of pitch ldb
-// (rows of one pitch that lie side by side do not)
-bool rows_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t T, int64_t H) {
-  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(b)) / 2;
-  if (T <= 0 || d >= (T - 1) * ldb + H || -d >= (T - 1) * lda + H) return false;
-  if (lda != ldb) return true;
-  const int64_t m = (d % lda + lda) % lda;
-  return m < H || m > lda - H;
-}
-
-struct Span {
-  const void* p;
-  size_t n;                                      // bytes (rows with a pitch: from the first to the last)
-};
-bool overlap(const Span& a, const Span& b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && a.n && b.n && (x < y ? y - x < a.n : x - y < b.n);
-}
-Span rows_span(const void* p, int64_t T, int64_t H, int64_t ld) { return {p, (size_t)((T - 1) * ld + H) * 2}; }
 
 // whether memory that a forward writes (y, ctx, the workspace) is also memory of another
 // operand of it that it reads or writes; y over x or the residual is not looked at here

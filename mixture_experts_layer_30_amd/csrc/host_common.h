@@ -1,5 +1,5 @@
-// Host helpers shared by the files behind the C ABI: buffer carving, the device
-// check and the launch tracer.
+// Host helpers shared by the files behind the C ABI: buffer carving, operands that
+// share memory, the device check and the launch tracer.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <string.h>
@@ -14,6 +14,28 @@ namespace mok {
 constexpr size_t kAlign = 256;
 inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// whether rows of H elements share memory: T rows at a of pitch lda, and at b of pitch ldb
+// (rows of one pitch that lie side by side do not)
+inline bool rows_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t T, int64_t H) {
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(b)) / 2;
+  if (T <= 0 || d >= (T - 1) * ldb + H || -d >= (T - 1) * lda + H) return false;
+  if (lda != ldb) return true;
+  const int64_t m = (d % lda + lda) % lda;
+  return m < H || m > lda - H;
+}
+
+struct Span {
+  const void* p;
+  size_t n;                                      // bytes (rows with a pitch: from the first to the last)
+};
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.n && b.n && (x < y ? y - x < a.n : x - y < b.n);
+}
+inline Span rows_span(const void* p, int64_t T, int64_t H, int64_t ld) { return {p, (size_t)((T - 1) * ld + H) * 2}; }
 
 // gfx950 check and compute-unit count, once per device (device properties
 // only; no device memory is touched).

@@ -1,0 +1,344 @@
+// Root-mean-square norm of the residual stream, forward and backward, and the
+// reading back of MXFP8 rows.
+//
+// Forward: z = bf16(x + residual), rstd = (mean z^2 + eps)^-1/2, y = z rstd w.
+// Backward, with xh = z rstd, g = dy w: dx = rstd (g - xh mean(g xh)) + d_sum,
+// dw = sum over the rows of dy xh. Both are bound by memory: every operand is
+// read once and every output written once.
+//
+// A row lies in the registers of TPR threads, CH chunks of 8 columns each
+// (thread l holds the chunks l, l + TPR, ...), from its load to its store, so
+// it is read from memory once although the norm needs all of it before the
+// first result. TPR and CH follow from H alone: the order of a row's sum does
+// too.
+#include <type_traits>
+
+#include "dense_core.h"
+#include "norm_launch.h"
+#include "rows_core.h"
+
+using namespace mok;
+
+namespace {
+
+template <int TPR>
+struct RowShape {
+  static constexpr int BT = TPR < 256 ? 256 : TPR;   // threads of a workgroup
+  static constexpr int RPB = BT / TPR;               // rows of a workgroup at a time
+  static constexpr int NW = TPR / 64;                // wavefronts of a row (0: a part of one)
+};
+
+// The sum of v over the TPR threads of a row, in every one of them: butterflies
+// within a wavefront, then the wavefronts' sums in ascending order. `turn`
+// alternates between calls, so that one barrier a call is enough: a wavefront
+// that writes a half again has passed the barrier of the call between, which
+// every other one reached after its reads.
+template <int TPR>
+MOK_DEV float row_sum(float v, float (*red)[RowShape<TPR>::BT / 64], int turn) {
+#pragma unroll
+  for (int d = (TPR < 64 ? TPR : 64) / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  if constexpr (TPR > 64) {
+    constexpr int NW = RowShape<TPR>::NW;
+    const int wave = (int)threadIdx.x >> 6;
+    if (lane_id() == 0) red[turn][wave] = v;
+    __syncthreads();
+    const float* r = red[turn] + wave / NW * NW;
+    v = r[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) v += r[i];
+  }
+  return v;
+}
+
+// eight weights from column 8c on
+MOK_DEV void load_weight(const void* w, int wf, int c, float v[8]) {
+  if (wf == 1) {
+    unpack8(reinterpret_cast<const uint4*>(w)[c], v);
+  } else if (wf == 2) {
+    const float4 a = reinterpret_cast<const float4*>(w)[2 * c], b = reinterpret_cast<const float4*>(w)[2 * c + 1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = 1.0f;
+  }
+}
+
+template <int TPR, int CH>
+__global__ __launch_bounds__(RowShape<TPR>::BT) void norm_fwd_kernel(const mok_norm_args a) {
+  using S = RowShape<TPR>;
+  __shared__ float red[2][S::BT / 64];
+  const int sub = (int)threadIdx.x / TPR, l = (int)threadIdx.x % TPR;
+  const int n8 = a.H / 8;
+  float w[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) w[i][u] = 0.f;
+    if (l + i * TPR < n8) load_weight(a.w, a.wf, l + i * TPR, w[i]);
+  }
+  const float inv_h = 1.0f / (float)a.H;
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * S::RPB; r0 < a.T; r0 += (int64_t)gridDim.x * S::RPB) {
+    const int64_t row = r0 + sub;
+    const bool live = row < a.T;
+    float z[CH][8];
+    float ss = 0.f;
+    uint4 xv[CH], rv[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = l + i * TPR;
+      xv[i] = rv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && c < n8) {
+        xv[i] = reinterpret_cast<const uint4*>(a.x + row * a.ldx)[c];
+        if (a.res) rv[i] = reinterpret_cast<const uint4*>(a.res + row * a.lds)[c];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = l + i * TPR;
+      if (a.res) {
+        float p[8], q[8];
+        unpack8(xv[i], p);
+        unpack8(rv[i], q);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) p[u] += q[u];
+        xv[i] = pack8(p);                        // the stream is kept, and normed, in bf16
+        if (live && c < n8) reinterpret_cast<uint4*>(a.sum + row * a.lds)[c] = xv[i];
+      }
+      unpack8(xv[i], z[i]);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) ss = fmaf(z[i][u], z[i][u], ss);
+    }
+    ss = row_sum<TPR>(ss, red, turn);
+    turn ^= 1;
+    const float rstd = 1.0f / sqrtf(fmaf(ss, inv_h, a.eps));
+    if (live && l == 0 && a.rstd) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = l + i * TPR;
+      const bool ok = live && c < n8;
+      float y[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) y[u] = z[i][u] * rstd * w[i][u];
+      if (a.y && ok) reinterpret_cast<uint4*>(a.y + row * a.ldy)[c] = pack8(y);
+      if (a.q) {
+        // four neighbouring threads hold a block (H is a multiple of 32: all four or none are in the row)
+        uint32_t m = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(y[u]) & 0x7FFFFFFFu);
+        m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+        const bool nan = m >= 0x7F800000u;
+        const int sc = nan ? 255 : mx_scale_byte(__uint_as_float(m));
+        const float inv = mx_inv_scale(sc);
+        const uint32_t lo = e4m3_pack4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+        const uint32_t hi = e4m3_pack4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+        if (ok) {
+          reinterpret_cast<uint2*>(a.q + row * a.H)[c] = nan ? make_uint2(0u, 0u) : make_uint2(lo, hi);
+          if ((l & 3) == 0) a.scales[row * (a.H / 32) + c / 4] = (uint8_t)sc;
+        }
+      }
+    }
+  }
+}
+
+// Rows as in the forward; each thread also adds up dy xh of its columns over the
+// workgroup's rows, and the workgroups' sums, one row of `part` each, are added
+// in ascending order by norm_dw_kernel (one workgroup alone writes d_weight).
+template <int TPR, int CH>
+__global__ __launch_bounds__(RowShape<TPR>::BT) void norm_bwd_kernel(const mok_norm_args a) {
+  using S = RowShape<TPR>;
+  __shared__ float red[2][S::BT / 64];
+  __shared__ float dws[S::RPB > 1 ? S::RPB : 1][S::RPB > 1 ? TPR * CH * 8 : 1];
+  const int sub = (int)threadIdx.x / TPR, l = (int)threadIdx.x % TPR;
+  const int n8 = a.H / 8;
+  float w[CH][8], dw[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) dw[i][u] = w[i][u] = 0.f;
+    if (l + i * TPR < n8) load_weight(a.w, a.wf, l + i * TPR, w[i]);
+  }
+  const float inv_h = 1.0f / (float)a.H;
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * S::RPB; r0 < a.T; r0 += (int64_t)gridDim.x * S::RPB) {
+    const int64_t row = r0 + sub;
+    const bool live = row < a.T;
+    uint4 zv[CH], dv[CH], sv[CH];
+    const float rstd = live ? a.rstd[row] : 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = l + i * TPR;
+      zv[i] = dv[i] = sv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && c < n8) {
+        zv[i] = reinterpret_cast<const uint4*>(a.x + row * a.ldx)[c];
+        dv[i] = reinterpret_cast<const uint4*>(a.dy + row * a.ldy)[c];
+        if (a.res) sv[i] = reinterpret_cast<const uint4*>(a.res + row * a.lds)[c];
+      }
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      float z[8], d[8];
+      unpack8(zv[i], z);
+      unpack8(dv[i], d);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float xh = z[u] * rstd;
+        s = fmaf(d[u] * w[i][u], xh, s);
+        dw[i][u] = fmaf(d[u], xh, dw[i][u]);
+      }
+    }
+    s = row_sum<TPR>(s, red, turn) * inv_h;
+    turn ^= 1;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = l + i * TPR;
+      float z[8], d[8], o[8];
+      unpack8(zv[i], z);
+      unpack8(dv[i], d);
+      unpack8(sv[i], o);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) o[u] = fmaf(rstd, fmaf(-z[u] * rstd, s, d[u] * w[i][u]), o[u]);
+      if (live && c < n8) reinterpret_cast<uint4*>(a.sum + row * a.lds)[c] = pack8(o);
+    }
+  }
+  if (!a.dw) return;
+  if constexpr (S::RPB > 1) {
+    // the rows' threads of one column, in ascending order
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) dws[sub][(l + i * TPR) * 8 + u] = dw[i][u];
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        for (int r = 1; r < S::RPB; ++r) dw[i][u] += dws[r][(l + i * TPR) * 8 + u];
+  }
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = l + i * TPR;
+    if (c >= n8) continue;
+    if (gridDim.x == 1 && a.wf == 1) {
+      reinterpret_cast<uint4*>(a.dw)[c] = pack8(dw[i]);
+    } else {
+      float4* d = reinterpret_cast<float4*>(gridDim.x == 1 ? (float*)a.dw : a.part + (int64_t)blockIdx.x * a.H) + 2 * c;
+      d[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+      d[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    }
+  }
+}
+
+// d_weight[h] = the sum of the n partial rows: 32 columns a workgroup, eight
+// groups of rows each (r, r + 8, ...), the groups added in ascending order
+__global__ __launch_bounds__(256) void norm_dw_kernel(const float* __restrict__ part, int n, int H, int wf,
+                                                     void* __restrict__ dw) {
+  __shared__ float g[8][32];
+  const int c = (int)threadIdx.x & 31, r = (int)threadIdx.x >> 5;
+  const int col = (int)blockIdx.x * 32 + c;
+  float s = 0.f;
+  if (col < H) {
+#pragma unroll 8
+    for (int i = r; i < n; i += 8) s += part[(int64_t)i * H + col];
+  }
+  g[r][c] = s;
+  __syncthreads();
+  if (r != 0 || col >= H) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += g[i][c];
+  if (wf == 1) static_cast<bf16_t*>(dw)[col] = f32_to_bf16(s);
+  else static_cast<float*>(dw)[col] = s;
+}
+
+// Sixteen codes a thread: E4M3 to fp32 is exact, and so is the product with
+// 2^(s-127) by ldexp (the smallest, 2^-9 * 2^-127, is an fp32 subnormal), so the
+// one rounding is that to bf16. Bound by memory.
+__global__ __launch_bounds__(256) void mxfp8_dequantize_kernel(const uint8_t* __restrict__ q,
+                                                               const uint8_t* __restrict__ scales, int64_t n16,
+                                                               bf16_t* __restrict__ dst) {
+  const int64_t idx = flat_block() * 256 + threadIdx.x;
+  if (idx >= n16) return;
+  const uint4 v = reinterpret_cast<const uint4*>(q)[idx];
+  const int s = scales[idx >> 1];
+  const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)wd[i], false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)wd[i], true);
+    f[4 * i] = lo[0]; f[4 * i + 1] = lo[1]; f[4 * i + 2] = hi[0]; f[4 * i + 3] = hi[1];
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = s == 255 ? __uint_as_float(0x7FC00000u) : ldexpf(f[i], s - 127);
+  uint4* d = reinterpret_cast<uint4*>(dst) + 2 * idx;
+  d[0] = pack8(f);
+  d[1] = pack8(f + 8);
+}
+
+// f(RowShape's TPR, CH) as constants, for rows of H columns
+template <class F>
+auto by_width(int H, F&& f) {
+  using std::integral_constant;
+#define MOK_ROW(tpr, ch) \
+  if (H <= 8 * (tpr) * (ch)) return f(integral_constant<int, tpr>{}, integral_constant<int, ch>{})
+  MOK_ROW(8, 1);
+  MOK_ROW(16, 1);
+  MOK_ROW(32, 1);
+  MOK_ROW(64, 1);
+  MOK_ROW(128, 1);
+  MOK_ROW(256, 1);
+  MOK_ROW(256, 2);
+  MOK_ROW(256, 4);
+  MOK_ROW(512, 4);
+#undef MOK_ROW
+  return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+}
+
+}  // namespace
+
+hipError_t mok_launch_norm_forward(const mok_norm_args& a, hipStream_t st) {
+  if (a.T <= 0) return hipSuccess;
+  by_width(a.H, [&](auto tpr, auto ch) {
+    using S = RowShape<decltype(tpr)::value>;
+    const int64_t blocks = (a.T + S::RPB - 1) / S::RPB, cap = 256 * 2048 / S::BT;
+    hipLaunchKernelGGL((norm_fwd_kernel<decltype(tpr)::value, decltype(ch)::value>),
+                       dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(S::BT), 0, st, a);
+  });
+  return hipGetLastError();
+}
+
+int mok_norm_groups(int64_t T, int H) {
+  return by_width(H, [&](auto tpr, auto) {
+    using S = RowShape<decltype(tpr)::value>;
+    const int64_t blocks = (T + S::RPB - 1) / S::RPB, cap = 256 * 1024 / S::BT;
+    return (int)(blocks < cap ? (blocks < 1 ? 1 : blocks) : cap);
+  });
+}
+
+hipError_t mok_launch_norm_backward(const mok_norm_args& a, hipStream_t st) {
+  const int groups = mok_norm_groups(a.T, a.H);
+  by_width(a.H, [&](auto tpr, auto ch) {
+    using S = RowShape<decltype(tpr)::value>;
+    hipLaunchKernelGGL((norm_bwd_kernel<decltype(tpr)::value, decltype(ch)::value>), dim3((unsigned)groups),
+                       dim3(S::BT), 0, st, a);
+  });
+  if (groups > 1 && a.dw) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(256), 0, st, a.part, groups, a.H, a.wf,
+                       a.dw);
+  }
+  return hipGetLastError();
+}
+
+hipError_t mok_launch_mxfp8_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, bf16_t* dst,
+                                       hipStream_t st) {
+  const int64_t n16 = rows * (K / 16);
+  if (n16 <= 0) return hipSuccess;
+  hipLaunchKernelGGL(mxfp8_dequantize_kernel, flat_grid((n16 + 255) / 256), dim3(256), 0, st, q, scales, n16, dst);
+  return hipGetLastError();
+}

@@ -6,14 +6,17 @@ libmok's kernels.
 from __future__ import annotations
 
 import dataclasses
+from typing import NamedTuple
 
 import torch
 
 from . import (ACT_SILU, MOK_BF16, backward, buffer_sizes, build_schedule, ffn_backward, ffn_buffer_sizes,
                ffn_forward, forward, forward_fused, make_config, make_ffn_problem, make_mx_problem, make_problem,
-               mx_matmul, mx_matmul_workspace, mxfp8_quantize, mxfp8_quantize_transposed, schedule_layout)
+               make_norm_problem, mx_matmul, mx_matmul_workspace, mxfp8_quantize, mxfp8_quantize_transposed,
+               norm_backward, norm_forward, norm_workspace, schedule_layout)
 from . import mxfp4_dequantize as _mxfp4_dequantize
 from . import mxfp4_quantize as _mxfp4_quantize
+from . import mxfp8_dequantize as _mxfp8_dequantize
 
 
 @dataclasses.dataclass
@@ -193,3 +196,71 @@ def quantize_ffn_weights_mxfp4(wg, wu, wd):
     """The six tensors a dense block with MXFP4 weights takes (codes, then scales)."""
     (qg, sg), (qu, su), (qd, sd) = (mxfp4_quantize(m) for m in (wg, wu, wd))
     return qg, qu, qd, sg, su, sd
+
+
+# ---------------------------------------------------------------- the norm before the layer
+def mxfp8_dequantize(q, scales):
+    """The bf16 values [..., K] of MXFP8 codes and scales."""
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    _mxfp8_dequantize(q, scales, out)
+    return out
+
+
+@dataclasses.dataclass
+class NormWorkspace:
+    problem: object
+    workspace: torch.Tensor | None
+    training: bool
+
+
+class NormOutput(NamedTuple):
+    y: torch.Tensor | None       # [T][H] bf16
+    sum: torch.Tensor            # [T][H] bf16: the residual stream (x itself without a residual)
+    rstd: torch.Tensor | None    # [T] fp32, in training
+    q: torch.Tensor | None       # [T][H] MXFP8 codes of y, and
+    scales: torch.Tensor | None  # [T][H/32] their scales
+
+
+def get_norm_workspace(T, H, eps=1e-6, weight_dtype=torch.bfloat16, device="cuda", training=True):
+    """The problem and (training) the backward's scratch of one norm."""
+    if weight_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"weight_dtype: {weight_dtype}, wanted torch.bfloat16 or torch.float32")
+    problem = make_norm_problem(T, H, eps, weight_dtype == torch.float32)
+    n = norm_workspace(problem) if training else 0
+    return NormWorkspace(problem, torch.empty(n, dtype=torch.uint8, device=device) if n else None, training)
+
+
+def run_norm_forward(w: NormWorkspace, x, weight, residual=None, out="bf16", y=None, sum_out=None):
+    """The norm of x, or of the stream x + residual, which is returned too (sum_out=residual updates it in place).
+    out: "bf16" (y), "mxfp8" (q and scales, as run_mx_matmul takes them) or "both". weight None: ones."""
+    if out not in ("bf16", "mxfp8", "both"):
+        raise ValueError(f"out: {out!r}, wanted 'bf16', 'mxfp8' or 'both'")
+    T, H = w.problem.T, w.problem.H
+    q = scales = rstd = None
+    if out == "mxfp8":
+        if y is not None:
+            raise ValueError("y: not written with out='mxfp8'")
+    elif y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    if out != "bf16":
+        q = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((T, H // 32), dtype=torch.uint8, device=x.device)
+    if residual is not None and sum_out is None:
+        sum_out = torch.empty_strided(residual.shape, residual.stride(), dtype=residual.dtype, device=x.device)
+    if w.training:
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    norm_forward(w.problem, x, weight, y, residual, sum_out, rstd, q, scales)
+    return NormOutput(y, x if residual is None else sum_out, rstd, q, scales)
+
+
+def run_norm_backward(w: NormWorkspace, z, rstd, weight, dy, d_sum=None, dx=None):
+    """(dx, dw) from the forward's sum (z) and rstd; d_sum, the gradient that reaches the stream from further on, is
+    added to dx. dw is None without a weight."""
+    if not w.training:
+        raise ValueError("a norm workspace without training has no backward")
+    if dx is None:
+        like = dy if d_sum is None else d_sum
+        dx = torch.empty_strided(like.shape, like.stride(), dtype=torch.bfloat16, device=dy.device)
+    dw = None if weight is None else torch.empty_like(weight)
+    norm_backward(w.problem, dy, z, rstd, weight, dx, dw, w.workspace, d_sum=d_sum)
+    return dx, dw
