@@ -510,6 +510,71 @@ mok_status mok_norm_backward(const mok_norm_problem* problem, const void* dy, co
                              const float* rstd, const void* weight, const void* d_sum, void* dx, void* d_weight,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- router losses
+ * What the router learns from besides the layer's d topk_w, on the logits of
+ * all E experts. With p = softmax(logits[t]) over E, lse its logarithm of the
+ * sum, m = token_mask (NULL: ones), n = sum_t m_t,
+ *   counts[e] = |{(t, j): m_t, topk_ids[t][j] = e}|, prob_sum[e] = sum_t m_t p[t][e]
+ *   losses[0] = E / (topk n^2) sum_e counts[e] prob_sum[e]   (balance; 1 when even)
+ *   losses[1] = 1/n sum_t m_t lse_t^2                        (z loss)
+ * and 0 both where n = 0. Ids outside [0, E) are counted nowhere. A token that
+ * the mask leaves out is not looked at, whatever its logits hold. Logits of
+ * -infinity are experts that cannot be chosen; a row of nothing else has p = 0
+ * and lse = 0. Sums are fp32 in a fixed order, counts exact integers.
+ * problem: as the router's, T at most 2^30 (MOK_ERR_UNSUPPORTED); the two
+ * losses' calls do not look at H and I beyond their being valid, and take any
+ * topk. logits and d_logits are 16-byte aligned. */
+
+/* Router forward that keeps the logits [T][E] fp32: mok_router_forward's
+ * results, bit for bit, and its errors; x and w_router 16-byte aligned, outputs
+ * apart from the inputs and each other (MOK_ERR_INVALID_ARG). */
+mok_status mok_router_forward_logits(const mok_problem* problem, const void* x, const float* w_router,
+                                     const float* bias, int32_t* topk_ids, float* topk_w, float* logits,
+                                     void* stream);
+
+/* [host] Workspace bytes of mok_router_losses and mok_router_logits_backward
+ * (the larger). One call at a time, as mok_mx_matmul's. */
+mok_status mok_router_workspace(const mok_problem* problem, size_t* workspace_bytes);
+
+/* token_mask [T] bytes, 0 = left out. losses [2], counts [E], prob_sum [E] and
+ * n_tokens [1] are overwritten and share no memory with each other, the
+ * workspace or an input (MOK_ERR_INVALID_ARG). Data-parallel ranks may add up
+ * counts, prob_sum and n_tokens before the backward, which then gives the
+ * gradient of the loss over all their tokens. */
+mok_status mok_router_losses(const mok_problem* problem, const float* logits, const int32_t* topk_ids,
+                             const uint8_t* token_mask, float* losses, int32_t* counts, float* prob_sum,
+                             int32_t* n_tokens, void* workspace, size_t workspace_bytes, void* stream);
+
+/* d_logits [T][E] fp32, overwritten, from d_losses [2] (device) and, where
+ * topk_w and d_topk_w are given (both or neither), the gradient through the
+ * combine weights too:
+ *   m_t (d_losses[0] E / (topk n^2) p[t][e] (counts[e] - sum_f counts[f] p[t][f])
+ *        + d_losses[1] 2/n lse_t p[t][e])
+ *   + sum_{j: topk_ids[t][j] = e} w_j (g_j - sum_i w_i g_i)
+ * (the second line for every token: it is mok_router_backward's d_sel). counts
+ * and n_tokens are what mok_router_losses wrote. d_logits may be logits; any
+ * other overlap with an input is refused (MOK_ERR_INVALID_ARG). */
+mok_status mok_router_losses_backward(const mok_problem* problem, const float* logits, const int32_t* topk_ids,
+                                      const uint8_t* token_mask, const int32_t* counts, const int32_t* n_tokens,
+                                      const float* d_losses, const float* topk_w, const float* d_topk_w,
+                                      float* d_logits, void* stream);
+
+/* Router backward from the gradient of every logit (mok_router_backward takes
+ * that of the selected ones alone), without a schedule:
+ *   dx[t] = sum_e d_logits[t][e] w_router[e] (+ residual[t])      [T][H] bf16
+ *   d_w_router[e] = sum_t d_logits[t][e] x[t]                     [E][H] fp32
+ * residual [T][H] bf16 (NULL: none) is the layer's own dx, added before the one
+ * rounding; it may be dx itself. fp32 sums in a fixed order on the matrix
+ * cores: for d_w_router the products are exact (d_logits in three bf16 parts),
+ * for dx, which is rounded to bf16, each factor is kept to 16 bits; a value of
+ * d_logits or w_router that is not finite makes NaN of what it enters. x, dx,
+ * residual, w_router, d_logits and d_w_router are 16-byte aligned. T = 0 gives zeros in
+ * d_w_router. Outputs and workspace share no memory with another operand but
+ * dx with residual (MOK_ERR_INVALID_ARG). */
+mok_status mok_router_logits_backward(const mok_problem* problem, const void* x, const float* w_router,
+                                      const float* d_logits, const void* residual, void* dx, float* d_w_router,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- tracing
  * Per-kernel timing for profiling ([MoK clip] How-to item 1: profile first to
  * see where the layer's time goes). While tracing is on, every kernel the

@@ -87,7 +87,9 @@ EXPORTS = ("mok_version", "mok_status_string", "mok_buffer_sizes", "mok_get_sche
            "mok_mxfp8_quantize_transposed", "mok_probe_mfma", "mok_build_schedule_noalloc",
            "mok_forward_fused", "mok_mxfp4_quantize", "mok_mxfp4_dequantize", "mok_mx_matmul_workspace",
            "mok_mx_matmul", "mok_ffn_buffer_sizes", "mok_ffn_forward", "mok_ffn_backward",
-           "mok_mxfp8_dequantize", "mok_norm_forward", "mok_norm_workspace", "mok_norm_backward")
+           "mok_mxfp8_dequantize", "mok_norm_forward", "mok_norm_workspace", "mok_norm_backward",
+           "mok_router_forward_logits", "mok_router_workspace", "mok_router_losses", "mok_router_losses_backward",
+           "mok_router_logits_backward")
 
 
 class TraceStat(ctypes.Structure):
@@ -162,6 +164,16 @@ def lib():
         L.mok_norm_workspace.argtypes = [P(NormProblem), P(sz)]
         L.mok_norm_backward.restype = ctypes.c_int
         L.mok_norm_backward.argtypes = [P(NormProblem), vp, vp, ctypes.c_int64, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.mok_router_forward_logits.restype = ctypes.c_int
+        L.mok_router_forward_logits.argtypes = [P(Problem)] + [vp] * 7
+        L.mok_router_workspace.restype = ctypes.c_int
+        L.mok_router_workspace.argtypes = [P(Problem), P(sz)]
+        L.mok_router_losses.restype = ctypes.c_int
+        L.mok_router_losses.argtypes = [P(Problem)] + [vp] * 8 + [sz, vp]
+        L.mok_router_losses_backward.restype = ctypes.c_int
+        L.mok_router_losses_backward.argtypes = [P(Problem)] + [vp] * 10
+        L.mok_router_logits_backward.restype = ctypes.c_int
+        L.mok_router_logits_backward.argtypes = [P(Problem)] + [vp] * 7 + [sz, vp]
         _lib = L
     return _lib
 
@@ -316,7 +328,7 @@ def router_backward(problem, schedule, x, w_router, topk_ids, topk_w, d_topk_w, 
            "mok_router_backward")
 
 
-# ---------------------------------------------------------------- MXFP4, the dense block, the norm
+# ---------------------------------------------------------------- MXFP4, the dense block, the norm, the router's losses
 # These calls check their tensors (device, type, shape, row layout) and run on
 # the tensors' device: with the caller's stream, or that device's current one.
 
@@ -579,6 +591,87 @@ def norm_backward(problem, dy, z, rstd, weight, dx, dw, workspace, d_sum=None, s
     p = _norm_call(problem, 0, _pitch(dx), _pitch(dy))
     _run("mok_norm_backward", dev, stream, lib().mok_norm_backward, ctypes.byref(p), dy.data_ptr(), z.data_ptr(),
          _pitch(z), rstd.data_ptr(), _ptr(weight), _ptr(d_sum), dx.data_ptr(), _ptr(dw), *_scratch(workspace, dev))
+
+
+# ---------------------------------------------------------------- router losses
+def router_workspace(problem):
+    """Workspace bytes of router_losses and router_logits_backward; host only."""
+    n = ctypes.c_size_t()
+    _check(lib().mok_router_workspace(ctypes.byref(problem), ctypes.byref(n)), "mok_router_workspace")
+    return n.value
+
+
+def router_forward_logits(problem, x, w_router, bias, topk_ids, topk_w, logits, stream=None):
+    """router_forward that keeps the logits [T][E] fp32."""
+    T, H, E, k = problem.T, problem.H, problem.E, problem.topk
+    dev = _device_of(x)
+    _want("x", x, "bf16", (T, H), dev)
+    _want("w_router", w_router, "f32", (E, H), dev)
+    if bias is not None:
+        _want("bias", bias, "f32", (E,), dev)
+    _want("topk_ids", topk_ids, "i32", (T, k), dev)
+    _want("topk_w", topk_w, "f32", (T, k), dev)
+    _want("logits", logits, "f32", (T, E), dev)
+    _run("mok_router_forward_logits", dev, stream, lib().mok_router_forward_logits, ctypes.byref(problem), x.data_ptr(),
+         w_router.data_ptr(), _ptr(bias), topk_ids.data_ptr(), topk_w.data_ptr(), logits.data_ptr())
+
+
+def _mask(mask, T, dev):
+    """A token mask as the bytes of a bool or uint8 tensor."""
+    if mask is not None and mask.dtype is _torch.bool:
+        mask = mask.view(_torch.uint8)
+    if mask is not None:
+        _want("mask", mask, "u8", (T,), dev)
+    return _ptr(mask)
+
+
+def router_losses(problem, logits, topk_ids, losses, counts, prob_sum, n_tokens, workspace, mask=None, stream=None):
+    """logits [T][E] fp32, topk_ids [T][k] int32, mask [T] bool or uint8 (None: every token) -> losses [2] fp32
+    (balance, z), counts [E] int32, prob_sum [E] fp32, n_tokens [1] int32."""
+    T, E, k = problem.T, problem.E, problem.topk
+    dev = _device_of(logits)
+    for n, t, dtype, shape in (("logits", logits, "f32", (T, E)), ("topk_ids", topk_ids, "i32", (T, k)),
+                               ("losses", losses, "f32", (2,)), ("counts", counts, "i32", (E,)),
+                               ("prob_sum", prob_sum, "f32", (E,)), ("n_tokens", n_tokens, "i32", (1,))):
+        _want(n, t, dtype, shape, dev)
+    _run("mok_router_losses", dev, stream, lib().mok_router_losses, ctypes.byref(problem), logits.data_ptr(),
+         topk_ids.data_ptr(), _mask(mask, T, dev), losses.data_ptr(), counts.data_ptr(), prob_sum.data_ptr(),
+         n_tokens.data_ptr(), *_scratch(workspace, dev))
+
+
+def router_losses_backward(problem, logits, topk_ids, counts, n_tokens, d_losses, d_logits, topk_w=None, d_topk_w=None,
+                           mask=None, stream=None):
+    """d_logits [T][E] fp32 (may be logits) from d_losses [2] fp32 on the device and, with topk_w and d_topk_w
+    [T][k] fp32, through the combine weights."""
+    T, E, k = problem.T, problem.E, problem.topk
+    dev = _device_of(logits)
+    if (topk_w is None) != (d_topk_w is None):
+        raise MokError(MOK_ERR_INVALID_ARG, "topk_w and d_topk_w come together")
+    for n, t, dtype, shape in (("logits", logits, "f32", (T, E)), ("topk_ids", topk_ids, "i32", (T, k)),
+                               ("counts", counts, "i32", (E,)), ("n_tokens", n_tokens, "i32", (1,)),
+                               ("d_losses", d_losses, "f32", (2,)), ("d_logits", d_logits, "f32", (T, E))):
+        _want(n, t, dtype, shape, dev)
+    if topk_w is not None:
+        _want("topk_w", topk_w, "f32", (T, k), dev)
+        _want("d_topk_w", d_topk_w, "f32", (T, k), dev)
+    _run("mok_router_losses_backward", dev, stream, lib().mok_router_losses_backward, ctypes.byref(problem),
+         logits.data_ptr(), topk_ids.data_ptr(), _mask(mask, T, dev), counts.data_ptr(), n_tokens.data_ptr(),
+         d_losses.data_ptr(), _ptr(topk_w), _ptr(d_topk_w), d_logits.data_ptr())
+
+
+def router_logits_backward(problem, x, w_router, d_logits, dx, d_w_router, workspace, residual=None, stream=None):
+    """dx [T][H] bf16 = d_logits . w_router (+ residual, which may be dx), d_w_router [E][H] fp32 = d_logits^T . x."""
+    T, H, E = problem.T, problem.H, problem.E
+    dev = _device_of(x)
+    for n, t, dtype, shape in (("x", x, "bf16", (T, H)), ("w_router", w_router, "f32", (E, H)),
+                               ("d_logits", d_logits, "f32", (T, E)), ("dx", dx, "bf16", (T, H)),
+                               ("d_w_router", d_w_router, "f32", (E, H))):
+        _want(n, t, dtype, shape, dev)
+    if residual is not None:
+        _want("residual", residual, "bf16", (T, H), dev)
+    _run("mok_router_logits_backward", dev, stream, lib().mok_router_logits_backward, ctypes.byref(problem),
+         x.data_ptr(), w_router.data_ptr(), d_logits.data_ptr(), _ptr(residual), dx.data_ptr(), d_w_router.data_ptr(),
+         *_scratch(workspace, dev))
 
 
 def trace_enable(on=True):

@@ -14,6 +14,7 @@
 // to e of d_sel * x[t]. No atomics: every sum has a fixed order.
 #include "mok_device.h"
 #include "mok_launch.h"
+#include "router_launch.h"
 
 namespace {
 
@@ -65,7 +66,7 @@ MOK_DEV void split3(float w0, float w1, uint32_t& hi, uint32_t& mid, uint32_t& l
 template <int TT>
 __global__ __launch_bounds__(kRouterThreads) void router_fwd_kernel(
     const bf16_t* __restrict__ x, const float* __restrict__ wr, const float* __restrict__ bias, int64_t T,
-    int H, int E, int k, int32_t* __restrict__ ids, float* __restrict__ w) {
+    int H, int E, int k, int32_t* __restrict__ ids, float* __restrict__ w, float* __restrict__ logits) {
   constexpr int NR = TT / 16;                                             // 16-row tiles
   constexpr int LGE = TT == 16 ? kRouterMaxE : 128;                       // logit row length in LDS
   constexpr int NU = TT == 16 ? 4 : 2;                                    // K steps per load batch
@@ -170,6 +171,10 @@ __global__ __launch_bounds__(kRouterThreads) void router_fwd_kernel(
       }
       __syncthreads();
     }
+  }
+  if (logits) {                                                           // kept for the losses
+    const int n = (int)(T - t0 < TT ? T - t0 : TT) * E;
+    for (int i = threadIdx.x; i < n; i += kRouterThreads) logits[t0 * E + i] = lg[i];
   }
   constexpr int TPW = TT / kRouterWaves;                                  // tokens per wavefront
   if (E <= 64) {
@@ -507,17 +512,22 @@ __global__ __launch_bounds__(64 * NW) void router_dwr_dense_kernel(
 
 hipError_t mok_launch_router_forward(const bf16_t* x, const float* wr, const float* bias, int64_t T, int H,
                                      int E, int k, int32_t* ids, float* w, hipStream_t st) {
+  return mok_launch_router_forward_logits(x, wr, bias, T, H, E, k, ids, w, nullptr, st);
+}
+
+hipError_t mok_launch_router_forward_logits(const bf16_t* x, const float* wr, const float* bias, int64_t T, int H,
+                                            int E, int k, int32_t* ids, float* w, float* logits, hipStream_t st) {
   if (T <= 0) return hipSuccess;
   // 64-token workgroups once they still fill every compute unit several
   // times over (and the logits of 64 tokens fit in LDS), else 16
   if (E <= 128 && T >= 64 * 256) {
     const unsigned grid = (unsigned)((T + 63) / 64);
     hipLaunchKernelGGL(router_fwd_kernel<64>, dim3(grid), dim3(kRouterThreads), 0, st, x, wr, bias, T, H, E, k, ids,
-                       w);
+                       w, logits);
   } else {
     const unsigned grid = (unsigned)((T + kRouterTokens - 1) / kRouterTokens);
     hipLaunchKernelGGL(router_fwd_kernel<kRouterTokens>, dim3(grid), dim3(kRouterThreads), 0, st, x, wr, bias, T, H,
-                       E, k, ids, w);
+                       E, k, ids, w, logits);
   }
   return hipGetLastError();
 }

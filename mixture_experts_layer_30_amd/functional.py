@@ -13,7 +13,8 @@ import torch
 from . import (ACT_SILU, MOK_BF16, backward, buffer_sizes, build_schedule, ffn_backward, ffn_buffer_sizes,
                ffn_forward, forward, forward_fused, make_config, make_ffn_problem, make_mx_problem, make_problem,
                make_norm_problem, mx_matmul, mx_matmul_workspace, mxfp8_quantize, mxfp8_quantize_transposed,
-               norm_backward, norm_forward, norm_workspace, schedule_layout)
+               norm_backward, norm_forward, norm_workspace, router_forward_logits, router_logits_backward,
+               router_losses, router_losses_backward, router_workspace, schedule_layout)
 from . import mxfp4_dequantize as _mxfp4_dequantize
 from . import mxfp4_quantize as _mxfp4_quantize
 from . import mxfp8_dequantize as _mxfp8_dequantize
@@ -264,3 +265,62 @@ def run_norm_backward(w: NormWorkspace, z, rstd, weight, dy, d_sum=None, dx=None
     dw = None if weight is None else torch.empty_like(weight)
     norm_backward(w.problem, dy, z, rstd, weight, dx, dw, w.workspace, d_sum=d_sum)
     return dx, dw
+
+
+# ---------------------------------------------------------------- the router in training, with its losses
+@dataclasses.dataclass
+class RouterWorkspace:
+    problem: object
+    workspace: torch.Tensor | None
+
+
+class RouterLosses(NamedTuple):
+    losses: torch.Tensor         # [2] fp32: balance loss, z loss
+    counts: torch.Tensor         # [E] int32: picks of each expert
+    prob_sum: torch.Tensor       # [E] fp32: summed probabilities
+    n_tokens: torch.Tensor       # [1] int32: tokens that the mask kept
+
+
+def get_router_workspace(T, H, E, topk, device="cuda"):
+    """The problem and scratch of one router's losses and backward."""
+    problem = make_problem(T, H, 128, E, topk)
+    n = router_workspace(problem)
+    return RouterWorkspace(problem, torch.empty(n, dtype=torch.uint8, device=device) if n else None)
+
+
+def run_router_forward(w: RouterWorkspace, x, w_router, bias=None):
+    """(topk_ids, topk_w, logits) of the tokens x."""
+    p = w.problem
+    ids = torch.empty((p.T, p.topk), dtype=torch.int32, device=x.device)
+    tw = torch.empty((p.T, p.topk), dtype=torch.float32, device=x.device)
+    logits = torch.empty((p.T, p.E), dtype=torch.float32, device=x.device)
+    router_forward_logits(p, x, w_router, bias, ids, tw, logits)
+    return ids, tw, logits
+
+
+def run_router_losses(w: RouterWorkspace, logits, topk_ids, mask=None):
+    """The balance and z losses of the tokens that mask [T] keeps (None: all), and the sums under them."""
+    E, dev = w.problem.E, logits.device
+    out = RouterLosses(torch.empty(2, dtype=torch.float32, device=dev), torch.empty(E, dtype=torch.int32, device=dev),
+                       torch.empty(E, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev))
+    router_losses(w.problem, logits, topk_ids, *out, w.workspace, mask=mask)
+    return out
+
+
+def run_router_losses_backward(w: RouterWorkspace, logits, topk_ids, sums: RouterLosses, d_losses, topk_w=None,
+                               d_topk_w=None, mask=None):
+    """d_logits from the gradients of the two losses (a tensor on the device) and, with topk_w and the layer's
+    d_topk_w, through the combine weights. sums: what run_router_losses returned for the same mask."""
+    d_logits = torch.empty_like(logits)
+    router_losses_backward(w.problem, logits, topk_ids, sums.counts, sums.n_tokens, d_losses, d_logits, topk_w, d_topk_w,
+                           mask=mask)
+    return d_logits
+
+
+def run_router_logits_backward(w: RouterWorkspace, x, w_router, d_logits, residual=None, dx=None):
+    """(dx, d_w_router); residual, the layer's own dx, is added (and may be the dx passed in)."""
+    if dx is None:
+        dx = torch.empty_like(x)
+    dwr = torch.empty_like(w_router)
+    router_logits_backward(w.problem, x, w_router, d_logits, dx, dwr, w.workspace, residual=residual)
+    return dx, dwr

@@ -1,6 +1,5 @@
-"""float64 references of the root-mean-square norm and of the router's losses
-and dense backward, written from the definitions in include/mok.h (test
-infrastructure; no code shared with the HIP path)."""
+"""float64 reference of the root-mean-square norm, written from its definition
+in include/mok.h (test infrastructure; no code shared with the HIP path)."""
 from __future__ import annotations
 
 import numpy as np
