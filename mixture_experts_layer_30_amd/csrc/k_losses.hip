@@ -13,25 +13,22 @@
 // 4 (l + L i) .. + 3), so a wavefront works on 64 / L tokens at once.
 #include <type_traits>
 
-#include "mok_device.h"
+#include "lane_reduce.h"
 #include "router_launch.h"
 
 namespace {
 
-constexpr int kBT = 256, kWaves = kBT / 64;
-constexpr int kGroups = 512;                     // most workgroups of the forward
+constexpr int kBT = 256, kWaves = kBT / 64;      // backward
+// forward: few large workgroups, so that few partial sums have to be added
+constexpr int kFT = 1024, kFWaves = kFT / 64;
+constexpr int kGroups = 256;                     // most of them
+constexpr int kAlone = 4;                        // passes that one workgroup makes by itself
 
-template <int L>
-MOK_DEV float group_max(float v) {
-#pragma unroll
-  for (int d = L / 2; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
-}
-template <int L>
-MOK_DEV float group_sum(float v) {
-#pragma unroll
-  for (int d = L / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+// LDS accesses of a wavefront's lanes above land before those below
+MOK_DEV void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // this lane's logits of one row; -infinity past E and in rows that are left out
@@ -54,72 +51,87 @@ MOK_DEV void load_row(const float* row, int E, int l, bool live, float v[I][4]) 
   }
 }
 
+// exp(x) for x <= 0, 0 from -200 down, NaN for NaN: within (1.3 |x| + 2) 2^-24 of itself
+MOK_DEV float exp_neg(float x) {
+  return __builtin_amdgcn_exp2f(__builtin_elementwise_maximum(x, -200.f) * 0x1.715476p+0f);
+}
+
 // v becomes exp(v - max); returns the sum's reciprocal and lse. A row of nothing
 // but -infinity has zeros for all three; a NaN stays one.
 template <int L, int I>
 MOK_DEV void softmax_row(float v[I][4], float& inv, float& lse) {
-  float top = -INFINITY;
+  float top = -INFINITY, den = 0.f;
 #pragma unroll
   for (int i = 0; i < I; ++i) top = fmaxf(top, fmaxf(fmaxf(v[i][0], v[i][1]), fmaxf(v[i][2], v[i][3])));
-  top = group_max<L>(top);
+  top = lanes_max<L>(top);
   if (top == -INFINITY) top = 0.f;
-  float den = 0.f;
 #pragma unroll
   for (int i = 0; i < I; ++i)
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      v[i][u] = expf(v[i][u] - top);
+      v[i][u] = exp_neg(v[i][u] - top);
       den += v[i][u];
     }
-  den = group_sum<L>(den);
+  den = lanes_sum<L>(den);
   const bool none = den == 0.f;
-  inv = none ? 0.f : 1.0f / den;
-  lse = none ? 0.f : top + logf(den);
+  const float r = __builtin_amdgcn_rcpf(den);
+  inv = none ? 0.f : fmaf(r, fmaf(-den, r, 1.0f), r);
+  lse = none ? 0.f : top + __logf(den);
 }
 
-// losses from the sums (one workgroup; prob and counts in memory it can read)
-MOK_DEV void finish(const mok_losses_args& a, const float* prob, const int32_t* counts, float z, int n,
-                    double (*red)[kBT]) {
-  double s = 0.0;
-  for (int e = threadIdx.x; e < a.E; e += kBT) s += (double)counts[e] * (double)prob[e];
-  (*red)[threadIdx.x] = s;
+// the sum of v over a workgroup of BT threads, in its first thread: within the
+// wavefronts, then theirs in ascending order
+template <int BT>
+MOK_DEV double block_sum(double v, double* red) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  if (lane_id() == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  for (int d = kBT / 2; d >= 1; d >>= 1) {
-    if ((int)threadIdx.x < d) (*red)[threadIdx.x] += (*red)[threadIdx.x + d];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    const double dn = n;
-    a.losses[0] = n ? (float)((*red)[0] * a.E / (a.k * dn * dn)) : 0.f;
-    a.losses[1] = n ? (float)((double)z / dn) : 0.f;
-    a.n[0] = n;
-  }
+  if (threadIdx.x == 0)
+    for (int w = 1; w < BT / 64; ++w) v += red[w];
+  return v;
+}
+
+// losses from the sums, by one workgroup of BT threads: cp is this thread's share of sum counts prob
+template <int BT>
+MOK_DEV void finish(const mok_losses_args& a, double cp, double z, int n, double* red) {
+  cp = block_sum<BT>(cp, red);
+  if (threadIdx.x != 0) return;
+  const double dn = n;
+  a.losses[0] = n ? (float)(cp * a.E / (a.k * dn * dn)) : 0.f;
+  a.losses[1] = n ? (float)(z / dn) : 0.f;
+  a.n[0] = n;
 }
 
 template <int L, int I, bool VEC>
-__global__ __launch_bounds__(kBT) void losses_rows_kernel(const mok_losses_args a) {
-  constexpr int SPW = 64 / L, TPB = kWaves * SPW;
+__global__ __launch_bounds__(kFT) void losses_rows_kernel(const mok_losses_args a) {
+  constexpr int SPW = 64 / L, TPB = kFWaves * SPW;
   __shared__ int hist[512];
-  __shared__ float ps[kWaves][512];
-  __shared__ float zs[kWaves];
-  __shared__ int ns[kWaves];
-  __shared__ double red[kBT];
+  __shared__ float ps[kFWaves][4 * L * I];
+  __shared__ float zs[kFWaves];
+  __shared__ int ns[kFWaves];
+  __shared__ double red[kFWaves];
   const int lane = lane_id(), wave = (int)threadIdx.x >> 6, l = lane % L;
-  for (int e = threadIdx.x; e < a.E; e += kBT) hist[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += kFT) hist[e] = 0;
   __syncthreads();
   float acc[I][4];
 #pragma unroll
   for (int i = 0; i < I; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   float z = 0.f;
   int n = 0;
-  for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < a.T; t0 += (int64_t)gridDim.x * TPB) {
-    const int64_t t = t0 + wave * SPW + lane / L;
-    const bool live = t < a.T && (!a.mask || a.mask[t]);
+  const int64_t step = (int64_t)gridDim.x * TPB, t0 = (int64_t)blockIdx.x * TPB;
+  const int at = wave * SPW + lane / L;
+  int64_t left = a.T - t0;                       // tokens from this pass's first one on
+  const float* row = a.logits + (t0 + at) * a.E;
+  const int32_t* ids = a.ids + (t0 + at) * a.k;
+  const uint8_t* mask = a.mask + (t0 + at);
+  for (; left > 0; left -= step, row += step * a.E, ids += step * a.k, mask += step) {
+    const bool live = at < left && (!a.mask || *mask);
     float v[I][4], inv, lse;
-    load_row<L, I, VEC>(a.logits + t * a.E, a.E, l, live, v);
+    load_row<L, I, VEC>(row, a.E, l, live, v);
     if (live)
       for (int j = l; j < a.k; j += L) {
-        const int id = a.ids[t * a.k + j];
+        const int id = ids[j];
         if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);      // integers: the order does not matter
       }
     softmax_row<L, I>(v, inv, lse);
@@ -145,103 +157,96 @@ __global__ __launch_bounds__(kBT) void losses_rows_kernel(const mok_losses_args 
   if (lane < L) {
 #pragma unroll
     for (int i = 0; i < I; ++i)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (4 * (l + L * i) + u < 512) ps[wave][4 * (l + L * i) + u] = acc[i][u];
+      *reinterpret_cast<float4*>(&ps[wave][4 * (l + L * i)]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
   }
   if (lane == 0) {
     zs[wave] = z;
     ns[wave] = n;
   }
   __syncthreads();
-  if (threadIdx.x == 0)
-    for (int w = 1; w < kWaves; ++w) {
-      zs[0] += zs[w];
-      ns[0] += ns[w];
-    }
   const bool alone = gridDim.x == 1;
   uint32_t* part = a.part + (int64_t)blockIdx.x * (2 * a.E + 2);
-  for (int e = threadIdx.x; e < a.E; e += kBT) {
+  double cp = 0.0;
+  for (int e = threadIdx.x; e < a.E; e += kFT) {
     float p = ps[0][e];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) p += ps[w][e];
+    for (int w = 1; w < kFWaves; ++w) p += ps[w][e];
     if (alone) {
-      a.prob[e] = ps[0][e] = p;
+      a.prob[e] = p;
       a.counts[e] = hist[e];
+      cp += (double)hist[e] * (double)p;
     } else {
       part[e] = __float_as_uint(p);
       part[a.E + e] = (uint32_t)hist[e];
     }
   }
-  __syncthreads();
+  z = zs[0];
+  n = ns[0];
+#pragma unroll
+  for (int w = 1; w < kFWaves; ++w) {
+    z += zs[w];
+    n += ns[w];
+  }
   if (alone) {
-    finish(a, ps[0], hist, zs[0], ns[0], &red);
+    finish<kFT>(a, cp, (double)z, n, red);
   } else if (threadIdx.x == 0) {
-    part[2 * a.E] = __float_as_uint(zs[0]);
-    part[2 * a.E + 1] = (uint32_t)ns[0];
-    // the next launch's count of finished workgroups
-    if (blockIdx.x == 0) a.part[(int64_t)gridDim.x * (2 * a.E + 2)] = 0;
+    part[2 * a.E] = __float_as_uint(z);
+    part[2 * a.E + 1] = (uint32_t)n;
   }
 }
 
-// The workgroups' sums, in ascending order: 32 experts a workgroup, eight groups
-// of partial rows each; the workgroup that ends last forms the losses.
-__global__ __launch_bounds__(kBT) void losses_join_kernel(const mok_losses_args a, int groups) {
-  __shared__ float pg[8][32];
-  __shared__ int cg[8][32];
-  __shared__ double red[kBT];
-  __shared__ int last;
-  const int64_t pitch = 2 * a.E + 2;
+// The workgroups' sums, in a fixed order: 32 experts a workgroup, its threads in
+// kJR rows that add every kJR-th partial row each, then the rows in ascending
+// order.
+constexpr int kJR = 32, kJT = 32 * kJR;
+__global__ __launch_bounds__(kJT) void losses_join_kernel(const mok_losses_args a, int groups) {
+  __shared__ float pg[kJR][32];
+  __shared__ int cg[kJR][32];
+  const int pitch = 2 * a.E + 2;
   const int c = (int)threadIdx.x & 31, r = (int)threadIdx.x >> 5, e = (int)blockIdx.x * 32 + c;
   float p = 0.f;
   int n = 0;
-  if (e < a.E)
-    for (int i = r; i < groups; i += 8) {
-      p += __uint_as_float(a.part[i * pitch + e]);
-      n += (int)a.part[i * pitch + a.E + e];
+  if (e < a.E) {
+#pragma unroll 8
+    for (int i = r; i < groups; i += kJR) {
+      p += __uint_as_float(a.part[(int64_t)i * pitch + e]);
+      n += (int)a.part[(int64_t)i * pitch + a.E + e];
     }
+  }
   pg[r][c] = p;
   cg[r][c] = n;
   __syncthreads();
-  if (r == 0 && e < a.E) {
+  if (r != 0 || e >= a.E) return;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      p += pg[i][c];
-      n += cg[i][c];
-    }
-    a.prob[e] = p;
-    a.counts[e] = n;
+  for (int i = 1; i < kJR; ++i) {
+    p += pg[i][c];
+    n += cg[i][c];
   }
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0)
-    last = __hip_atomic_fetch_add(a.part + groups * pitch, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-           gridDim.x - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  // z and n of the workgroups: one or two a thread, then halves in a fixed order
+  a.prob[e] = p;
+  a.counts[e] = n;
+}
+
+// the losses, from the joined sums and the workgroups' z and n
+__global__ __launch_bounds__(512) void losses_finish_kernel(const mok_losses_args a, int groups) {
+  __shared__ double red[8], rz[8];
+  __shared__ int rn[8];
+  const int pitch = 2 * a.E + 2;
+  const int e = (int)threadIdx.x;
+  const double cp = e < a.E ? (double)a.counts[e] * (double)a.prob[e] : 0.0;
   double z = 0.0;
-  int m = 0;
-  for (int i = threadIdx.x; i < groups; i += kBT) {
-    z += (double)__uint_as_float(a.part[i * pitch + 2 * a.E]);
-    m += (int)a.part[i * pitch + 2 * a.E + 1];
+  int n = 0;
+  for (int i = threadIdx.x; i < groups; i += 512) {
+    z += (double)__uint_as_float(a.part[(int64_t)i * pitch + 2 * a.E]);
+    n += (int)a.part[(int64_t)i * pitch + 2 * a.E + 1];
   }
-  int* im = &cg[0][0];
-  red[threadIdx.x] = z;
-  im[threadIdx.x] = m;
-  __syncthreads();
-  for (int d = kBT / 2; d >= 1; d >>= 1) {
-    if ((int)threadIdx.x < d) {
-      red[threadIdx.x] += red[threadIdx.x + d];
-      im[threadIdx.x] += im[threadIdx.x + d];
-    }
-    __syncthreads();
-  }
-  const float zz = (float)red[0];
-  m = im[0];
-  __syncthreads();
-  finish(a, a.prob, a.counts, zz, m, &red);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) n += __shfl_xor(n, d);
+  if (lane_id() == 0) rn[threadIdx.x >> 6] = n;
+  z = block_sum<512>(z, rz);
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) n += rn[w];
+  finish<512>(a, cp, z, n, red);
 }
 
 template <int L, int I, bool VEC>
@@ -253,9 +258,9 @@ __global__ __launch_bounds__(kBT) void losses_bwd_kernel(const mok_losses_args a
 #pragma unroll
   for (int i = 0; i < I; ++i) *reinterpret_cast<float4*>(mine + 4 * (l + L * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
   const int n = a.n[0];
-  const double dn = n ? (double)n : 1.0;
-  const float gb = n ? a.d_losses[0] : 0.f, gz = n ? (float)(2.0 * (double)a.d_losses[1] / dn) : 0.f;
-  // E / (k n^2) (c_e - k n / E)
+  const double per = n ? 1.0 / (double)n : 0.0, share = n ? (double)a.d_losses[0] * per * per / a.k : 0.0;
+  const float gz = n ? (float)(2.0 * (double)a.d_losses[1] * per) : 0.f;
+  // gb E / (k n^2) (c_e - k n / E)
   float ce[I][4];
 #pragma unroll
   for (int i = 0; i < I; ++i)
@@ -263,38 +268,59 @@ __global__ __launch_bounds__(kBT) void losses_bwd_kernel(const mok_losses_args a
     for (int u = 0; u < 4; ++u) {
       const int e = 4 * (l + L * i) + u;
       ce[i][u] = 0.f;
-      if (e < a.E && n)
-        ce[i][u] = (float)((double)((int64_t)a.E * a.counts[e] - (int64_t)a.k * n) / (a.k * dn * dn));
+      if (e < a.E) ce[i][u] = (float)((double)((int64_t)a.E * a.counts[e] - (int64_t)a.k * n) * share);
     }
-  for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < a.T; t0 += (int64_t)gridDim.x * TPB) {
-    const int64_t t = t0 + wave * SPW + lane / L;
-    const bool in = t < a.T, live = in && (!a.mask || a.mask[t]);
-    float v[I][4], inv, lse;
-    load_row<L, I, VEC>(a.logits + t * a.E, a.E, l, live, v);
+  const int64_t step = (int64_t)gridDim.x * TPB, t0 = (int64_t)blockIdx.x * TPB;
+  const int at = wave * SPW + lane / L;
+  int64_t left = a.T - t0;                       // tokens from this pass's first one on
+  const float* row = a.logits + (t0 + at) * a.E;
+  float* out = a.d_logits + (t0 + at) * a.E;
+  const uint8_t* mask = a.mask + (t0 + at);
+  int64_t pick = (t0 + at) * a.k + l;
+  for (; left > 0; left -= step, row += step * a.E, out += step * a.E, mask += step, pick += step * a.k) {
+    const bool in = at < left, live = in && (!a.mask || *mask);
+    // the first L picks, one a lane, are loaded with the row
+    int id = -1;
+    float v[I][4], w = 0.f, g = 0.f;
+    if (a.w && in && l < a.k) {
+      id = a.ids[pick];
+      w = a.w[pick];
+      g = a.g[pick];
+    }
+    load_row<L, I, VEC>(row, a.E, l, live, v);
     if (a.w) {
-      float s = 0.f;
+      float s = w * g;
       if (in)
-        for (int j = l; j < a.k; j += L) s = fmaf(a.w[t * a.k + j], a.g[t * a.k + j], s);
-      s = group_sum<L>(s);
-      // one pick of every token after the other: an expert picked twice adds up in the order of the picks
-      for (int j0 = 0; j0 < a.k; j0 += L) {
-        int id = -1;
-        float d = 0.f;
-        if (in && j0 + l < a.k) {
-          const int64_t at = t * a.k + j0 + l;
-          id = a.ids[at];
-          d = a.w[at] * (a.g[at] - s);
+        for (int j = L; j + l < a.k; j += L) s = fmaf(a.w[pick + j], a.g[pick + j], s);
+      s = lanes_sum<L>(s);
+      for (int j = 0; j < a.k; j += L) {
+        if (j > 0) {
+          const bool more = in && j + l < a.k;
+          id = more ? a.ids[pick + j] : -1;
+          w = more ? a.w[pick + j] : 0.f;
+          g = more ? a.g[pick + j] : 0.f;
         }
-        const int m = min(L, a.k - j0);
-        for (int j = 0; j < m; ++j) {
-          if (l == j && id >= 0 && id < a.E)
-            (void)__hip_atomic_fetch_add(mine + id, d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
-          __builtin_amdgcn_wave_barrier();       // (keeps the picks one instruction each)
+        const float d = w * (g - s);
+        const bool ok = id >= 0 && id < a.E;
+        const float old = ok && a.k > L ? mine[id] : 0.f;
+        wave_order();
+        if (ok) (void)__hip_atomic_fetch_add(mine + id, d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+        wave_order();
+        // Another pick of the same expert has been added as well: once more, one pick of each token after the other,
+        // so that they add up in the order of the picks. (Where none sees the others, all are zeros.)
+        if (__ballot(ok && mine[id] != old + d)) {
+          wave_order();
+          if (ok) mine[id] = old;
+          for (int q = 0; q < L; ++q) {
+            wave_order();
+            if (l == q && ok) mine[id] += d;
+          }
         }
+        wave_order();
       }
     }
+    float inv, lse, s = 0.f;
     softmax_row<L, I>(v, inv, lse);
-    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < I; ++i)
 #pragma unroll
@@ -302,36 +328,31 @@ __global__ __launch_bounds__(kBT) void losses_bwd_kernel(const mok_losses_args a
         v[i][u] *= inv;
         s = fmaf(v[i][u], ce[i][u], s);
       }
-    s = group_sum<L>(s);
-    const float zt = gz * lse;
-    // the wavefront's LDS writes above land in order before its reads here
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    s = lanes_sum<L>(s);
+    // (a row that is left out has zeros for v)
+    const float rest = live ? fmaf(gz, lse, -s) : 0.f;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int e = 4 * (l + L * i);
-      float o[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) o[u] = live ? v[i][u] * fmaf(gb, ce[i][u] - s, zt) : 0.f;
+      float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
       if (a.w) {
-        float4* at = reinterpret_cast<float4*>(mine + e);
-        const float4 q = *at;
-        *at = make_float4(0.f, 0.f, 0.f, 0.f);
-        o[0] += q.x; o[1] += q.y; o[2] += q.z; o[3] += q.w;
+        d = *reinterpret_cast<const float4*>(mine + e);
+        *reinterpret_cast<float4*>(mine + e) = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      float* d = a.d_logits + t * a.E + e;
+      d.x = fmaf(v[i][0], ce[i][0] + rest, d.x);
+      d.y = fmaf(v[i][1], ce[i][1] + rest, d.y);
+      d.z = fmaf(v[i][2], ce[i][2] + rest, d.z);
+      d.w = fmaf(v[i][3], ce[i][3] + rest, d.w);
       if constexpr (VEC) {
-        if (in && e < a.E) *reinterpret_cast<float4*>(d) = make_float4(o[0], o[1], o[2], o[3]);
+        if (in && e < a.E) *reinterpret_cast<float4*>(out + e) = d;
       } else {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (in && e + u < a.E) d[u] = o[u];
+        if (in && e < a.E) out[e] = d.x;
+        if (in && e + 1 < a.E) out[e + 1] = d.y;
+        if (in && e + 2 < a.E) out[e + 2] = d.z;
+        if (in && e + 3 < a.E) out[e + 3] = d.w;
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_order();
   }
 }
 
@@ -355,29 +376,31 @@ auto by_experts(int E, F&& f) {
 }
 
 int groups_of(int64_t T, int L) {
-  const int tpb = kWaves * 64 / L;
+  const int tpb = kFWaves * 64 / L;
   const int64_t blocks = (T + tpb - 1) / tpb;
-  return (int)(blocks < 1 ? 1 : blocks < kGroups ? blocks : kGroups);
+  return (int)(blocks <= kAlone ? 1 : blocks < kGroups ? blocks : kGroups);
 }
 
 }  // namespace
 
 size_t mok_losses_part_bytes(int64_t T, int E) {
   const int groups = by_experts(E, [&](auto L, auto, auto) { return groups_of(T, decltype(L)::value); });
-  return groups > 1 ? ((size_t)groups * (2 * E + 2) + 1) * 4 : 0;
+  return groups > 1 ? (size_t)groups * (2 * E + 2) * 4 : 0;
 }
 
 hipError_t mok_launch_losses(const mok_losses_args& a, hipStream_t st) {
   const int groups = by_experts(a.E, [&](auto L, auto I, auto vec) {
     const int g = groups_of(a.T, decltype(L)::value);
     hipLaunchKernelGGL((losses_rows_kernel<decltype(L)::value, decltype(I)::value, decltype(vec)::value>),
-                       dim3((unsigned)g), dim3(kBT), 0, st, a);
+                       dim3((unsigned)g), dim3(kFT), 0, st, a);
     return g;
   });
   if (groups > 1) {
-    const hipError_t e = hipGetLastError();
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(losses_join_kernel, dim3((unsigned)((a.E + 31) / 32)), dim3(kBT), 0, st, a, groups);
+    hipLaunchKernelGGL(losses_join_kernel, dim3((unsigned)((a.E + 31) / 32)), dim3(kJT), 0, st, a, groups);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(losses_finish_kernel, dim3(1), dim3(512), 0, st, a, groups);
   }
   return hipGetLastError();
 }

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "dense_core.h"
+#include "lane_reduce.h"
 #include "norm_launch.h"
 #include "rows_core.h"
 
@@ -28,15 +29,14 @@ struct RowShape {
   static constexpr int NW = TPR / 64;                // wavefronts of a row (0: a part of one)
 };
 
-// The sum of v over the TPR threads of a row, in every one of them: butterflies
+// The sum of v over the TPR threads of a row, in every one of them: pairwise
 // within a wavefront, then the wavefronts' sums in ascending order. `turn`
 // alternates between calls, so that one barrier a call is enough: a wavefront
 // that writes a half again has passed the barrier of the call between, which
 // every other one reached after its reads.
 template <int TPR>
 MOK_DEV float row_sum(float v, float (*red)[RowShape<TPR>::BT / 64], int turn) {
-#pragma unroll
-  for (int d = (TPR < 64 ? TPR : 64) / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  v = lanes_sum<(TPR < 64 ? TPR : 64)>(v);
   if constexpr (TPR > 64) {
     constexpr int NW = RowShape<TPR>::NW;
     const int wave = (int)threadIdx.x >> 6;
