@@ -10,7 +10,14 @@
 // (thread l holds the chunks l, l + TPR, ...), from its load to its store, so
 // it is read from memory once although the norm needs all of it before the
 // first result. TPR and CH follow from H alone: the order of a row's sum does
-// too.
+// too. Many threads with one chunk each are fastest for many rows (backward of
+// 16384 x 7168: 166 us with 1024 threads a row, 174 with 512, 189 with 256, 266
+// with 128) and for a single one (forward with MXFP8 rows: 6.1, 6.4, 7.6 us).
+// Stores carry the nontemporal hint (forward of 16384 x 7168: 156 us with it,
+// 164 without).
+//
+// Forward of 16384 x 7168 with a residual: 157 us, 6.0 TB/s; backward 166 us,
+// 5.7 TB/s with the partial sums of d_weight.
 #include <type_traits>
 
 #include "dense_core.h"
@@ -77,7 +84,8 @@ __global__ __launch_bounds__(RowShape<TPR>::BT) void norm_fwd_kernel(const mok_n
     for (int u = 0; u < 8; ++u) w[i][u] = 0.f;
     if (l + i * TPR < n8) load_weight(a.w, a.wf, l + i * TPR, w[i]);
   }
-  const float inv_h = 1.0f / (float)a.H;
+  const double inv_h64 = 1.0 / a.H;
+  const float inv_h = (float)inv_h64;
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * S::RPB; r0 < a.T; r0 += (int64_t)gridDim.x * S::RPB) {
     const int64_t row = r0 + sub;
@@ -104,7 +112,7 @@ __global__ __launch_bounds__(RowShape<TPR>::BT) void norm_fwd_kernel(const mok_n
 #pragma unroll
         for (int u = 0; u < 8; ++u) p[u] += q[u];
         xv[i] = pack8(p);                        // the stream is kept, and normed, in bf16
-        if (live && c < n8) reinterpret_cast<uint4*>(a.sum + row * a.lds)[c] = xv[i];
+        if (live && c < n8) store_nt(reinterpret_cast<uint4*>(a.sum + row * a.lds) + c, xv[i]);
       }
       unpack8(xv[i], z[i]);
 #pragma unroll
@@ -113,16 +121,26 @@ __global__ __launch_bounds__(RowShape<TPR>::BT) void norm_fwd_kernel(const mok_n
     ss = row_sum<TPR>(ss, red, turn);
     turn ^= 1;
     const float rstd = 1.0f / sqrtf(fmaf(ss, inv_h, a.eps));
+    // for the codes: one Newton step in 64 bits
+    double rstd64 = rstd;
+    if (a.q && rstd > 0.f)
+      rstd64 += 0.5 * rstd64 * (1.0 - fma((double)ss, inv_h64, (double)a.eps) * rstd64 * rstd64);
     if (live && l == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = l + i * TPR;
       const bool ok = live && c < n8;
       float y[8];
+      if (a.y) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) y[u] = z[i][u] * rstd * w[i][u];
-      if (a.y && ok) reinterpret_cast<uint4*>(a.y + row * a.ldy)[c] = pack8(y);
+        for (int u = 0; u < 8; ++u) y[u] = z[i][u] * rstd * w[i][u];
+        if (ok) store_nt(reinterpret_cast<uint4*>(a.y + row * a.ldy) + c, pack8(y));
+      }
       if (a.q) {
+        // (a value within its error of the middle between two codes may take either: in 64 bits, at the rate of 32,
+        // the products add nothing to rstd's error)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) y[u] = (float)((double)z[i][u] * rstd64 * (double)w[i][u]);
         // four neighbouring threads hold a block (H is a multiple of 32: all four or none are in the row)
         uint32_t m = 0;
 #pragma unroll
@@ -150,16 +168,31 @@ template <int TPR, int CH>
 __global__ __launch_bounds__(RowShape<TPR>::BT) void norm_bwd_kernel(const mok_norm_args a) {
   using S = RowShape<TPR>;
   __shared__ float red[2][S::BT / 64];
-  __shared__ float dws[S::RPB > 1 ? S::RPB : 1][S::RPB > 1 ? TPR * CH * 8 : 1];
+  // Up to 16384 columns the weights and their gradient's sums stay in registers. Beyond, there are not enough: the sums
+  // lie in LDS, one place a thread and column, and the weights are read again for each row.
+  constexpr bool KEEP = CH <= 2;
+  constexpr int DWS = !KEEP ? TPR * CH * 8 : S::RPB > 1 ? S::BT * CH * 8 : 1;
+  __shared__ float dws[DWS];
   const int sub = (int)threadIdx.x / TPR, l = (int)threadIdx.x % TPR;
   const int n8 = a.H / 8;
-  float w[CH][8], dw[CH][8];
+  float wk[KEEP ? CH : 1][8], dw[CH][8];
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
+  for (int i = 0; i < CH; ++i)
 #pragma unroll
-    for (int u = 0; u < 8; ++u) dw[i][u] = w[i][u] = 0.f;
-    if (l + i * TPR < n8) load_weight(a.w, a.wf, l + i * TPR, w[i]);
+    for (int u = 0; u < 8; ++u) {
+      if constexpr (KEEP) dw[i][u] = wk[i][u] = 0.f;
+      else dws[(8 * i + u) * TPR + l] = 0.f;
+    }
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (l + i * TPR < n8) load_weight(a.w, a.wf, l + i * TPR, wk[i]);
   }
+  const auto weight = [&](int i, float v[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = KEEP ? wk[KEEP ? i : 0][u] : 0.f;
+    if (!KEEP && l + i * TPR < n8) load_weight(a.w, a.wf, l + i * TPR, v);
+  };
   const float inv_h = 1.0f / (float)a.H;
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * S::RPB; r0 < a.T; r0 += (int64_t)gridDim.x * S::RPB) {
@@ -180,44 +213,58 @@ __global__ __launch_bounds__(RowShape<TPR>::BT) void norm_bwd_kernel(const mok_n
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      float z[8], d[8];
+      float z[8], d[8], w[8];
       unpack8(zv[i], z);
       unpack8(dv[i], d);
+      weight(i, w);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const float xh = z[u] * rstd;
-        s = fmaf(d[u] * w[i][u], xh, s);
-        dw[i][u] = fmaf(d[u], xh, dw[i][u]);
+        s = fmaf(d[u] * w[u], xh, s);
+        if constexpr (KEEP) dw[i][u] = fmaf(d[u], xh, dw[i][u]);
+        else dws[(8 * i + u) * TPR + l] = fmaf(d[u], xh, dws[(8 * i + u) * TPR + l]);
       }
     }
     s = row_sum<TPR>(s, red, turn) * inv_h;
     turn ^= 1;
+    // (kept as loaded: unpacked once more below, not held in twice the registers over the sum)
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      asm volatile("" : "+v"(zv[i].x), "+v"(zv[i].y), "+v"(zv[i].z), "+v"(zv[i].w));
+      asm volatile("" : "+v"(dv[i].x), "+v"(dv[i].y), "+v"(dv[i].z), "+v"(dv[i].w));
+    }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = l + i * TPR;
-      float z[8], d[8], o[8];
+      float z[8], d[8], o[8], w[8];
       unpack8(zv[i], z);
       unpack8(dv[i], d);
       unpack8(sv[i], o);
+      weight(i, w);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) o[u] = fmaf(rstd, fmaf(-z[u] * rstd, s, d[u] * w[i][u]), o[u]);
-      if (live && c < n8) reinterpret_cast<uint4*>(a.sum + row * a.lds)[c] = pack8(o);
+      for (int u = 0; u < 8; ++u) o[u] = fmaf(rstd, fmaf(-z[u] * rstd, s, d[u] * w[u]), o[u]);
+      if (live && c < n8) store_nt(reinterpret_cast<uint4*>(a.sum + row * a.lds) + c, pack8(o));
     }
   }
   if (!a.dw) return;
-  if constexpr (S::RPB > 1) {
+  if constexpr (!KEEP) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) dw[i][u] = dws[(8 * i + u) * TPR + l];
+  } else if constexpr (S::RPB > 1) {
     // the rows' threads of one column, in ascending order
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) dws[sub][(l + i * TPR) * 8 + u] = dw[i][u];
+      for (int u = 0; u < 8; ++u) dws[(8 * i + u) * S::BT + threadIdx.x] = dw[i][u];
     __syncthreads();
     if (sub != 0) return;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        for (int r = 1; r < S::RPB; ++r) dw[i][u] += dws[r][(l + i * TPR) * 8 + u];
+        for (int r = 1; r < S::RPB; ++r) dw[i][u] += dws[(8 * i + u) * S::BT + r * TPR + l];
   }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
@@ -233,23 +280,23 @@ __global__ __launch_bounds__(RowShape<TPR>::BT) void norm_bwd_kernel(const mok_n
   }
 }
 
-// d_weight[h] = the sum of the n partial rows: 32 columns a workgroup, eight
-// groups of rows each (r, r + 8, ...), the groups added in ascending order
-__global__ __launch_bounds__(256) void norm_dw_kernel(const float* __restrict__ part, int n, int H, int wf,
-                                                     void* __restrict__ dw) {
-  __shared__ float g[8][32];
+// d_weight[h] = the sum of the n partial rows: 32 columns a workgroup, 32 rows of
+// threads that add every 32nd partial row each, then theirs in ascending order
+__global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__ part, int n, int H, int wf,
+                                                      void* __restrict__ dw) {
+  __shared__ float g[32][32];
   const int c = (int)threadIdx.x & 31, r = (int)threadIdx.x >> 5;
   const int col = (int)blockIdx.x * 32 + c;
   float s = 0.f;
   if (col < H) {
 #pragma unroll 8
-    for (int i = r; i < n; i += 8) s += part[(int64_t)i * H + col];
+    for (int i = r; i < n; i += 32) s += part[(int64_t)i * H + col];
   }
   g[r][c] = s;
   __syncthreads();
   if (r != 0 || col >= H) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) s += g[i][c];
+  for (int i = 1; i < 32; ++i) s += g[i][c];
   if (wf == 1) static_cast<bf16_t*>(dw)[col] = f32_to_bf16(s);
   else static_cast<float*>(dw)[col] = s;
 }
@@ -291,9 +338,9 @@ auto by_width(int H, F&& f) {
   MOK_ROW(64, 1);
   MOK_ROW(128, 1);
   MOK_ROW(256, 1);
-  MOK_ROW(256, 2);
-  MOK_ROW(256, 4);
-  MOK_ROW(512, 4);
+  MOK_ROW(512, 1);
+  MOK_ROW(1024, 1);
+  MOK_ROW(1024, 2);
 #undef MOK_ROW
   return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
@@ -304,7 +351,9 @@ hipError_t mok_launch_norm_forward(const mok_norm_args& a, hipStream_t st) {
   if (a.T <= 0) return hipSuccess;
   by_width(a.H, [&](auto tpr, auto ch) {
     using S = RowShape<decltype(tpr)::value>;
-    const int64_t blocks = (a.T + S::RPB - 1) / S::RPB, cap = 256 * 2048 / S::BT;
+    // A workgroup for each RPB rows: 157 us at 16384 x 7168, against 170 with workgroups that go round and keep the
+    // weights. (A launch holds 2^32 threads; more rows go round.)
+    const int64_t blocks = (a.T + S::RPB - 1) / S::RPB, cap = (int64_t)1 << 21;
     hipLaunchKernelGGL((norm_fwd_kernel<decltype(tpr)::value, decltype(ch)::value>),
                        dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(S::BT), 0, st, a);
   });
@@ -329,7 +378,7 @@ hipError_t mok_launch_norm_backward(const mok_norm_args& a, hipStream_t st) {
   if (groups > 1 && a.dw) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(256), 0, st, a.part, groups, a.H, a.wf,
+    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(1024), 0, st, a.part, groups, a.H, a.wf,
                        a.dw);
   }
   return hipGetLastError();
