@@ -1,18 +1,17 @@
 // Router backward from the gradient of every logit: dx = dl . Wr (+ residual)
-// and dWr = dl^T . x, on the matrix cores (v_mfma_f32_32x32x16_bf16). dl and Wr
+// and dWr = dl^T . x, on the matrix cores. dl and Wr
 // are fp32, the operands bf16: for dWr, which is fp32, dl is split exactly into
 // three bf16 parts (x is bf16, so every product is exact); for dx, which is
 // rounded to bf16, dl and Wr go in as two parts each, the nearest bf16 and the
 // nearest to what that leaves (at most 2^-16 of a value is lost), and the
 // product of the two small parts, at most 2^-16 of the whole, is left out.
 //
-// A lane l of the instruction supplies row l % 32 of an operand, 8 values of K
-// from 8 (l / 32) on, and holds of the result column l % 32 the rows
-// 8 (i / 4) + 4 (l / 32) + i % 4, i = 0 .. 15.
 #include <type_traits>
 
-#include "mok_device.h"
+#include "gemm_core.h"
 #include "router_launch.h"
+
+using namespace mok;
 
 namespace {
 
@@ -36,220 +35,326 @@ MOK_DEV void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo)
   lo = pack_bf16x2(ra - bf_lo(mid), rb - bf_hi(mid));
 }
 
-MOK_DEV f32x16_t mfma(const uint4& a, const uint4& b, f32x16_t c) {
+MOK_DEV f32x16_t mfma32(const uint4& a, const uint4& b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
                                                  0, 0);
 }
-
-// four values of row t of dl from expert e on; zeros past the ends
-MOK_DEV float4 load_dl(const mok_logits_bwd_args& a, int64_t t, int64_t t1, int e, bool vec) {
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* p = a.dl + t * a.E + e;
-  if (t >= t1) return v;
-  if (vec) {
-    if (e < a.E) v = *reinterpret_cast<const float4*>(p);
-  } else {
-    if (e < a.E) v.x = p[0];
-    if (e + 1 < a.E) v.y = p[1];
-    if (e + 2 < a.E) v.z = p[2];
-    if (e + 3 < a.E) v.w = p[3];
-  }
-  return v;
+MOK_DEV f32x4_t mfma16(const uint4& a, const uint4& b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
+                                                 0, 0);
 }
 
-// ---------------------------------------------------------------- dx
-// The columns of dx are rows of the first operand, tokens columns of the second,
-// so a lane ends up with 16 neighbouring columns of one token. A wavefront keeps
-// its 32 columns of Wr, both parts, in registers (8 KS of them, KS = E / 16) and
-// the tokens stream past: 32 at a time are split into LDS by the whole workgroup,
-// the next 32 on their way in registers meanwhile.
-template <int KS, int NW>
-__global__ __launch_bounds__(64 * NW) void router_dx_kernel(const mok_logits_bwd_args a, int panels, int slices) {
-  constexpr int EP = 16 * KS, PITCH = EP + 8, BT = 64 * NW, NL = (32 * EP / 4 + BT - 1) / BT;
-  __shared__ __attribute__((aligned(16))) bf16_t tile[2][32 * PITCH];
-  const int panel = (int)blockIdx.x % panels, slice = (int)blockIdx.x / panels;
-  const int wave = (int)threadIdx.x >> 6, lane = lane_id(), r = lane & 31, half = lane >> 5;
-  const int64_t blocks = (a.T + 31) / 32;
-  const int64_t t0 = blocks * slice / slices * 32, te = blocks * (slice + 1) / slices * 32, t1 = te < a.T ? te : a.T;
-  const int h0 = panel * 32 * NW + 32 * wave;
-  const bool cols = h0 < a.H;                    // (H is a multiple of 32)
-  const bool vec = a.E % 4 == 0;
-  const int nks = (a.E + 15) / 16;
-  // row r of the operand is column 16 ((r / 4) % 2) + 4 (r / 8) + r % 4, so that lane half b holds columns 16 b .. + 15
-  const int col = h0 + 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3);
-  uint4 whi[KS], wmid[KS];
-#pragma unroll
-  for (int s = 0; s < KS; ++s) {
-    float v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int e = 16 * s + 8 * half + u;
-      v[u] = cols && e < a.E ? a.wr[(int64_t)e * a.H + col] : 0.f;
-    }
-    split2(v[0], v[1], whi[s].x, wmid[s].x);
-    split2(v[2], v[3], whi[s].y, wmid[s].y);
-    split2(v[4], v[5], whi[s].z, wmid[s].z);
-    split2(v[6], v[7], whi[s].w, wmid[s].w);
+// Loads and stores go through buffer descriptors: what lies past a descriptor's
+// bytes reads as zero and is not written, so that no access stands in a branch.
+// (With branches round them the compiler cannot tell how many are in flight at the
+// wait for one, and waits for all: a step then takes as long as the memory's
+// latency, 164 us instead of xxx for 16384 x 4096 with 128 experts.)
+typedef __amdgpu_buffer_rsrc_t buf_t;
+constexpr uint32_t kOut = 0x7ffffff0u;           // past every descriptor's bytes
+MOK_DEV buf_t make_buf(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(p && bytes > 0 ? bytes : 0), 0x00020000);
+}
+MOK_DEV uint4 load16(buf_t b, uint32_t off) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0));
+}
+MOK_DEV void store16(buf_t b, uint32_t off, const uint4& v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), b, (int)off, 0, 0);
+}
+
+// Workgroup b of n in an order that gives each of the eight dies (workgroups go
+// round them) a contiguous share, so that the panels of one slice of tokens, which
+// read the same rows of dl, share an L2.
+MOK_DEV int die_order(int b, int n) { return n % 8 ? b : b % 8 * (n / 8) + b / 8; }
+
+// tokens of slice s of n, in whole blocks of 32
+struct Slice {
+  int64_t t0, t1;
+  MOK_DEV Slice(int64_t T, int s, int n) {
+    const int64_t blocks = (T + 31) / 32;
+    t0 = blocks * s / n * 32;
+    t1 = min(blocks * (s + 1) / n * 32, T);
   }
-  float4 next[NL];
-  auto load = [&](int64_t t) {
+};
+
+// f(step's buffer as a constant, first token) for every 32 tokens
+template <class F>
+MOK_DEV void steps(const Slice& s, F&& f) {
+  for (int64_t t = s.t0; t < s.t1; t += 64) {
+    f(std::integral_constant<int, 0>{}, t);
+    if (t + 32 >= s.t1) break;
+    f(std::integral_constant<int, 1>{}, t + 32);
+  }
+}
+
+// ---------------------------------------------------------------- kernel
+// A workgroup takes 32 NW columns and a slice of the tokens, 32 tokens at a time
+// through two sets of LDS buffers: while one is multiplied, the other is filled
+// from registers that were loaded two steps ahead (one beyond 128 experts). Its barriers wait for LDS alone
+// (__syncthreads would wait for every load and store in flight, which makes a step
+// as long as the memory's latency). Up to 128 experts the workgroup forms both
+// results (DX and DWR), so that dl is read and split once and reading x goes on
+// beside writing dx; beyond, the accumulators of all experts do not fit beside Wr,
+// and there are two launches, that of DWR with 128 experts a workgroup.
+//
+// dl of a step lies in LDS as bf16 parts [32 tokens][EP experts]; 16-byte chunk c
+// of token row t at c ^ swz(t): eight rows at one chunk (dx), and four rows at two
+// neighbouring chunks (dWr, transposed), fall on the eight places of 128 bytes.
+//
+// dx: the columns of dx are rows of the first operand, tokens columns of the
+// second. A wavefront keeps its 32 columns of Wr, both parts, in registers (16 KS
+// of them, KS = EP / 32) and the tokens stream past. v_mfma_f32_16x16x32_bf16: lane
+// l supplies row l % 16 of an operand, 8 values of K from 8 (l / 16) on, and holds
+// of result column l % 16 the rows 4 (l / 16) + i. Row r of the wavefront's tile m
+// (0, 1) is column 8 (r / 4) + 4 m + r % 4, so a lane ends up with 8 neighbouring
+// columns of a token and four lanes with 64 bytes of it.
+//
+// dWr: x as it is and dl in its three parts are both read transposed
+// (ds_read_b64_tr_b16: lane 4 q + p of 16 names row q and columns 4 p .. + 3, and
+// gets column l of the four rows) for v_mfma_f32_32x32x16_bf16 (lane l supplies row
+// l % 32 of an operand, 8 values of K from 8 (l / 32) on, and holds of result column
+// l % 32 the rows 8 (i / 4) + 4 (l / 32) + i % 4). The slices' sums, one [E][H] each,
+// are added in ascending order by router_dwr_join_kernel.
+MOK_DEV int swz(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+
+template <int KS, bool DX, bool DWR, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(const mok_logits_bwd_args a, int panels, int eblocks,
+                                                              int slices) {
+  constexpr int BT = 64 * NW, NC = 32 * NW, EP = 32 * KS;
+  constexpr int DP = 2 * EP < 128 ? 128 : 2 * EP, XP = 2 * NC + 64;    // row pitches of dl and x in bytes
+  constexpr int PARTS = DWR ? 3 : 2;
+  constexpr int kD = 32 * DP, kX = DWR ? 32 * XP : 0;
+  constexpr int kW = DX ? 32 * (NC + 4) * 4 : 0;                       // 32 rows of Wr, before the first step
+  constexpr int kBuf = 2 * (PARTS * kD + kX), kLds = kBuf > kW ? kBuf : kW;
+  constexpr int WM = KS == 4 ? 2 : 1, TM = KS / WM, TN = WM;           // dWr: 32 x 32 tiles of a wavefront
+  constexpr int AHEAD = KS <= 4 ? 2 : 1;         // steps whose loads are in flight
+  constexpr int ND = (32 * EP / 4 + BT - 1) / BT, NX = 32 * NC / 8 / BT;   // 16-byte loads of a thread and step
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+  const auto dl_buf = [&](int buf, int part) { return lds + (buf * PARTS + part) * kD; };
+  const auto x_buf = [&](int buf) { return lds + 2 * PARTS * kD + buf * kX; };
+  const int b = die_order((int)blockIdx.x, (int)gridDim.x);
+  const int panel = b % panels, eb = b / panels % eblocks, slice = b / (panels * eblocks);
+  const Slice sl(a.T, slice, slices);
+  const int wave = wave_id(), lane = lane_id(), r = lane & 15, g = lane >> 4;
+  const int c0 = panel * NC, h0 = c0 + 32 * wave, e0 = eb * EP;
+  const bool cols = h0 < a.H;                    // (H is a multiple of 128)
+  const int nks = (a.E - e0 + 31) / 32;          // steps of 32 experts that hold any
+
+  // ---- Wr: 32 rows at a time through LDS into the operand's registers
+  uint4 whi[2][DX ? KS : 1], wmid[2][DX ? KS : 1];
+  if constexpr (DX) {
+    constexpr int NWL = 32 * NC / 4 / BT;
+    float* wl = reinterpret_cast<float*>(lds);
+    uint4 wn[NWL];
+    const auto load_w = [&](int s) {
+      const buf_t src = make_buf(a.wr + (int64_t)32 * s * a.H + c0, ((int64_t)(a.E - 32 * s) * a.H - c0) * 4);
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int q = (int)threadIdx.x + BT * i;
-      next[i] = q < 32 * EP / 4 ? load_dl(a, t + q / (EP / 4), t1, 4 * (q % (EP / 4)), vec)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  };
-  load(t0);
-  for (int64_t t = t0; t < t1; t += 32) {
-    __syncthreads();                             // the last tile's reads are done
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int q = (int)threadIdx.x + BT * i;
-      if (q >= 32 * EP / 4) break;
-      uint2 hi, mid;
-      split2(next[i].x, next[i].y, hi.x, mid.x);
-      split2(next[i].z, next[i].w, hi.y, mid.y);
-      const int at = q / (EP / 4) * PITCH + 4 * (q % (EP / 4));
-      *reinterpret_cast<uint2*>(tile[0] + at) = hi;
-      *reinterpret_cast<uint2*>(tile[1] + at) = mid;
-    }
-    __syncthreads();
-    load(t + 32);
-    if (!cols) continue;
-    const int64_t tok = t + r;
-    bf16_t* out = a.dx + tok * a.H + h0 + 16 * half;
-    uint4 rv[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    if (a.res && tok < t1) {
-      const uint4* p = reinterpret_cast<const uint4*>(a.res + tok * a.H + h0 + 16 * half);
-      rv[0] = p[0];
-      rv[1] = p[1];
-    }
-    f32x16_t acc;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+      for (int i = 0; i < NWL; ++i) {
+        const int q = (int)threadIdx.x + BT * i;
+        wn[i] = load16(src, 4u * (q / (NC / 4) * a.H + 4 * (q % (NC / 4))));
+      }
+    };
+    load_w(0);
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      if (s < nks) {
-        const uint4 dhi = *reinterpret_cast<const uint4*>(tile[0] + r * PITCH + 16 * s + 8 * half);
-        const uint4 dmid = *reinterpret_cast<const uint4*>(tile[1] + r * PITCH + 16 * s + 8 * half);
-        acc = mfma(wmid[s], dhi, acc);
-        acc = mfma(whi[s], dmid, acc);
-        acc = mfma(whi[s], dhi, acc);
-      }
-    }
-    if (tok < t1) {
-      const uint32_t rw[8] = {rv[0].x, rv[0].y, rv[0].z, rv[0].w, rv[1].x, rv[1].y, rv[1].z, rv[1].w};
-      uint32_t o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(acc[2 * i] + bf_lo(rw[i]), acc[2 * i + 1] + bf_hi(rw[i]));
-      reinterpret_cast<uint4*>(out)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      reinterpret_cast<uint4*>(out)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      for (int i = 0; i < NWL; ++i) {
+        const int q = (int)threadIdx.x + BT * i;
+        *reinterpret_cast<uint4*>(wl + q / (NC / 4) * (NC + 4) + 4 * (q % (NC / 4))) = wn[i];
+      }
+      if (s + 1 < KS) load_w(s + 1);
+      barrier_lds_only();
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = wl[(8 * g + u) * (NC + 4) + 32 * wave + 8 * (r >> 2) + 4 * m + (r & 3)];
+        split2(v[0], v[1], whi[m][s].x, wmid[m][s].x);
+        split2(v[2], v[3], whi[m][s].y, wmid[m][s].y);
+        split2(v[4], v[5], whi[m][s].z, wmid[m][s].z);
+        split2(v[6], v[7], whi[m][s].w, wmid[m][s].w);
+      }
+      barrier_lds_only();
     }
   }
-}
 
-// ---------------------------------------------------------------- dWr
-// A workgroup sums 32 MT experts x 128 columns over its slice of the tokens, 32
-// at a time through LDS: x as it is, dl in its three parts, both read transposed
-// (ds_read_b64_tr_b16: lane 4 q + p of 16 names row q and columns 4 p .. + 3, and
-// gets column l of the four rows). The slices' sums, one [E][H] each, are added
-// in ascending order by router_dwr_join_kernel.
-constexpr int kNC = 128;
-template <int MT>
-__global__ __launch_bounds__(256) void router_dwr_slices_kernel(const mok_logits_bwd_args a, int panels, int eblocks,
-                                                                int slices) {
-  constexpr int EB = 32 * MT;
-  constexpr int XP = 2 * kNC + 64, DP = 2 * EB + (EB > 32 ? 64 : 0);   // row pitches in bytes
-  constexpr int WM = MT == 4 ? 2 : 1;            // wavefronts along the experts
-  constexpr int TM = MT / WM, TN = MT == 4 ? 2 : 1;
-  constexpr int NL = EB / 32;                    // float4s of dl a thread loads
-  __shared__ __attribute__((aligned(16))) uint8_t xs[32 * XP];
-  __shared__ __attribute__((aligned(16))) uint8_t ds[3][32 * DP];
-  const int panel = (int)blockIdx.x % panels, eb = (int)blockIdx.x / panels % eblocks;
-  const int slice = (int)blockIdx.x / (panels * eblocks);
-  const int wave = (int)threadIdx.x >> 6, lane = lane_id();
-  const int wm = wave % WM, wn = wave / WM;
-  const int64_t blocks = (a.T + 31) / 32;
-  const int64_t t0 = blocks * slice / slices * 32, te = blocks * (slice + 1) / slices * 32, t1 = te < a.T ? te : a.T;
-  const int c0 = panel * kNC, e0 = eb * EB;
-  const bool vec = a.E % 4 == 0;
-  f32x16_t acc[TM][TN];
+  f32x16_t acc[DWR ? TM : 1][DWR ? TN : 1];
+  if constexpr (DWR) {
 #pragma unroll
-  for (int m = 0; m < TM; ++m)
+    for (int m = 0; m < TM; ++m)
 #pragma unroll
-    for (int n = 0; n < TN; ++n)
+      for (int n = 0; n < TN; ++n)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
-  uint4 xn[2];
-  float4 dn[NL];
-  auto load = [&](int64_t t) {
+        for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
+  }
+
+  // a thread's places in a step's rows, in bytes from the first of them
+  uint32_t doff[ND], xoff[DWR ? NX : 1], roff[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int q = (int)threadIdx.x + 256 * i;
-      const int64_t tok = t + q / 16;
-      xn[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (tok < t1) xn[i] = *reinterpret_cast<const uint4*>(a.x + tok * a.H + c0 + 8 * (q % 16));
-    }
+  for (int i = 0; i < ND; ++i) {
+    const int q = (int)threadIdx.x + BT * i, row = q / (EP / 4), e = 4 * (q % (EP / 4));
+    doff[i] = row < 32 && e0 + e < a.E ? 4u * (row * a.E + e) : kOut;
+  }
+  if constexpr (DWR) {
+    // (columns past H read the next row, for sums that are not stored)
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int q = (int)threadIdx.x + 256 * i;
-      dn[i] = load_dl(a, t + q / (EB / 4), t1, e0 + 4 * (q % (EB / 4)), vec);
-    }
-  };
-  // this lane's place in a transposed read: row 8 (l / 32) + (l % 16) / 4, columns 16 ((l / 16) % 2) + 4 (l % 4)
-  const int tr = 8 * (lane >> 5) + ((lane & 15) >> 2), tc = 2 * (16 * ((lane >> 4) & 1) + 4 * (lane & 3));
-  auto frag = [&](const uint8_t* base, int pitch, int k, int c) {
-    const uint8_t* p = base + (16 * k + tr) * pitch + 2 * c + tc;
-    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_ptr)(p));
-    const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_ptr)(p + 4 * pitch));
-    return __builtin_bit_cast(uint4, i16x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
-  };
-  load(t0);
-  for (int64_t t = t0; t < t1; t += 32) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int q = (int)threadIdx.x + 256 * i;
-      *reinterpret_cast<uint4*>(xs + q / 16 * XP + 16 * (q % 16)) = xn[i];
-    }
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int q = (int)threadIdx.x + 256 * i;
-      uint2 p[3];
-      split3(dn[i].x, dn[i].y, p[0].x, p[1].x, p[2].x);
-      split3(dn[i].z, dn[i].w, p[0].y, p[1].y, p[2].y);
-#pragma unroll
-      for (int s = 0; s < 3; ++s)
-        *reinterpret_cast<uint2*>(ds[s] + q / (EB / 4) * DP + 8 * (q % (EB / 4))) = p[s];
-    }
-    __syncthreads();
-    load(t + 32);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint4 xf[TN];
-#pragma unroll
-      for (int n = 0; n < TN; ++n) xf[n] = frag(xs, XP, k, 32 * (wn * TN + n));
-#pragma unroll
-      for (int m = 0; m < TM; ++m)
-#pragma unroll
-        for (int s = 2; s >= 0; --s) {
-          const uint4 df = frag(ds[s], DP, k, 32 * (wm * TM + m));
-#pragma unroll
-          for (int n = 0; n < TN; ++n) acc[m][n] = mfma(df, xf[n], acc[m][n]);
-        }
+    for (int i = 0; i < NX; ++i) {
+      const int q = (int)threadIdx.x + BT * i;
+      xoff[i] = 2u * (q / (NC / 8) * a.H + 8 * (q % (NC / 8)));
     }
   }
-  float* out = slices > 1 ? a.part + (int64_t)slice * a.E * a.H : a.dwr;
 #pragma unroll
-  for (int m = 0; m < TM; ++m)
+  for (int n = 0; n < 2; ++n) roff[n] = cols ? 2u * ((16 * n + r) * a.H + h0 + 8 * g) : kOut;
+  // of four experts from 4 j on, how many there are (E is not always a multiple of 4: the others' place holds the next
+  // token's, and must not enter a product)
+  const auto loaded = [&](int i) { return a.E - e0 - 4 * (((int)threadIdx.x + BT * i) % (EP / 4)); };
+
+  uint4 dn[AHEAD][ND], xn[AHEAD][DWR ? NX : 1], rn[AHEAD][DX ? 2 : 1];
+  const auto load = [&](auto buf, int64_t t) {
+    constexpr int P = decltype(buf)::value % AHEAD;
+    const int64_t left = min(sl.t1 - t, (int64_t)32);                  // tokens of the step
+    const buf_t dl = make_buf(a.dl + t * a.E + e0, (left * a.E - e0) * 4);
 #pragma unroll
-    for (int n = 0; n < TN; ++n)
+    for (int i = 0; i < ND; ++i) dn[P][i] = load16(dl, doff[i]);
+    if constexpr (DWR) {
+      const buf_t x = make_buf(a.x + t * a.H + c0, (left * a.H - c0) * 2);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int e = e0 + 32 * (wm * TM + m) + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-        if (e < a.E) out[(int64_t)e * a.H + c0 + 32 * (wn * TN + n) + (lane & 31)] = acc[m][n][i];
+      for (int i = 0; i < NX; ++i) xn[P][i] = load16(x, xoff[i]);
+    }
+  };
+  // the residual of a step, loaded where that of an earlier step has been used
+  const auto load_res = [&](auto buf, int64_t t) {
+    constexpr int P = decltype(buf)::value % AHEAD;
+    if constexpr (DX) {
+      const buf_t res = make_buf(a.res ? a.res + t * a.H : nullptr, min(sl.t1 - t, (int64_t)32) * a.H * 2);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) rn[P][n] = load16(res, roff[n]);
+    }
+  };
+  load(std::integral_constant<int, 0>{}, sl.t0);
+  load_res(std::integral_constant<int, 0>{}, sl.t0);
+  if constexpr (AHEAD == 2) {
+    load(std::integral_constant<int, 1>{}, sl.t0 + 32);
+    load_res(std::integral_constant<int, 1>{}, sl.t0 + 32);
+  }
+
+  // places in dl's buffers: this thread's when it fills them, and this lane's of the two kinds of operand. A step of 32
+  // experts is four chunks on, which the exchange of chunks turns into bit 6 of the place and whole 128 bytes.
+  constexpr int RI = BT / (EP / 4);              // rows between a thread's loads (a multiple of 8, or one load, or few)
+  const auto put_at = [&](int row, int j) { return row * DP + (((j >> 1) ^ swz(row)) << 4) + 8 * (j & 1); };
+  const int put0 = put_at((int)threadIdx.x / (EP / 4), (int)threadIdx.x % (EP / 4));
+  const int get0 = r * DP + ((g ^ swz(r)) << 4);
+  const auto at_step = [](int place, int s) { return (place ^ ((s & 1) << 6)) + (s >> 1) * 128; };
+  // a transposed read: row 8 (l / 32) + (l % 16) / 4, columns 16 ((l / 16) % 2) + 4 (l % 4)
+  const int tr = 8 * (lane >> 5) + (r >> 2), tc = 16 * (g & 1) + 4 * (lane & 3);
+  const int trl = tr * DP + (((tc >> 3) ^ swz(tr)) << 4) + 2 * (tc & 7);
+  const int trh = (tr + 4) * DP + (((tc >> 3) ^ swz(tr + 4)) << 4) + 2 * (tc & 7);
+  const int wm = wave % WM, wn = wave / WM;
+  const int trx = tr * XP + 2 * (32 * wn * TN + tc);
+
+  steps(sl, [&](auto buf, int64_t t) {
+    constexpr int P = decltype(buf)::value, R = P % AHEAD;
+#pragma unroll
+    for (int i = 0; i < ND; ++i) {
+      const int q = (int)threadIdx.x + BT * i;
+      if (32 * EP / 4 < BT && wave >= 32 * EP / 4 / 64) break;         // (fewer places than threads)
+      const int at = RI % 8 == 0 ? put0 + i * RI * DP : put_at(q / (EP / 4), q % (EP / 4));
+      uint2 p[3];
+      const int n = loaded(i);
+      const float4 v = make_float4(__uint_as_float(dn[R][i].x), n > 1 ? __uint_as_float(dn[R][i].y) : 0.f,
+                                   n > 2 ? __uint_as_float(dn[R][i].z) : 0.f, n > 3 ? __uint_as_float(dn[R][i].w) : 0.f);
+      split3(v.x, v.y, p[0].x, p[1].x, p[2].x);
+      split3(v.z, v.w, p[0].y, p[1].y, p[2].y);
+#pragma unroll
+      for (int s = 0; s < PARTS; ++s) *reinterpret_cast<uint2*>(dl_buf(P, s) + at) = p[s];
+    }
+    if constexpr (DWR) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) {
+        const int q = (int)threadIdx.x + BT * i;
+        *reinterpret_cast<uint4*>(x_buf(P) + q / (NC / 8) * XP + 16 * (q % (NC / 8))) = xn[R][i];
       }
+    }
+    load(buf, t + 32 * AHEAD);
+    // everyone has written these buffers, and is done with the other ones
+    barrier_lds_only();
+    if constexpr (DWR) {
+      const auto pair = [&](const uint8_t* lo, const uint8_t* hi) {
+        const i16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_ptr)lo);
+        const i16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_ptr)hi);
+        return __builtin_bit_cast(uint4, i16x8_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+      };
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint4 xf[TN];
+#pragma unroll
+        for (int n = 0; n < TN; ++n) {
+          const uint8_t* p = x_buf(P) + trx + 16 * k * XP + 64 * n;
+          xf[n] = pair(p, p + 4 * XP);
+        }
+#pragma unroll
+        for (int m = 0; m < TM; ++m)
+#pragma unroll
+          for (int s = 2; s >= 0; --s) {
+            // (WM = 2 wavefronts along the experts take the tiles 0, 1 and 2, 3: the second pair is 128 bytes on)
+            const uint8_t* p = dl_buf(P, s) + 16 * k * DP + wm * 128;
+            const uint4 df = pair(p + at_step(trl, m), p + at_step(trh, m));
+#pragma unroll
+            for (int n = 0; n < TN; ++n) acc[m][n] = mfma32(df, xf[n], acc[m][n]);
+          }
+      }
+    }
+    if constexpr (DX) {
+      f32x4_t o[2][2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) o[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        if (s < nks) {
+          uint4 d[2][2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              d[n][p] = *reinterpret_cast<const uint4*>(dl_buf(P, p) + 16 * n * DP + at_step(get0, s));
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              o[m][n] = mfma16(wmid[m][s], d[n][0], o[m][n]);
+              o[m][n] = mfma16(whi[m][s], d[n][1], o[m][n]);
+              o[m][n] = mfma16(whi[m][s], d[n][0], o[m][n]);
+            }
+        }
+      }
+      const buf_t dx = make_buf(a.dx + t * a.H, min(sl.t1 - t, (int64_t)32) * a.H * 2);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const uint32_t rw[4] = {rn[R][n].x, rn[R][n].y, rn[R][n].z, rn[R][n].w};
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = pack_bf16x2(o[i >> 1][n][2 * (i & 1)] + bf_lo(rw[i]), o[i >> 1][n][2 * (i & 1) + 1] + bf_hi(rw[i]));
+        store16(dx, roff[n], make_uint4(v[0], v[1], v[2], v[3]));
+      }
+      load_res(buf, t + 32 * AHEAD);
+    }
+  });
+
+  if constexpr (DWR) {
+    float* out = slices > 1 ? a.part + (int64_t)slice * a.E * a.H : a.dwr;
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = e0 + 32 * (wm * TM + m) + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+          const int c = c0 + 32 * (wn * TN + n) + (lane & 31);
+          if (e < a.E && c < a.H) out[(int64_t)e * a.H + c] = acc[m][n][i];
+        }
+  }
 }
 
 __global__ __launch_bounds__(256) void router_dwr_join_kernel(const float* __restrict__ part, int slices, int64_t n4,
@@ -257,7 +362,7 @@ __global__ __launch_bounds__(256) void router_dwr_join_kernel(const float* __res
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n4) return;
   float4 s = reinterpret_cast<const float4*>(part)[i];
-#pragma unroll 4
+#pragma unroll 8
   for (int k = 1; k < slices; ++k) {
     const float4 v = reinterpret_cast<const float4*>(part)[k * n4 + i];
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
@@ -265,63 +370,65 @@ __global__ __launch_bounds__(256) void router_dwr_join_kernel(const float* __res
   reinterpret_cast<float4*>(dwr)[i] = s;
 }
 
-struct DwrPlan {
-  int mt, panels, eblocks, slices;
+#ifndef DWR_WG1
+#define DWR_WG1 512
+#define DWR_WG2 512
+#define DWR_WG4 256
+#define DX_WG 512
+#endif
+#ifndef GW1
+#define GW1 256
+#define GW2 256
+#define GW4 256
+#define GWX 256
+#endif
+// workgroups to aim at: as many as are resident together
+struct Plan {
+  int panels, eblocks, slices;
 };
-DwrPlan dwr_plan(int64_t T, int H, int E) {
-  DwrPlan p;
-  p.mt = E <= 32 ? 1 : E <= 64 ? 2 : 4;
-  p.panels = H / kNC;
-  p.eblocks = (E + 32 * p.mt - 1) / (32 * p.mt);
-  const int64_t blocks = (T + 31) / 32;
-  int64_t s = 512 / ((int64_t)p.panels * p.eblocks);
-  if (s > blocks / 2) s = blocks / 2;
-  p.slices = (int)(s < 1 ? 1 : s);
+Plan plan_of(int64_t T, int H, int columns, int eblocks, int workgroups) {
+  Plan p;
+  p.panels = (H + columns - 1) / columns;
+  p.eblocks = eblocks;
+  const int64_t blocks = (T + 31) / 32, s = workgroups / ((int64_t)p.panels * eblocks);
+  p.slices = (int)(s < 1 ? 1 : s < blocks ? s : blocks < 1 ? 1 : blocks);
   return p;
+}
+// of the launch that forms dWr
+Plan dwr_plan(int64_t T, int H, int E) {
+  return plan_of(T, H, 256, (E + 127) / 128, E <= 32 ? GW1 : E <= 64 ? GW2 : GW4);
+}
+
+template <int KS, bool DX, bool DWR, int NW>
+hipError_t launch(const mok_logits_bwd_args& a, const Plan& p, hipStream_t st) {
+  hipLaunchKernelGGL((router_grad_kernel<KS, DX, DWR, NW>), dim3((unsigned)(p.panels * p.eblocks * p.slices)),
+                     dim3(64 * NW), 0, st, a, p.panels, p.eblocks, p.slices);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 size_t mok_logits_bwd_part_bytes(int64_t T, int H, int E) {
-  const DwrPlan p = dwr_plan(T, H, E);
+  const Plan p = dwr_plan(T, H, E);
   return p.slices > 1 ? (size_t)p.slices * E * H * 4 : 0;
 }
 
-hipError_t mok_launch_logits_bwd_dx(const mok_logits_bwd_args& a, hipStream_t st) {
-  if (a.T <= 0) return hipSuccess;
-  const int64_t blocks = (a.T + 31) / 32;
-  const auto launch = [&](auto ks, auto nw) {
-    constexpr int KS = decltype(ks)::value, NW = decltype(nw)::value;
-    const int panels = (a.H + 32 * NW - 1) / (32 * NW);
-    int64_t s = (512 + panels - 1) / panels;
-    if (s > blocks) s = blocks;
-    hipLaunchKernelGGL((router_dx_kernel<KS, NW>), dim3((unsigned)(panels * s)), dim3(64 * NW), 0, st, a, panels, (int)s);
-  };
-  using std::integral_constant;
-  if (a.E <= 16) launch(integral_constant<int, 1>{}, integral_constant<int, 8>{});
-  else if (a.E <= 32) launch(integral_constant<int, 2>{}, integral_constant<int, 8>{});
-  else if (a.E <= 64) launch(integral_constant<int, 4>{}, integral_constant<int, 8>{});
-  else if (a.E <= 128) launch(integral_constant<int, 8>{}, integral_constant<int, 8>{});
-  else if (a.E <= 256) launch(integral_constant<int, 16>{}, integral_constant<int, 8>{});
-  else launch(integral_constant<int, 32>{}, integral_constant<int, 4>{});
-  return hipGetLastError();
-}
-
-hipError_t mok_launch_logits_bwd_dwr(const mok_logits_bwd_args& a, hipStream_t st) {
-  const DwrPlan p = dwr_plan(a.T, a.H, a.E);
-  const dim3 grid((unsigned)(p.panels * p.eblocks * p.slices));
-  if (p.mt == 1)
-    hipLaunchKernelGGL(router_dwr_slices_kernel<1>, grid, dim3(256), 0, st, a, p.panels, p.eblocks, p.slices);
-  else if (p.mt == 2)
-    hipLaunchKernelGGL(router_dwr_slices_kernel<2>, grid, dim3(256), 0, st, a, p.panels, p.eblocks, p.slices);
-  else
-    hipLaunchKernelGGL(router_dwr_slices_kernel<4>, grid, dim3(256), 0, st, a, p.panels, p.eblocks, p.slices);
-  if (p.slices > 1) {
-    const hipError_t e = hipGetLastError();
+hipError_t mok_launch_logits_bwd(const mok_logits_bwd_args& a, hipStream_t st) {
+  const Plan p = dwr_plan(a.T, a.H, a.E);
+  hipError_t e = hipSuccess;
+  if (a.E <= 32) e = launch<1, true, true, 8>(a, p, st);
+  else if (a.E <= 64) e = launch<2, true, true, 8>(a, p, st);
+  else {
+    if (a.T > 0)
+      e = a.E <= 128   ? launch<4, true, false, 8>(a, plan_of(a.T, a.H, 256, 1, GWX), st)
+          : a.E <= 256 ? launch<8, true, false, 8>(a, plan_of(a.T, a.H, 256, 1, GWX), st)
+                       : launch<16, true, false, 4>(a, plan_of(a.T, a.H, 128, 1, GWX), st);
     if (e != hipSuccess) return e;
-    const int64_t n4 = (int64_t)a.E * a.H / 4;
-    hipLaunchKernelGGL(router_dwr_join_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st, a.part, p.slices,
-                       n4, a.dwr);
+    e = launch<4, false, true, 8>(a, p, st);
   }
+  if (e != hipSuccess || p.slices <= 1) return e;
+  const int64_t n4 = (int64_t)a.E * a.H / 4;
+  hipLaunchKernelGGL(router_dwr_join_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st, a.part, p.slices, n4,
+                     a.dwr);
   return hipGetLastError();
 }

@@ -171,9 +171,8 @@ mok_status mok_router_logits_backward(const mok_problem* problem, const void* x,
   a.dwr = d_w_router;
   a.part = static_cast<float*>(workspace);
   hipStream_t st = (hipStream_t)stream;
-  if (T > 0) MOK_RUN("router_logits_dx", mok_launch_logits_bwd_dx(a, st));
-  // (no tokens: the sums over them are empty)
-  MOK_RUN("router_logits_dwr", mok_launch_logits_bwd_dwr(a, st));
+  // (no tokens: the sums over them are empty, and there is no dx)
+  MOK_RUN("router_logits_backward", mok_launch_logits_bwd(a, st));
   return MOK_OK;
 }
 

@@ -44,5 +44,4 @@ struct mok_logits_bwd_args {
   float* part;                         // [slices][E][H]
 };
 size_t mok_logits_bwd_part_bytes(int64_t T, int H, int E);
-hipError_t mok_launch_logits_bwd_dx(const mok_logits_bwd_args& a, hipStream_t st);
-hipError_t mok_launch_logits_bwd_dwr(const mok_logits_bwd_args& a, hipStream_t st);
+hipError_t mok_launch_logits_bwd(const mok_logits_bwd_args& a, hipStream_t st);   // with no tokens: dWr = 0 alone
