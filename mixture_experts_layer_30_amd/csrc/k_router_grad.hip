@@ -58,7 +58,7 @@ MOK_DEV uint4 load16(buf_t b, uint32_t off) {
   return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0));
 }
 MOK_DEV void store16(buf_t b, uint32_t off, const uint4& v) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), b, (int)off, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), b, (int)off, 0, 2);
 }
 
 // Workgroup b of n in an order that gives each of the eight dies (workgroups go
@@ -117,14 +117,15 @@ MOK_DEV void steps(const Slice& s, F&& f) {
 MOK_DEV int swz(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
 
 template <int KS, bool DX, bool DWR, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(const mok_logits_bwd_args a, int panels, int eblocks,
+__global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(const mok_logits_bwd_args a, int panels, int eblocks,
                                                               int slices) {
   constexpr int BT = 64 * NW, NC = 32 * NW, EP = 32 * KS;
   constexpr int DP = 2 * EP < 128 ? 128 : 2 * EP, XP = 2 * NC + 64;    // row pitches of dl and x in bytes
   constexpr int PARTS = DWR ? 3 : 2;
   constexpr int kD = 32 * DP, kX = DWR ? 32 * XP : 0;
   constexpr int kW = DX ? 32 * (NC + 4) * 4 : 0;                       // 32 rows of Wr, before the first step
-  constexpr int kBuf = 2 * (PARTS * kD + kX), kLds = kBuf > kW ? kBuf : kW;
+  constexpr int OP = 4 * NC + 16, kO = DX ? 32 * OP : 0, NO = 32 * NC / 8 / BT;
+  constexpr int kBuf = 2 * (PARTS * kD + kX) + kO, kLds = kBuf > kW ? kBuf : kW;
   constexpr int WM = KS == 4 ? 2 : 1, TM = KS / WM, TN = WM;           // dWr: 32 x 32 tiles of a wavefront
   constexpr int AHEAD = KS <= 4 ? 2 : 1;         // steps whose loads are in flight
   constexpr int ND = (32 * EP / 4 + BT - 1) / BT, NX = 32 * NC / 8 / BT;   // 16-byte loads of a thread and step
@@ -135,8 +136,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(c
   const int panel = b % panels, eb = b / panels % eblocks, slice = b / (panels * eblocks);
   const Slice sl(a.T, slice, slices);
   const int wave = wave_id(), lane = lane_id(), r = lane & 15, g = lane >> 4;
-  const int c0 = panel * NC, h0 = c0 + 32 * wave, e0 = eb * EP;
-  const bool cols = h0 < a.H;                    // (H is a multiple of 128)
+  const int c0 = panel * NC, e0 = eb * EP;
   const int nks = (a.E - e0 + 31) / 32;          // steps of 32 experts that hold any
 
   // ---- Wr: 32 rows at a time through LDS into the operand's registers
@@ -188,7 +188,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(c
   }
 
   // a thread's places in a step's rows, in bytes from the first of them
-  uint32_t doff[ND], xoff[DWR ? NX : 1], roff[2];
+  uint8_t* o_buf = lds + 2 * (PARTS * kD + kX);
+  uint32_t doff[ND], xoff[DWR ? NX : 1], roff[NO];
 #pragma unroll
   for (int i = 0; i < ND; ++i) {
     const int q = (int)threadIdx.x + BT * i, row = q / (EP / 4), e = 4 * (q % (EP / 4));
@@ -203,12 +204,15 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(c
     }
   }
 #pragma unroll
-  for (int n = 0; n < 2; ++n) roff[n] = cols ? 2u * ((16 * n + r) * a.H + h0 + 8 * g) : kOut;
+  for (int i = 0; i < NO; ++i) {
+    const int q = (int)threadIdx.x + BT * i, c = c0 + 8 * (q % (NC / 8));
+    roff[i] = c < a.H ? 2u * (q / (NC / 8) * a.H + c) : kOut;
+  }
   // of four experts from 4 j on, how many there are (E is not always a multiple of 4: the others' place holds the next
   // token's, and must not enter a product)
   const auto loaded = [&](int i) { return a.E - e0 - 4 * (((int)threadIdx.x + BT * i) % (EP / 4)); };
 
-  uint4 dn[AHEAD][ND], xn[AHEAD][DWR ? NX : 1], rn[AHEAD][DX ? 2 : 1];
+  uint4 dn[AHEAD][ND], xn[AHEAD][DWR ? NX : 1], rn[AHEAD][DX ? NO : 1];
   const auto load = [&](auto buf, int64_t t) {
     constexpr int P = decltype(buf)::value % AHEAD;
     const int64_t left = min(sl.t1 - t, (int64_t)32);                  // tokens of the step
@@ -227,7 +231,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(c
     if constexpr (DX) {
       const buf_t res = make_buf(a.res ? a.res + t * a.H : nullptr, min(sl.t1 - t, (int64_t)32) * a.H * 2);
 #pragma unroll
-      for (int n = 0; n < 2; ++n) rn[P][n] = load16(res, roff[n]);
+      for (int i = 0; i < NO; ++i) rn[P][i] = load16(res, roff[i]);
     }
   };
   load(std::integral_constant<int, 0>{}, sl.t0);
@@ -251,7 +255,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(c
   const int wm = wave % WM, wn = wave / WM;
   const int trx = tr * XP + 2 * (32 * wn * TN + tc);
 
-  steps(sl, [&](auto buf, int64_t t) {
+  // a step's values from its registers into its buffers, and the loads of a later one into the registers
+  const auto stage = [&](auto buf, int64_t t) {
     constexpr int P = decltype(buf)::value, R = P % AHEAD;
 #pragma unroll
     for (int i = 0; i < ND; ++i) {
@@ -275,7 +280,11 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(c
       }
     }
     load(buf, t + 32 * AHEAD);
-    // everyone has written these buffers, and is done with the other ones
+  };
+  stage(std::integral_constant<int, 0>{}, sl.t0);
+  steps(sl, [&](auto buf, int64_t t) {
+    constexpr int P = decltype(buf)::value, R = P % AHEAD;
+    // everyone has written this step's buffers, and is done with the other ones
     barrier_lds_only();
     if constexpr (DWR) {
       const auto pair = [&](const uint8_t* lo, const uint8_t* hi) {
@@ -291,6 +300,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(c
           const uint8_t* p = x_buf(P) + trx + 16 * k * XP + 64 * n;
           xf[n] = pair(p, p + 4 * XP);
         }
+        if (k == 0) stage(std::integral_constant<int, P ^ 1>{}, t + 32);
 #pragma unroll
         for (int m = 0; m < TM; ++m)
 #pragma unroll
@@ -318,6 +328,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(c
 #pragma unroll
             for (int p = 0; p < 2; ++p)
               d[n][p] = *reinterpret_cast<const uint4*>(dl_buf(P, p) + 16 * n * DP + at_step(get0, s));
+          if (!DWR && s == 0) stage(std::integral_constant<int, P ^ 1>{}, t + 32);
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -328,15 +339,22 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void router_grad_kernel(c
             }
         }
       }
+      // through LDS, so that rows are read and written 512 bytes at a time
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          *reinterpret_cast<f32x4_t*>(o_buf + (16 * n + r) * OP + 4 * (32 * wave + 8 * g + 4 * m)) = o[m][n];
+      barrier_lds_only();
       const buf_t dx = make_buf(a.dx + t * a.H, min(sl.t1 - t, (int64_t)32) * a.H * 2);
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const uint32_t rw[4] = {rn[R][n].x, rn[R][n].y, rn[R][n].z, rn[R][n].w};
-        uint32_t v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = pack_bf16x2(o[i >> 1][n][2 * (i & 1)] + bf_lo(rw[i]), o[i >> 1][n][2 * (i & 1) + 1] + bf_hi(rw[i]));
-        store16(dx, roff[n], make_uint4(v[0], v[1], v[2], v[3]));
+      for (int i = 0; i < NO; ++i) {
+        const int q = (int)threadIdx.x + BT * i;
+        const float4* p = reinterpret_cast<const float4*>(o_buf + q / (NC / 8) * OP + 32 * (q % (NC / 8)));
+        const float4 x = p[0], y = p[1];
+        const uint4 w = rn[R][i];
+        store16(dx, roff[i], make_uint4(pack_bf16x2(x.x + bf_lo(w.x), x.y + bf_hi(w.x)), pack_bf16x2(x.z + bf_lo(w.y), x.w + bf_hi(w.y)),
+                                        pack_bf16x2(y.x + bf_lo(w.z), y.y + bf_hi(w.z)), pack_bf16x2(y.z + bf_lo(w.w), y.w + bf_hi(w.w))));
       }
       load_res(buf, t + 32 * AHEAD);
     }
@@ -376,28 +394,23 @@ __global__ __launch_bounds__(256) void router_dwr_join_kernel(const float* __res
 #define DWR_WG4 256
 #define DX_WG 512
 #endif
-#ifndef GW1
-#define GW1 256
-#define GW2 256
-#define GW4 256
-#define GWX 256
-#endif
-// workgroups to aim at: as many as are resident together
+// A workgroup a CU, and two steps of tokens at least (1037 tokens x 2048, 60
+// experts: 16.3 us with two, 17.2 with one, 18.4 with four: partial sums against
+// workgroups). Two workgroups a CU of four wavefronts took 4 to 8% longer.
+constexpr int kWorkgroups = 256;
 struct Plan {
   int panels, eblocks, slices;
 };
-Plan plan_of(int64_t T, int H, int columns, int eblocks, int workgroups) {
+Plan plan_of(int64_t T, int H, int columns, int eblocks) {
   Plan p;
   p.panels = (H + columns - 1) / columns;
   p.eblocks = eblocks;
-  const int64_t blocks = (T + 31) / 32, s = workgroups / ((int64_t)p.panels * eblocks);
-  p.slices = (int)(s < 1 ? 1 : s < blocks ? s : blocks < 1 ? 1 : blocks);
+  const int64_t steps = (T + 31) / 32, most = steps < 2 ? 1 : steps / 2, s = kWorkgroups / ((int64_t)p.panels * eblocks);
+  p.slices = (int)(s < 1 ? 1 : s < most ? s : most);
   return p;
 }
 // of the launch that forms dWr
-Plan dwr_plan(int64_t T, int H, int E) {
-  return plan_of(T, H, 256, (E + 127) / 128, E <= 32 ? GW1 : E <= 64 ? GW2 : GW4);
-}
+Plan dwr_plan(int64_t T, int H, int E) { return plan_of(T, H, 256, (E + 127) / 128); }
 
 template <int KS, bool DX, bool DWR, int NW>
 hipError_t launch(const mok_logits_bwd_args& a, const Plan& p, hipStream_t st) {
@@ -420,9 +433,9 @@ hipError_t mok_launch_logits_bwd(const mok_logits_bwd_args& a, hipStream_t st) {
   else if (a.E <= 64) e = launch<2, true, true, 8>(a, p, st);
   else {
     if (a.T > 0)
-      e = a.E <= 128   ? launch<4, true, false, 8>(a, plan_of(a.T, a.H, 256, 1, GWX), st)
-          : a.E <= 256 ? launch<8, true, false, 8>(a, plan_of(a.T, a.H, 256, 1, GWX), st)
-                       : launch<16, true, false, 4>(a, plan_of(a.T, a.H, 128, 1, GWX), st);
+      e = a.E <= 128   ? launch<4, true, false, 8>(a, plan_of(a.T, a.H, 256, 1), st)
+          : a.E <= 256 ? launch<8, true, false, 8>(a, plan_of(a.T, a.H, 256, 1), st)
+                       : launch<16, true, false, 4>(a, plan_of(a.T, a.H, 128, 1), st);
     if (e != hipSuccess) return e;
     e = launch<4, false, true, 8>(a, p, st);
   }
