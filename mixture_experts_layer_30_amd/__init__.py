@@ -341,7 +341,8 @@ def _device_of(t):
     global _torch
     if _torch is None:
         import torch
-        _types.update(bf16=torch.bfloat16, u8=torch.uint8, f32=torch.float32, i32=torch.int32)
+        _types.update(bf16=torch.bfloat16, u8=torch.uint8, f32=torch.float32, i32=torch.int32,
+                      bool=torch.bool)
         _torch = torch
     return t.get_device()
 
@@ -358,6 +359,10 @@ def _want(what, t, dtype, shape, index, rows=False):
         raise MokError(MOK_ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, wanted {dtype} {tuple(shape)}")
     if not (rows and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
         raise MokError(MOK_ERR_INVALID_ARG, f"{what}: strides {t.stride()}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _pitch(t):
@@ -537,7 +542,26 @@ def norm_workspace(problem):
 
 
 def _norm_call(problem, ld_x, ld_s, ld_y):
-    return NormProblem(problem.T, problem.H, ld_x, ld_s, ld_y, problem.eps, problem.weight_f32)
+    if not (ld_x or ld_s or ld_y or problem.ld_x or problem.ld_s or problem.ld_y):
+        return ctypes.byref(problem)
+    return ctypes.byref(NormProblem(problem.T, problem.H, ld_x, ld_s, ld_y, problem.eps, problem.weight_f32))
+
+
+def _norm_forward(problem, dev, x, weight, y, residual, sum_out, rstd, q, scales, stream):
+    """norm_forward with outputs that are known to fit."""
+    T, H = problem.T, problem.H
+    _want("x", x, "bf16", (T, H), dev, rows=True)
+    if weight is not None:
+        _want("weight", weight, "f32" if problem.weight_f32 else "bf16", (H,), dev)
+    ld_s = 0
+    if residual is not None:
+        _want("residual", residual, "bf16", (T, H), dev, rows=True)
+        ld_s = _pitch(residual)
+        if _pitch(sum_out) != ld_s:
+            raise MokError(MOK_ERR_INVALID_ARG, "sum_out: another row pitch than residual")
+    _run("mok_norm_forward", dev, stream, lib().mok_norm_forward,
+         _norm_call(problem, _pitch(x), ld_s, 0 if y is None else _pitch(y)), x.data_ptr(), _addr(residual), _addr(weight),
+         _addr(y), _addr(sum_out), _addr(rstd), _addr(q), _addr(scales))
 
 
 def norm_forward(problem, x, weight, y=None, residual=None, sum_out=None, rstd=None, q=None, scales=None, stream=None):
@@ -546,51 +570,45 @@ def norm_forward(problem, x, weight, y=None, residual=None, sum_out=None, rstd=N
     multiple of 8 (taken from the tensors). weight [H] in the problem's type, or None for ones."""
     T, H = problem.T, problem.H
     dev = _device_of(x)
-    _want("x", x, "bf16", (T, H), dev, rows=True)
-    if weight is not None:
-        _want("weight", weight, "f32" if problem.weight_f32 else "bf16", (H,), dev)
-    ld_y = ld_s = 0
-    if y is not None:
-        _want("y", y, "bf16", (T, H), dev, rows=True)
-        ld_y = _pitch(y)
     if (residual is None) != (sum_out is None) or (q is None) != (scales is None):
         raise MokError(MOK_ERR_INVALID_ARG, "residual with sum_out, and q with scales, come together")
-    if residual is not None:
-        _want("residual", residual, "bf16", (T, H), dev, rows=True)
+    if y is not None:
+        _want("y", y, "bf16", (T, H), dev, rows=True)
+    if sum_out is not None:
         _want("sum_out", sum_out, "bf16", (T, H), dev, rows=True)
-        ld_s = _pitch(residual)
-        if _pitch(sum_out) != ld_s:
-            raise MokError(MOK_ERR_INVALID_ARG, "sum_out: another row pitch than residual")
     if rstd is not None:
         _want("rstd", rstd, "f32", (T,), dev)
     if q is not None:
         _want("q", q, "u8", (T, H), dev)
         _want("scales", scales, "u8", (T, H // 32), dev)
-    p = _norm_call(problem, _pitch(x), ld_s, ld_y)
-    _run("mok_norm_forward", dev, stream, lib().mok_norm_forward, ctypes.byref(p), x.data_ptr(), _ptr(residual),
-         _ptr(weight), _ptr(y), _ptr(sum_out), _ptr(rstd), _ptr(q), _ptr(scales))
+    _norm_forward(problem, dev, x, weight, y, residual, sum_out, rstd, q, scales, stream)
+
+
+def _norm_backward(problem, dev, dy, z, rstd, weight, dx, dw, workspace, d_sum, stream):
+    """norm_backward with outputs that are known to fit."""
+    T, H = problem.T, problem.H
+    _want("dy", dy, "bf16", (T, H), dev, rows=True)
+    _want("z", z, "bf16", (T, H), dev, rows=True)
+    _want("rstd", rstd, "f32", (T,), dev)
+    if weight is not None:
+        _want("weight", weight, "f32" if problem.weight_f32 else "bf16", (H,), dev)
+    if d_sum is not None:
+        _want("d_sum", d_sum, "bf16", (T, H), dev, rows=True)
+        if _pitch(d_sum) != _pitch(dx):
+            raise MokError(MOK_ERR_INVALID_ARG, "dx: another row pitch than d_sum")
+    _run("mok_norm_backward", dev, stream, lib().mok_norm_backward, _norm_call(problem, 0, _pitch(dx), _pitch(dy)),
+         dy.data_ptr(), z.data_ptr(), _pitch(z), rstd.data_ptr(), _addr(weight), _addr(d_sum), dx.data_ptr(), _addr(dw),
+         *_scratch(workspace, dev))
 
 
 def norm_backward(problem, dy, z, rstd, weight, dx, dw, workspace, d_sum=None, stream=None):
     """dx [T][H] bf16 (with d_sum added) and dw [H] in the weight's type, from the forward's stored stream z and rstd.
     weight and dw may be None (ones; no gradient). d_sum and dx share one row pitch, dy and z may have others."""
-    T, H = problem.T, problem.H
     dev = _device_of(dy)
-    for n, t in (("dy", dy), ("z", z), ("dx", dx)):
-        _want(n, t, "bf16", (T, H), dev, rows=True)
-    _want("rstd", rstd, "f32", (T,), dev)
-    wt = "f32" if problem.weight_f32 else "bf16"
-    if weight is not None:
-        _want("weight", weight, wt, (H,), dev)
+    _want("dx", dx, "bf16", (problem.T, problem.H), dev, rows=True)
     if dw is not None:
-        _want("dw", dw, wt, (H,), dev)
-    if d_sum is not None:
-        _want("d_sum", d_sum, "bf16", (T, H), dev, rows=True)
-        if _pitch(d_sum) != _pitch(dx):
-            raise MokError(MOK_ERR_INVALID_ARG, "dx: another row pitch than d_sum")
-    p = _norm_call(problem, 0, _pitch(dx), _pitch(dy))
-    _run("mok_norm_backward", dev, stream, lib().mok_norm_backward, ctypes.byref(p), dy.data_ptr(), z.data_ptr(),
-         _pitch(z), rstd.data_ptr(), _ptr(weight), _ptr(d_sum), dx.data_ptr(), _ptr(dw), *_scratch(workspace, dev))
+        _want("dw", dw, "f32" if problem.weight_f32 else "bf16", (problem.H,), dev)
+    _norm_backward(problem, dev, dy, z, rstd, weight, dx, dw, workspace, d_sum, stream)
 
 
 # ---------------------------------------------------------------- router losses
@@ -618,60 +636,83 @@ def router_forward_logits(problem, x, w_router, bias, topk_ids, topk_w, logits, 
 
 def _mask(mask, T, dev):
     """A token mask as the bytes of a bool or uint8 tensor."""
-    if mask is not None and mask.dtype is _torch.bool:
-        mask = mask.view(_torch.uint8)
-    if mask is not None:
+    if mask is None:
+        return None
+    if mask.dtype is _torch.bool:
+        _want("mask", mask, "bool", (T,), dev)
+    else:
         _want("mask", mask, "u8", (T,), dev)
-    return _ptr(mask)
+    return mask.data_ptr()
+
+
+def _router_losses(problem, dev, logits, topk_ids, losses, counts, prob_sum, n_tokens, workspace, mask, stream):
+    """router_losses with outputs that are known to fit."""
+    T = problem.T
+    _want("logits", logits, "f32", (T, problem.E), dev)
+    _want("topk_ids", topk_ids, "i32", (T, problem.topk), dev)
+    _run("mok_router_losses", dev, stream, lib().mok_router_losses, ctypes.byref(problem), logits.data_ptr(),
+         topk_ids.data_ptr(), _mask(mask, T, dev), losses.data_ptr(), counts.data_ptr(), prob_sum.data_ptr(),
+         n_tokens.data_ptr(), *_scratch(workspace, dev))
 
 
 def router_losses(problem, logits, topk_ids, losses, counts, prob_sum, n_tokens, workspace, mask=None, stream=None):
     """logits [T][E] fp32, topk_ids [T][k] int32, mask [T] bool or uint8 (None: every token) -> losses [2] fp32
     (balance, z), counts [E] int32, prob_sum [E] fp32, n_tokens [1] int32."""
-    T, E, k = problem.T, problem.E, problem.topk
     dev = _device_of(logits)
-    for n, t, dtype, shape in (("logits", logits, "f32", (T, E)), ("topk_ids", topk_ids, "i32", (T, k)),
-                               ("losses", losses, "f32", (2,)), ("counts", counts, "i32", (E,)),
-                               ("prob_sum", prob_sum, "f32", (E,)), ("n_tokens", n_tokens, "i32", (1,))):
+    for n, t, dtype, shape in (("losses", losses, "f32", (2,)), ("counts", counts, "i32", (problem.E,)),
+                               ("prob_sum", prob_sum, "f32", (problem.E,)), ("n_tokens", n_tokens, "i32", (1,))):
         _want(n, t, dtype, shape, dev)
-    _run("mok_router_losses", dev, stream, lib().mok_router_losses, ctypes.byref(problem), logits.data_ptr(),
-         topk_ids.data_ptr(), _mask(mask, T, dev), losses.data_ptr(), counts.data_ptr(), prob_sum.data_ptr(),
-         n_tokens.data_ptr(), *_scratch(workspace, dev))
+    _router_losses(problem, dev, logits, topk_ids, losses, counts, prob_sum, n_tokens, workspace, mask, stream)
+
+
+def _router_losses_backward(problem, dev, logits, topk_ids, counts, n_tokens, d_losses, d_logits, topk_w, d_topk_w, mask,
+                            stream):
+    """router_losses_backward with a d_logits that is known to fit."""
+    T, E, k = problem.T, problem.E, problem.topk
+    if (topk_w is None) != (d_topk_w is None):
+        raise MokError(MOK_ERR_INVALID_ARG, "topk_w and d_topk_w come together")
+    _want("logits", logits, "f32", (T, E), dev)
+    _want("topk_ids", topk_ids, "i32", (T, k), dev)
+    _want("counts", counts, "i32", (E,), dev)
+    _want("n_tokens", n_tokens, "i32", (1,), dev)
+    _want("d_losses", d_losses, "f32", (2,), dev)
+    if topk_w is not None:
+        _want("topk_w", topk_w, "f32", (T, k), dev)
+        _want("d_topk_w", d_topk_w, "f32", (T, k), dev)
+    _run("mok_router_losses_backward", dev, stream, lib().mok_router_losses_backward, ctypes.byref(problem),
+         logits.data_ptr(), topk_ids.data_ptr(), _mask(mask, T, dev), counts.data_ptr(), n_tokens.data_ptr(),
+         d_losses.data_ptr(), _addr(topk_w), _addr(d_topk_w), d_logits.data_ptr())
 
 
 def router_losses_backward(problem, logits, topk_ids, counts, n_tokens, d_losses, d_logits, topk_w=None, d_topk_w=None,
                            mask=None, stream=None):
     """d_logits [T][E] fp32 (may be logits) from d_losses [2] fp32 on the device and, with topk_w and d_topk_w
     [T][k] fp32, through the combine weights."""
-    T, E, k = problem.T, problem.E, problem.topk
     dev = _device_of(logits)
-    if (topk_w is None) != (d_topk_w is None):
-        raise MokError(MOK_ERR_INVALID_ARG, "topk_w and d_topk_w come together")
-    for n, t, dtype, shape in (("logits", logits, "f32", (T, E)), ("topk_ids", topk_ids, "i32", (T, k)),
-                               ("counts", counts, "i32", (E,)), ("n_tokens", n_tokens, "i32", (1,)),
-                               ("d_losses", d_losses, "f32", (2,)), ("d_logits", d_logits, "f32", (T, E))):
-        _want(n, t, dtype, shape, dev)
-    if topk_w is not None:
-        _want("topk_w", topk_w, "f32", (T, k), dev)
-        _want("d_topk_w", d_topk_w, "f32", (T, k), dev)
-    _run("mok_router_losses_backward", dev, stream, lib().mok_router_losses_backward, ctypes.byref(problem),
-         logits.data_ptr(), topk_ids.data_ptr(), _mask(mask, T, dev), counts.data_ptr(), n_tokens.data_ptr(),
-         d_losses.data_ptr(), _ptr(topk_w), _ptr(d_topk_w), d_logits.data_ptr())
+    _want("d_logits", d_logits, "f32", (problem.T, problem.E), dev)
+    _router_losses_backward(problem, dev, logits, topk_ids, counts, n_tokens, d_losses, d_logits, topk_w, d_topk_w, mask,
+                            stream)
+
+
+def _router_logits_backward(problem, dev, x, w_router, d_logits, dx, d_w_router, workspace, residual, stream):
+    """router_logits_backward with outputs that are known to fit."""
+    T, H, E = problem.T, problem.H, problem.E
+    _want("x", x, "bf16", (T, H), dev)
+    _want("w_router", w_router, "f32", (E, H), dev)
+    _want("d_logits", d_logits, "f32", (T, E), dev)
+    if residual is not None:
+        _want("residual", residual, "bf16", (T, H), dev)
+    _run("mok_router_logits_backward", dev, stream, lib().mok_router_logits_backward, ctypes.byref(problem),
+         x.data_ptr(), w_router.data_ptr(), d_logits.data_ptr(), _addr(residual), dx.data_ptr(), d_w_router.data_ptr(),
+         *_scratch(workspace, dev))
 
 
 def router_logits_backward(problem, x, w_router, d_logits, dx, d_w_router, workspace, residual=None, stream=None):
     """dx [T][H] bf16 = d_logits . w_router (+ residual, which may be dx), d_w_router [E][H] fp32 = d_logits^T . x."""
-    T, H, E = problem.T, problem.H, problem.E
     dev = _device_of(x)
-    for n, t, dtype, shape in (("x", x, "bf16", (T, H)), ("w_router", w_router, "f32", (E, H)),
-                               ("d_logits", d_logits, "f32", (T, E)), ("dx", dx, "bf16", (T, H)),
-                               ("d_w_router", d_w_router, "f32", (E, H))):
-        _want(n, t, dtype, shape, dev)
-    if residual is not None:
-        _want("residual", residual, "bf16", (T, H), dev)
-    _run("mok_router_logits_backward", dev, stream, lib().mok_router_logits_backward, ctypes.byref(problem),
-         x.data_ptr(), w_router.data_ptr(), d_logits.data_ptr(), _ptr(residual), dx.data_ptr(), d_w_router.data_ptr(),
-         *_scratch(workspace, dev))
+    _want("dx", dx, "bf16", (problem.T, problem.H), dev)
+    _want("d_w_router", d_w_router, "f32", (problem.E, problem.H), dev)
+    _router_logits_backward(problem, dev, x, w_router, d_logits, dx, d_w_router, workspace, residual, stream)
 
 
 def trace_enable(on=True):

@@ -14,10 +14,12 @@ from . import (ACT_SILU, MOK_BF16, backward, buffer_sizes, build_schedule, ffn_b
                ffn_forward, forward, forward_fused, make_config, make_ffn_problem, make_mx_problem, make_problem,
                make_norm_problem, mx_matmul, mx_matmul_workspace, mxfp8_quantize, mxfp8_quantize_transposed,
                norm_backward, norm_forward, norm_workspace, router_forward_logits, router_logits_backward,
-               router_losses, router_losses_backward, router_workspace, schedule_layout)
+               router_workspace, schedule_layout)
 from . import mxfp4_dequantize as _mxfp4_dequantize
 from . import mxfp4_quantize as _mxfp4_quantize
 from . import mxfp8_dequantize as _mxfp8_dequantize
+# the calls below that allocate their outputs leave out the checks of those
+from . import _device_of, _norm_backward, _norm_forward, _router_logits_backward, _router_losses, _router_losses_backward
 
 
 @dataclasses.dataclass
@@ -202,7 +204,7 @@ def quantize_ffn_weights_mxfp4(wg, wu, wd):
 # ---------------------------------------------------------------- the norm before the layer
 def mxfp8_dequantize(q, scales):
     """The bf16 values [..., K] of MXFP8 codes and scales."""
-    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    out = torch.empty_like(q, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
     _mxfp8_dequantize(q, scales, out)
     return out
 
@@ -236,22 +238,33 @@ def run_norm_forward(w: NormWorkspace, x, weight, residual=None, out="bf16", y=N
     out: "bf16" (y), "mxfp8" (q and scales, as run_mx_matmul takes them) or "both". weight None: ones."""
     if out not in ("bf16", "mxfp8", "both"):
         raise ValueError(f"out: {out!r}, wanted 'bf16', 'mxfp8' or 'both'")
-    T, H = w.problem.T, w.problem.H
+    given = y is not None or sum_out is not None
+    dense = x.is_contiguous()                    # (the cheapest way to an output of x's shape)
     q = scales = rstd = None
     if out == "mxfp8":
         if y is not None:
             raise ValueError("y: not written with out='mxfp8'")
     elif y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        y = torch.empty_like(x) if dense else x.new_empty(x.shape)
     if out != "bf16":
-        q = torch.empty((T, H), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((T, H // 32), dtype=torch.uint8, device=x.device)
+        q = torch.empty_like(x, dtype=torch.uint8) if dense else x.new_empty(x.shape, dtype=torch.uint8)
+        scales = x.new_empty((w.problem.T, w.problem.H // 32), dtype=torch.uint8)
     if residual is not None and sum_out is None:
-        sum_out = torch.empty_strided(residual.shape, residual.stride(), dtype=residual.dtype, device=x.device)
+        sum_out = _rows_like(residual)
     if w.training:
-        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-    norm_forward(w.problem, x, weight, y, residual, sum_out, rstd, q, scales)
+        rstd = x.new_empty(w.problem.T, dtype=torch.float32)
+    if given:
+        norm_forward(w.problem, x, weight, y, residual, sum_out, rstd, q, scales)
+    else:
+        _norm_forward(w.problem, _device_of(x), x, weight, y, residual, sum_out, rstd, q, scales, None)
     return NormOutput(y, x if residual is None else sum_out, rstd, q, scales)
+
+
+def _rows_like(t):
+    """An empty tensor of t's shape and row pitch."""
+    if t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
 
 
 def run_norm_backward(w: NormWorkspace, z, rstd, weight, dy, d_sum=None, dx=None):
@@ -259,11 +272,12 @@ def run_norm_backward(w: NormWorkspace, z, rstd, weight, dy, d_sum=None, dx=None
     added to dx. dw is None without a weight."""
     if not w.training:
         raise ValueError("a norm workspace without training has no backward")
-    if dx is None:
-        like = dy if d_sum is None else d_sum
-        dx = torch.empty_strided(like.shape, like.stride(), dtype=torch.bfloat16, device=dy.device)
     dw = None if weight is None else torch.empty_like(weight)
-    norm_backward(w.problem, dy, z, rstd, weight, dx, dw, w.workspace, d_sum=d_sum)
+    if dx is not None:
+        norm_backward(w.problem, dy, z, rstd, weight, dx, dw, w.workspace, d_sum=d_sum)
+    else:
+        dx = _rows_like(dy if d_sum is None else d_sum)
+        _norm_backward(w.problem, _device_of(dy), dy, z, rstd, weight, dx, dw, w.workspace, d_sum, None)
     return dx, dw
 
 
@@ -300,10 +314,9 @@ def run_router_forward(w: RouterWorkspace, x, w_router, bias=None):
 
 def run_router_losses(w: RouterWorkspace, logits, topk_ids, mask=None):
     """The balance and z losses of the tokens that mask [T] keeps (None: all), and the sums under them."""
-    E, dev = w.problem.E, logits.device
-    out = RouterLosses(torch.empty(2, dtype=torch.float32, device=dev), torch.empty(E, dtype=torch.int32, device=dev),
-                       torch.empty(E, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev))
-    router_losses(w.problem, logits, topk_ids, *out, w.workspace, mask=mask)
+    E = w.problem.E
+    out = RouterLosses(logits.new_empty(2), topk_ids.new_empty(E), logits.new_empty(E), topk_ids.new_empty(1))
+    _router_losses(w.problem, _device_of(logits), logits, topk_ids, *out, w.workspace, mask, None)
     return out
 
 
@@ -312,15 +325,17 @@ def run_router_losses_backward(w: RouterWorkspace, logits, topk_ids, sums: Route
     """d_logits from the gradients of the two losses (a tensor on the device) and, with topk_w and the layer's
     d_topk_w, through the combine weights. sums: what run_router_losses returned for the same mask."""
     d_logits = torch.empty_like(logits)
-    router_losses_backward(w.problem, logits, topk_ids, sums.counts, sums.n_tokens, d_losses, d_logits, topk_w, d_topk_w,
-                           mask=mask)
+    _router_losses_backward(w.problem, _device_of(logits), logits, topk_ids, sums.counts, sums.n_tokens, d_losses,
+                            d_logits, topk_w, d_topk_w, mask, None)
     return d_logits
 
 
 def run_router_logits_backward(w: RouterWorkspace, x, w_router, d_logits, residual=None, dx=None):
     """(dx, d_w_router); residual, the layer's own dx, is added (and may be the dx passed in)."""
-    if dx is None:
-        dx = torch.empty_like(x)
     dwr = torch.empty_like(w_router)
-    router_logits_backward(w.problem, x, w_router, d_logits, dx, dwr, w.workspace, residual=residual)
+    if dx is not None:
+        router_logits_backward(w.problem, x, w_router, d_logits, dx, dwr, w.workspace, residual=residual)
+    else:
+        dx = torch.empty_like(x)
+        _router_logits_backward(w.problem, _device_of(x), x, w_router, d_logits, dx, dwr, w.workspace, residual, None)
     return dx, dwr
