@@ -8,9 +8,15 @@
 // each chosen expert. As the p of a token add up to 1, c may be taken from its
 // mean k n / E in that difference; then nearly even counts lose no digits.
 //
-// Both are one pass over the logits and bound by reading (and writing) them. A
-// token lies in L lanes of a wavefront, 4 I experts each (lane l: the experts
-// 4 (l + L i) .. + 3), so a wavefront works on 64 / L tokens at once.
+// Both are one pass over the logits and bound by reading (and writing) them, small
+// ones by latency. A token lies in L lanes of a wavefront, 4 I experts each (lane l:
+// the experts 4 (l + L i) .. + 3), so a wavefront works on 64 / L tokens at once.
+// 65536 tokens x 512 experts: forward 34 us for 134 MB and 8 us for the joining of
+// the sums, gradient 45 us for 268 MB (6.0 TB/s); 16384 x 128: 5.5, 7 and 9.8 us.
+// Tried and dropped: several rows side by side in a lane, and loading a row ahead
+// (the forward as it is, the gradient 5 to 10 us longer for its registers and LDS);
+// joining in one launch whose last workgroup goes on (every wavefront's fence writes
+// an L2 back: 15 us at 203 tokens).
 #include <type_traits>
 
 #include "lane_reduce.h"

@@ -1,11 +1,16 @@
 // Router backward from the gradient of every logit: dx = dl . Wr (+ residual)
-// and dWr = dl^T . x, on the matrix cores. dl and Wr
-// are fp32, the operands bf16: for dWr, which is fp32, dl is split exactly into
-// three bf16 parts (x is bf16, so every product is exact); for dx, which is
-// rounded to bf16, dl and Wr go in as two parts each, the nearest bf16 and the
-// nearest to what that leaves (at most 2^-16 of a value is lost), and the
-// product of the two small parts, at most 2^-16 of the whole, is left out.
+// and dWr = dl^T . x, on the matrix cores. dl and Wr are fp32, the operands bf16:
+// for dWr, which is fp32, dl is split exactly into three bf16 parts (x is bf16, so
+// every product is exact); for dx, which is rounded to bf16, dl and Wr go in as two
+// parts each, the nearest bf16 and the nearest to what that leaves (at most 2^-16 of
+// a value is lost), and the product of the two small parts, at most 2^-16 of the
+// whole, is left out.
 //
+// Bound by memory with few experts (16384 x 7168, 32 experts, residual: 141 us for
+// 708 MB, 5.0 TB/s; a copy reaches 4.8). With 128 experts (16384 x 4096) the
+// instructions alone are 20 us of either launch, and both come out nearer to the sum
+// of memory and instructions than to the larger: dx 64 us for 268 MB, dWr 57 us for
+// 134 MB and 34 MB of partial sums (37 without its products).
 #include <type_traits>
 
 #include "gemm_core.h"
@@ -47,8 +52,9 @@ MOK_DEV f32x4_t mfma16(const uint4& a, const uint4& b, f32x4_t c) {
 // Loads and stores go through buffer descriptors: what lies past a descriptor's
 // bytes reads as zero and is not written, so that no access stands in a branch.
 // (With branches round them the compiler cannot tell how many are in flight at the
-// wait for one, and waits for all: a step then takes as long as the memory's
-// latency, 164 us instead of xxx for 16384 x 4096 with 128 experts.)
+// wait for one, and waits for all: dWr of 16384 x 4096 with 128 experts 77 us against
+// 57.) A 16-byte load that the end of the bytes cuts reads its part before the end and
+// zeros (checked on gfx950). Offsets are 32 bits: a step's rows, at most 2^26 bytes.
 typedef __amdgpu_buffer_rsrc_t buf_t;
 constexpr uint32_t kOut = 0x7ffffff0u;           // past every descriptor's bytes
 MOK_DEV buf_t make_buf(const void* p, int64_t bytes) {
@@ -89,12 +95,12 @@ MOK_DEV void steps(const Slice& s, F&& f) {
 // ---------------------------------------------------------------- kernel
 // A workgroup takes 32 NW columns and a slice of the tokens, 32 tokens at a time
 // through two sets of LDS buffers: while one is multiplied, the other is filled
-// from registers that were loaded two steps ahead (one beyond 128 experts). Its barriers wait for LDS alone
-// (__syncthreads would wait for every load and store in flight, which makes a step
-// as long as the memory's latency). Up to 128 experts the workgroup forms both
-// results (DX and DWR), so that dl is read and split once and reading x goes on
-// beside writing dx; beyond, the accumulators of all experts do not fit beside Wr,
-// and there are two launches, that of DWR with 128 experts a workgroup.
+// from registers that were loaded two steps ahead (one beyond 128 experts). Its
+// barriers wait for LDS alone (__syncthreads would wait for every load and store in
+// flight). Up to 64 experts the workgroup forms both results (DX and DWR), so that dl
+// is read and split once (16384 x 4096 with 64 experts: 93 us); beyond, there are not
+// enough registers for Wr beside the accumulators (128 experts in one launch 160 us,
+// in two 130), and DWR takes 128 experts a workgroup.
 //
 // dl of a step lies in LDS as bf16 parts [32 tokens][EP experts]; 16-byte chunk c
 // of token row t at c ^ swz(t): eight rows at one chunk (dx), and four rows at two
@@ -106,7 +112,9 @@ MOK_DEV void steps(const Slice& s, F&& f) {
 // l supplies row l % 16 of an operand, 8 values of K from 8 (l / 16) on, and holds
 // of result column l % 16 the rows 4 (l / 16) + i. Row r of the wavefront's tile m
 // (0, 1) is column 8 (r / 4) + 4 m + r % 4, so a lane ends up with 8 neighbouring
-// columns of a token and four lanes with 64 bytes of it.
+// columns of a token. dx goes through LDS once more, in fp32, so that rows of it and
+// of the residual are written and read in 512 bytes (16384 x 7168 with 32 experts: in
+// the operand's 64-byte pieces 155 us, so 138).
 //
 // dWr: x as it is and dl in its three parts are both read transposed
 // (ds_read_b64_tr_b16: lane 4 q + p of 16 names row q and columns 4 p .. + 3, and
@@ -117,8 +125,8 @@ MOK_DEV void steps(const Slice& s, F&& f) {
 MOK_DEV int swz(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
 
 template <int KS, bool DX, bool DWR, int NW>
-__global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(const mok_logits_bwd_args a, int panels, int eblocks,
-                                                              int slices) {
+__global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(const mok_logits_bwd_args a, int panels,
+                                                                               int eblocks, int slices) {
   constexpr int BT = 64 * NW, NC = 32 * NW, EP = 32 * KS;
   constexpr int DP = 2 * EP < 128 ? 128 : 2 * EP, XP = 2 * NC + 64;    // row pitches of dl and x in bytes
   constexpr int PARTS = DWR ? 3 : 2;
@@ -146,7 +154,7 @@ __global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(c
     float* wl = reinterpret_cast<float*>(lds);
     uint4 wn[NWL];
     const auto load_w = [&](int s) {
-      const buf_t src = make_buf(a.wr + (int64_t)32 * s * a.H + c0, ((int64_t)(a.E - 32 * s) * a.H - c0) * 4);
+      const buf_t src = make_buf(a.wr + (int64_t)32 * s * a.H + c0, ((int64_t)min(a.E - 32 * s, 32) * a.H - c0) * 4);
 #pragma unroll
       for (int i = 0; i < NWL; ++i) {
         const int q = (int)threadIdx.x + BT * i;

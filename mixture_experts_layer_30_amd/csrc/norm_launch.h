@@ -7,7 +7,6 @@
 #include "mok_device.h"
 
 constexpr int kNormMaxH = 32768;
-constexpr int kNormParts = 1024;       // most partial rows of d_weight
 
 struct mok_norm_args {
   int64_t T;
