@@ -113,7 +113,7 @@ template <int L, int I, bool VEC>
 __global__ __launch_bounds__(kFT) void losses_rows_kernel(const mok_losses_args a) {
   constexpr int SPW = 64 / L, TPB = kFWaves * SPW;
   __shared__ int hist[512];
-  __shared__ float ps[kFWaves][4 * L * I];
+  __shared__ __attribute__((aligned(16))) float ps[kFWaves][4 * L * I];
   __shared__ float zs[kFWaves];
   __shared__ int ns[kFWaves];
   __shared__ double red[kFWaves];
