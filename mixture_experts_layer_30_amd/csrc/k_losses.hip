@@ -335,8 +335,7 @@ __global__ __launch_bounds__(kBT) void losses_bwd_kernel(const mok_losses_args a
         s = fmaf(v[i][u], ce[i][u], s);
       }
     s = lanes_sum<L>(s);
-    // (a row that is left out has zeros for v)
-    const float rest = live ? fmaf(gz, lse, -s) : 0.f;
+    const float rest = fmaf(gz, lse, -s);
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int e = 4 * (l + L * i);
@@ -345,10 +344,13 @@ __global__ __launch_bounds__(kBT) void losses_bwd_kernel(const mok_losses_args a
         d = *reinterpret_cast<const float4*>(mine + e);
         *reinterpret_cast<float4*>(mine + e) = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      d.x = fmaf(v[i][0], ce[i][0] + rest, d.x);
-      d.y = fmaf(v[i][1], ce[i][1] + rest, d.y);
-      d.z = fmaf(v[i][2], ce[i][2] + rest, d.z);
-      d.w = fmaf(v[i][3], ce[i][3] + rest, d.w);
+      // (not 0 times the coefficients in rows that are left out: a loss's gradient may have overflowed)
+      if (live) {
+        d.x = fmaf(v[i][0], ce[i][0] + rest, d.x);
+        d.y = fmaf(v[i][1], ce[i][1] + rest, d.y);
+        d.z = fmaf(v[i][2], ce[i][2] + rest, d.z);
+        d.w = fmaf(v[i][3], ce[i][3] + rest, d.w);
+      }
       if constexpr (VEC) {
         if (in && e < a.E) *reinterpret_cast<float4*>(out + e) = d;
       } else {

@@ -127,6 +127,21 @@ def test_losses_tokens(T, E, k):
     check(T, E, k, mask=T % 2 == 1)
 
 
+@pytest.mark.parametrize("E", [7, 8, 128, 512])
+@pytest.mark.parametrize("dl", [(np.inf, 0.0), (0.0, np.nan)])
+def test_losses_backward_of_overflowed_gradients(E, dl):
+    """A token that the mask leaves out keeps the gradient through its combine weights, whatever d_losses holds."""
+    import torch
+    logits, ids, w, g, m = routing(50, E, 2)
+    ws = F.get_router_workspace(50, 128, E, 2)
+    L, I, W, G, M = f32(logits), i32(ids), f32(w), f32(g), torch.from_numpy(m).cuda()
+    o = F.run_router_losses(ws, L, I, mask=M)
+    for sel in ((None, None), (W, G)):
+        a, b = (F.run_router_losses_backward(ws, L, I, o, f32(np.array(v)), *sel, mask=M) for v in (dl, (0.0, 0.0)))
+        assert torch.equal(a[~M], b[~M])
+        assert not torch.isfinite(a[M]).all(1).any()
+
+
 @pytest.mark.parametrize("E,k", [(4, 4), (8, 8), (12, 12), (100, 100), (512, 65)])
 def test_losses_many_picks(E, k):
     check(37, E, k)
