@@ -12,11 +12,12 @@
 // ones by latency. A token lies in L lanes of a wavefront, 4 I experts each (lane l:
 // the experts 4 (l + L i) .. + 3), so a wavefront works on 64 / L tokens at once.
 // 65536 tokens x 512 experts: forward 34 us for 134 MB and 8 us for the joining of
-// the sums, gradient 45 us for 268 MB (6.0 TB/s); 16384 x 128: 5.5, 7 and 9.8 us.
+// the sums, gradient 45 us for 268 MB (6.0 TB/s); 16384 x 128: 5.5, 6.4 and 8.4 us.
 // Tried and dropped: several rows side by side in a lane, and loading a row ahead
 // (the forward as it is, the gradient 5 to 10 us longer for its registers and LDS);
 // joining in one launch whose last workgroup goes on (every wavefront's fence writes
 // an L2 back: 15 us at 203 tokens).
+#include <algorithm>
 #include <type_traits>
 
 #include "lane_reduce.h"
@@ -232,6 +233,55 @@ __global__ __launch_bounds__(kJT) void losses_join_kernel(const mok_losses_args 
   a.counts[e] = n;
 }
 
+// The same for up to C experts by one workgroup, which goes on to the losses: rows
+// of C threads. (Both losses' calls at 65536 x 8: 12.4 us, 13.7 with two launches;
+// 16384 x 64: 14.2, 15.7; 16384 x 128: 21.0 either way; 256 experts: 27.0, 23.8.)
+template <int C>
+__global__ __launch_bounds__(1024) void losses_join_finish_kernel(const mok_losses_args a, int groups) {
+  constexpr int R = 1024 / C;
+  __shared__ float pg[R][C];
+  __shared__ int cg[R][C];
+  __shared__ double red[16], rz[16];
+  __shared__ int rn[16];
+  const int pitch = 2 * a.E + 2;
+  const int e = (int)threadIdx.x % C, r = (int)threadIdx.x / C;
+  float p = 0.f;
+  double z = 0.0;
+  int n = 0, m = 0;
+  if ((int)threadIdx.x < groups) {
+    z = (double)__uint_as_float(a.part[(int64_t)threadIdx.x * pitch + 2 * a.E]);
+    m = (int)a.part[(int64_t)threadIdx.x * pitch + 2 * a.E + 1];
+  }
+  if (e < a.E) {
+#pragma unroll 16
+    for (int i = r; i < groups; i += R) {
+      p += __uint_as_float(a.part[(int64_t)i * pitch + e]);
+      n += (int)a.part[(int64_t)i * pitch + a.E + e];
+    }
+  }
+  pg[r][e] = p;
+  cg[r][e] = n;
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) m += __shfl_xor(m, d);
+  if (lane_id() == 0) rn[threadIdx.x >> 6] = m;
+  z = block_sum<1024>(z, rz);
+  m = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) m += rn[w];
+  double cp = 0.0;
+  if (r == 0 && e < a.E) {
+#pragma unroll
+    for (int i = 1; i < R; ++i) {
+      p += pg[i][e];
+      n += cg[i][e];
+    }
+    a.prob[e] = p;
+    a.counts[e] = n;
+    cp = (double)n * (double)p;
+  }
+  finish<1024>(a, cp, z, m, red);
+}
+
 // the losses, from the joined sums and the workgroups' z and n
 __global__ __launch_bounds__(512) void losses_finish_kernel(const mok_losses_args a, int groups) {
   __shared__ double red[8], rz[8];
@@ -406,6 +456,13 @@ hipError_t mok_launch_losses(const mok_losses_args& a, hipStream_t st) {
   if (groups > 1) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (a.E <= 128) {
+      const auto join = a.E <= 32   ? losses_join_finish_kernel<32>
+                        : a.E <= 64 ? losses_join_finish_kernel<64>
+                                    : losses_join_finish_kernel<128>;
+      hipLaunchKernelGGL(join, dim3(1), dim3(1024), 0, st, a, groups);
+      return hipGetLastError();
+    }
     hipLaunchKernelGGL(losses_join_kernel, dim3((unsigned)((a.E + 31) / 32)), dim3(kJT), 0, st, a, groups);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(losses_finish_kernel, dim3(1), dim3(512), 0, st, a, groups);
@@ -417,9 +474,12 @@ hipError_t mok_launch_losses_backward(const mok_losses_args& a, hipStream_t st) 
   if (a.T <= 0) return hipSuccess;
   by_experts(a.E, [&](auto L, auto I, auto vec) {
     const int tpb = kWaves * 64 / decltype(L)::value;
-    const int64_t blocks = (a.T + tpb - 1) / tpb, cap = 2048;
+    // Two passes a workgroup, once 512 have work: both losses' calls at 16384 x 128 19.6 us, with one pass 21.0, with
+    // four 20.5; up to 2048 workgroups, what the card holds.
+    const int64_t blocks = (a.T + tpb - 1) / tpb;
+    const int64_t groups = std::min<int64_t>(blocks, std::clamp<int64_t>(blocks / 2, 512, 2048));
     hipLaunchKernelGGL((losses_bwd_kernel<decltype(L)::value, decltype(I)::value, decltype(vec)::value>),
-                       dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(kBT), 0, st, a);
+                       dim3((unsigned)groups), dim3(kBT), 0, st, a);
     return 0;
   });
   return hipGetLastError();
