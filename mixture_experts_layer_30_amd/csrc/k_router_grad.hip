@@ -396,12 +396,6 @@ __global__ __launch_bounds__(256) void router_dwr_join_kernel(const float* __res
   reinterpret_cast<float4*>(dwr)[i] = s;
 }
 
-#ifndef DWR_WG1
-#define DWR_WG1 512
-#define DWR_WG2 512
-#define DWR_WG4 256
-#define DX_WG 512
-#endif
 // A workgroup a CU, and two steps of tokens at least (1037 tokens x 2048, 60
 // experts: 16.3 us with two, 17.2 with one, 18.4 with four: partial sums against
 // workgroups). Two workgroups a CU of four wavefronts took 4 to 8% longer.
