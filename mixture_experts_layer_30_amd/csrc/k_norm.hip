@@ -16,7 +16,7 @@
 // Stores carry the nontemporal hint (forward of 16384 x 7168: 156 us with it,
 // 164 without).
 //
-// Forward of 16384 x 7168 with a residual: 157 us, 6.0 TB/s; backward 166 us,
+// Whole calls of 16384 x 7168 with a residual: forward 154 us, 6.1 TB/s; backward 164 us,
 // 5.7 TB/s with the partial sums of d_weight.
 #include <type_traits>
 

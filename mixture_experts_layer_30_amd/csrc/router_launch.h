@@ -21,7 +21,7 @@ struct mok_losses_args {
   int32_t* counts;                     // backward: in
   float* prob;
   int32_t* n;                          // backward: in
-  uint32_t* part;                      // [groups][2E + 2]: prob, counts, z, n of each workgroup; then a counter
+  uint32_t* part;                      // [groups][2E + 2]: prob, counts, z, n of each workgroup
   const float* d_losses;
   const float* w;                      // NULL with g: no gradient through the combine weights
   const float* g;
