@@ -431,13 +431,14 @@ size_t mok_logits_bwd_part_bytes(int64_t T, int H, int E) {
 hipError_t mok_launch_logits_bwd(const mok_logits_bwd_args& a, hipStream_t st) {
   const Plan p = dwr_plan(a.T, a.H, a.E);
   hipError_t e = hipSuccess;
+  // no tokens: empty sums, and nothing that reads Wr, which may be NULL then
+  if (a.T == 0) return launch<4, false, true, 8>(a, p, st);
   if (a.E <= 32) e = launch<1, true, true, 8>(a, p, st);
   else if (a.E <= 64) e = launch<2, true, true, 8>(a, p, st);
   else {
-    if (a.T > 0)
-      e = a.E <= 128   ? launch<4, true, false, 8>(a, plan_of(a.T, a.H, 256, 1), st)
-          : a.E <= 256 ? launch<8, true, false, 8>(a, plan_of(a.T, a.H, 256, 1), st)
-                       : launch<16, true, false, 4>(a, plan_of(a.T, a.H, 128, 1), st);
+    e = a.E <= 128   ? launch<4, true, false, 8>(a, plan_of(a.T, a.H, 256, 1), st)
+        : a.E <= 256 ? launch<8, true, false, 8>(a, plan_of(a.T, a.H, 256, 1), st)
+                     : launch<16, true, false, 4>(a, plan_of(a.T, a.H, 128, 1), st);
     if (e != hipSuccess) return e;
     e = launch<4, false, true, 8>(a, p, st);
   }

@@ -202,6 +202,19 @@ def test_losses_ids_out_of_range_and_picked_twice():
     check(T, E, k, data=(logits, ids, w, g, m))
 
 
+@pytest.mark.parametrize("E", [8, 60, 130])
+def test_logits_backward_of_no_tokens_and_no_operands(E):
+    """Without tokens every input may be NULL; d_w_router is set to zeros."""
+    import ctypes
+    import torch
+    p = mok.make_problem(0, 1024, 128, E, 2)
+    dwr = torch.full((E, 1024), 7.0, device="cuda")
+    st = mok.lib().mok_router_logits_backward(ctypes.byref(p), None, None, None, None, None, dwr.data_ptr(), None, 0,
+                                              torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == mok.MOK_OK and (dwr == 0).all()
+
+
 def test_losses_of_no_tokens():
     import torch
     ws = F.get_router_workspace(0, 128, 9, 2)
