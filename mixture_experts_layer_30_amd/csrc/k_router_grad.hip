@@ -7,10 +7,9 @@
 // whole, is left out.
 //
 // Bound by memory with few experts (16384 x 7168, 32 experts, residual: 141 us for
-// 708 MB, 5.0 TB/s; a copy reaches 4.8). With 128 experts (16384 x 4096) the
-// instructions alone are 20 us of either launch, and both come out nearer to the sum
-// of memory and instructions than to the larger: dx 64 us for 268 MB, dWr 57 us for
-// 134 MB and 34 MB of partial sums (37 without its products).
+// 708 MB, 5.0 TB/s; a copy reaches 4.9), nearly so with 128 (16384 x 4096: 127 us for
+// 415 MB and 34 MB of partial sums that are written and read; from a graph 132, without
+// the matrix instructions 109).
 #include <type_traits>
 
 #include "gemm_core.h"
@@ -82,25 +81,37 @@ struct Slice {
   }
 };
 
-// f(step's buffer as a constant, first token) for every 32 tokens
-template <class F>
+// f(step's buffer, first token) for every 32 tokens. With the loads of two steps in
+// flight (AHEAD) the buffer is a constant, as the registers that hold a step are; with
+// one it is not, and the accumulators have one place (in two copies of the step, which
+// the loop leaves after either, they take twice their registers).
+template <int AHEAD, class F>
 MOK_DEV void steps(const Slice& s, F&& f) {
-  for (int64_t t = s.t0; t < s.t1; t += 64) {
-    f(std::integral_constant<int, 0>{}, t);
-    if (t + 32 >= s.t1) break;
-    f(std::integral_constant<int, 1>{}, t + 32);
+  if constexpr (AHEAD == 1) {
+    int p = 0;
+#pragma unroll 1
+    for (int64_t t = s.t0; t < s.t1; t += 32, p ^= 1) f(p, t);
+  } else {
+    for (int64_t t = s.t0; t < s.t1; t += 64) {
+      f(0, t);
+      if (t + 32 >= s.t1) break;
+      f(1, t + 32);
+    }
   }
 }
 
 // ---------------------------------------------------------------- kernel
 // A workgroup takes 32 NW columns and a slice of the tokens, 32 tokens at a time
 // through two sets of LDS buffers: while one is multiplied, the other is filled
-// from registers that were loaded two steps ahead (one beyond 128 experts). Its
+// from registers that were loaded two steps ahead (one where registers are few). Its
 // barriers wait for LDS alone (__syncthreads would wait for every load and store in
-// flight). Up to 64 experts the workgroup forms both results (DX and DWR), so that dl
-// is read and split once (16384 x 4096 with 64 experts: 93 us); beyond, there are not
-// enough registers for Wr beside the accumulators (128 experts in one launch 160 us,
-// in two 130), and DWR takes 128 experts a workgroup.
+// flight). Up to 64 experts and with much data a workgroup forms both results (DX and
+// DWR), so that dl is read and split once (16384 x 4096 with 64 experts: 92 us, as a
+// pair 95). Else up to 128 experts workgroups of either kind share the CUs, two on each,
+// one's instructions beside the other's copies (16384 x 4096 with 128 experts: 132 us on
+// the card, in two launches 140, one workgroup for both, with spilled registers, 160;
+// 1000 x 4096: 25, 30). Beyond, Wr leaves no registers for a second workgroup: two
+// launches, and DWR takes 128 experts a workgroup.
 //
 // dl of a step lies in LDS as bf16 parts [32 tokens][EP experts]; 16-byte chunk c
 // of token row t at c ^ swz(t): eight rows at one chunk (dx), and four rows at two
@@ -124,23 +135,34 @@ MOK_DEV void steps(const Slice& s, F&& f) {
 // are added in ascending order by router_dwr_join_kernel.
 MOK_DEV int swz(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
 
-template <int KS, bool DX, bool DWR, int NW>
-__global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(const mok_logits_bwd_args a, int panels,
-                                                                               int eblocks, int slices) {
-  constexpr int BT = 64 * NW, NC = 32 * NW, EP = 32 * KS;
-  constexpr int DP = 2 * EP < 128 ? 128 : 2 * EP, XP = 2 * NC + 64;    // row pitches of dl and x in bytes
-  constexpr int PARTS = DWR ? 3 : 2;
-  constexpr int kD = 32 * DP, kX = DWR ? 32 * XP : 0;
-  constexpr int kW = DX ? 32 * (NC + 4) * 4 : 0;                       // 32 rows of Wr, before the first step
-  constexpr int OP = 4 * NC + 16, kO = DX ? 32 * OP : 0, NO = 32 * NC / 8 / BT;
-  constexpr int kBuf = 2 * (PARTS * kD + kX) + kO, kLds = kBuf > kW ? kBuf : kW;
-  constexpr int WM = KS == 4 ? 2 : 1, TM = KS / WM, TN = WM;           // dWr: 32 x 32 tiles of a wavefront
-  constexpr int AHEAD = KS <= 4 ? 2 : 1;         // steps whose loads are in flight
-  constexpr int ND = (32 * EP / 4 + BT - 1) / BT, NX = 32 * NC / 8 / BT;   // 16-byte loads of a thread and step
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+struct Plan {
+  int panels, eblocks, slices;
+  __host__ __device__ int groups() const { return panels * eblocks * slices; }
+};
+
+// One workgroup of NW wavefronts. LOW: registers for two of them on a CU.
+template <int KS, bool DX, bool DWR, int NW, int AHEAD, bool LOW>
+struct Body {
+  static constexpr int BT = 64 * NW, NC = 32 * NW, EP = 32 * KS;
+  static constexpr int DP = 2 * EP < 128 ? 128 : 2 * EP, XP = 2 * NC;  // row pitches of dl and x in bytes
+  static constexpr int PARTS = DWR ? 3 : 2;
+  static constexpr int kD = 32 * DP, kX = DWR ? 32 * XP : 0;
+  static constexpr int kW = DX ? 32 * (NC + 4) * 4 : 0;                // 32 rows of Wr, before the first step
+  static constexpr int OP = 4 * NC + 16, kO = DX ? 32 * OP : 0, NO = 32 * NC / 8 / BT;
+  static constexpr int kBuf = 2 * (PARTS * kD + kX) + kO, kLds = kBuf > kW ? kBuf : kW;
+  static constexpr int WM = KS == 4 ? 2 : 1, TM = KS / WM, TN = WM;    // dWr: 32 x 32 tiles of a wavefront
+  static constexpr int ND = (32 * EP / 4 + BT - 1) / BT, NX = 32 * NC / 8 / BT;   // 16-byte loads of a thread and step
+
+  MOK_DEV static void run(const mok_logits_bwd_args& a, const Plan& plan, int block, uint8_t* lds);
+};
+
+template <int KS, bool DX, bool DWR, int NW, int AHEAD, bool LOW>
+MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a, const Plan& plan, int block,
+                                                    uint8_t* lds) {
+  const int panels = plan.panels, eblocks = plan.eblocks, slices = plan.slices;
   const auto dl_buf = [&](int buf, int part) { return lds + (buf * PARTS + part) * kD; };
   const auto x_buf = [&](int buf) { return lds + 2 * PARTS * kD + buf * kX; };
-  const int b = die_order((int)blockIdx.x, (int)gridDim.x);
+  const int b = die_order(block, plan.groups());
   const int panel = b % panels, eb = b / panels % eblocks, slice = b / (panels * eblocks);
   const Slice sl(a.T, slice, slices);
   const int wave = wave_id(), lane = lane_id(), r = lane & 15, g = lane >> 4;
@@ -221,8 +243,8 @@ __global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(c
   const auto loaded = [&](int i) { return a.E - e0 - 4 * (((int)threadIdx.x + BT * i) % (EP / 4)); };
 
   uint4 dn[AHEAD][ND], xn[AHEAD][DWR ? NX : 1], rn[AHEAD][DX ? NO : 1];
-  const auto load = [&](auto buf, int64_t t) {
-    constexpr int P = decltype(buf)::value % AHEAD;
+  const auto load = [&](int buf, int64_t t) {
+    const int P = buf % AHEAD;
     const int64_t left = min(sl.t1 - t, (int64_t)32);                  // tokens of the step
     const buf_t dl = make_buf(a.dl + t * a.E + e0, (left * a.E - e0) * 4);
 #pragma unroll
@@ -234,19 +256,19 @@ __global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(c
     }
   };
   // the residual of a step, loaded where that of an earlier step has been used
-  const auto load_res = [&](auto buf, int64_t t) {
-    constexpr int P = decltype(buf)::value % AHEAD;
+  const auto load_res = [&](int buf, int64_t t) {
+    const int P = buf % AHEAD;
     if constexpr (DX) {
       const buf_t res = make_buf(a.res ? a.res + t * a.H : nullptr, min(sl.t1 - t, (int64_t)32) * a.H * 2);
 #pragma unroll
       for (int i = 0; i < NO; ++i) rn[P][i] = load16(res, roff[i]);
     }
   };
-  load(std::integral_constant<int, 0>{}, sl.t0);
-  load_res(std::integral_constant<int, 0>{}, sl.t0);
+  load(0, sl.t0);
+  load_res(0, sl.t0);
   if constexpr (AHEAD == 2) {
-    load(std::integral_constant<int, 1>{}, sl.t0 + 32);
-    load_res(std::integral_constant<int, 1>{}, sl.t0 + 32);
+    load(1, sl.t0 + 32);
+    load_res(1, sl.t0 + 32);
   }
 
   // places in dl's buffers: this thread's when it fills them, and this lane's of the two kinds of operand. A step of 32
@@ -261,11 +283,13 @@ __global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(c
   const int trl = tr * DP + (((tc >> 3) ^ swz(tr)) << 4) + 2 * (tc & 7);
   const int trh = (tr + 4) * DP + (((tc >> 3) ^ swz(tr + 4)) << 4) + 2 * (tc & 7);
   const int wm = wave % WM, wn = wave / WM;
-  const int trx = tr * XP + 2 * (32 * wn * TN + tc);
+  const int xc = 4 * wn * TN + (tc >> 3);
+  const auto x_at = [&](int row) { return row * XP + (((xc & 7) ^ swz(row)) << 4) + (xc >> 3) * 128 + 2 * (tc & 7); };
+  const int trx = x_at(tr), trxh = x_at(tr + 4);
 
   // a step's values from its registers into its buffers, and the loads of a later one into the registers
-  const auto stage = [&](auto buf, int64_t t) {
-    constexpr int P = decltype(buf)::value, R = P % AHEAD;
+  const auto stage = [&](int buf, int64_t t) {
+    const int P = buf, R = P % AHEAD;
 #pragma unroll
     for (int i = 0; i < ND; ++i) {
       const int q = (int)threadIdx.x + BT * i;
@@ -284,14 +308,15 @@ __global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(c
 #pragma unroll
       for (int i = 0; i < NX; ++i) {
         const int q = (int)threadIdx.x + BT * i;
-        *reinterpret_cast<uint4*>(x_buf(P) + q / (NC / 8) * XP + 16 * (q % (NC / 8))) = xn[R][i];
+        const int row = q / (NC / 8);
+        *reinterpret_cast<uint4*>(x_buf(P) + row * XP + ((q % (NC / 8) ^ swz(row)) << 4)) = xn[R][i];
       }
     }
     load(buf, t + 32 * AHEAD);
   };
-  stage(std::integral_constant<int, 0>{}, sl.t0);
-  steps(sl, [&](auto buf, int64_t t) {
-    constexpr int P = decltype(buf)::value, R = P % AHEAD;
+  stage(0, sl.t0);
+  steps<AHEAD>(sl, [&](int buf, int64_t t) {
+    const int P = buf, R = P % AHEAD;
     // everyone has written this step's buffers, and is done with the other ones
     barrier_lds_only();
     if constexpr (DWR) {
@@ -305,10 +330,10 @@ __global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(c
         uint4 xf[TN];
 #pragma unroll
         for (int n = 0; n < TN; ++n) {
-          const uint8_t* p = x_buf(P) + trx + 16 * k * XP + 64 * n;
-          xf[n] = pair(p, p + 4 * XP);
+          const uint8_t* p = x_buf(P) + 16 * k * XP;
+          xf[n] = pair(p + (trx ^ (n << 6)), p + (trxh ^ (n << 6)));
         }
-        if (k == 0) stage(std::integral_constant<int, P ^ 1>{}, t + 32);
+        if (k == 0) stage(P ^ 1, t + 32);
 #pragma unroll
         for (int m = 0; m < TM; ++m)
 #pragma unroll
@@ -318,6 +343,7 @@ __global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(c
             const uint4 df = pair(p + at_step(trl, m), p + at_step(trh, m));
 #pragma unroll
             for (int n = 0; n < TN; ++n) acc[m][n] = mfma32(df, xf[n], acc[m][n]);
+            if constexpr (LOW) __builtin_amdgcn_sched_barrier(0);      // (fragments for one part at a time)
           }
       }
     }
@@ -336,7 +362,7 @@ __global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(c
 #pragma unroll
             for (int p = 0; p < 2; ++p)
               d[n][p] = *reinterpret_cast<const uint4*>(dl_buf(P, p) + 16 * n * DP + at_step(get0, s));
-          if (!DWR && s == 0) stage(std::integral_constant<int, P ^ 1>{}, t + 32);
+          if (!DWR && s == 0) stage(P ^ 1, t + 32);
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -383,6 +409,28 @@ __global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(c
   }
 }
 
+template <int KS, bool DX, bool DWR, int NW, int AHEAD>
+__global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(const mok_logits_bwd_args a,
+                                                                               const Plan p) {
+  using B = Body<KS, DX, DWR, NW, AHEAD, false>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[B::kLds];
+  B::run(a, p, (int)blockIdx.x, lds);
+}
+
+// dx and dWr in one launch, p.groups() workgroups each, two a CU. They take turns by
+// eights, so that each die has both, and what eights leave comes last.
+template <int KS>
+__global__ __launch_bounds__(512, 4) void router_grad_pair_kernel(const mok_logits_bwd_args a, const Plan p) {
+  using X = Body<KS, true, false, 8, 1, true>;
+  using W = Body<KS, false, true, 8, 1, true>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[X::kLds > W::kLds ? X::kLds : W::kLds];
+  const int b = (int)blockIdx.x, n = p.groups(), eights = n & ~7, rest = b - 2 * eights;
+  const bool w = rest < 0 ? (b & 8) != 0 : rest < n - eights;
+  const int i = rest < 0 ? (b >> 4) * 8 + (b & 7) : w ? eights + rest : rest + 2 * eights - n;
+  if (w) W::run(a, p, i, lds);
+  else X::run(a, p, i, lds);
+}
+
 __global__ __launch_bounds__(256) void router_dwr_join_kernel(const float* __restrict__ part, int slices, int64_t n4,
                                                              float* __restrict__ dwr) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -400,9 +448,6 @@ __global__ __launch_bounds__(256) void router_dwr_join_kernel(const float* __res
 // experts: 16.3 us with two, 17.2 with one, 18.4 with four: partial sums against
 // workgroups). Two workgroups a CU of four wavefronts took 4 to 8% longer.
 constexpr int kWorkgroups = 256;
-struct Plan {
-  int panels, eblocks, slices;
-};
 Plan plan_of(int64_t T, int H, int columns, int eblocks) {
   Plan p;
   p.panels = (H + columns - 1) / columns;
@@ -414,10 +459,10 @@ Plan plan_of(int64_t T, int H, int columns, int eblocks) {
 // of the launch that forms dWr
 Plan dwr_plan(int64_t T, int H, int E) { return plan_of(T, H, 256, (E + 127) / 128); }
 
-template <int KS, bool DX, bool DWR, int NW>
+template <int KS, bool DX, bool DWR, int NW, int AHEAD>
 hipError_t launch(const mok_logits_bwd_args& a, const Plan& p, hipStream_t st) {
-  hipLaunchKernelGGL((router_grad_kernel<KS, DX, DWR, NW>), dim3((unsigned)(p.panels * p.eblocks * p.slices)),
-                     dim3(64 * NW), 0, st, a, p.panels, p.eblocks, p.slices);
+  hipLaunchKernelGGL((router_grad_kernel<KS, DX, DWR, NW, AHEAD>), dim3((unsigned)p.groups()), dim3(64 * NW), 0, st, a,
+                     p);
   return hipGetLastError();
 }
 
@@ -432,15 +477,23 @@ hipError_t mok_launch_logits_bwd(const mok_logits_bwd_args& a, hipStream_t st) {
   const Plan p = dwr_plan(a.T, a.H, a.E);
   hipError_t e = hipSuccess;
   // no tokens: empty sums, and nothing that reads Wr, which may be NULL then
-  if (a.T == 0) return launch<4, false, true, 8>(a, p, st);
-  if (a.E <= 32) e = launch<1, true, true, 8>(a, p, st);
-  else if (a.E <= 64) e = launch<2, true, true, 8>(a, p, st);
-  else {
-    e = a.E <= 128   ? launch<4, true, false, 8>(a, plan_of(a.T, a.H, 256, 1), st)
-        : a.E <= 256 ? launch<8, true, false, 8>(a, plan_of(a.T, a.H, 256, 1), st)
-                     : launch<16, true, false, 4>(a, plan_of(a.T, a.H, 128, 1), st);
+  if (a.T == 0) return launch<4, false, true, 8, 2>(a, p, st);
+  // With much data, and x read for both at once, the one kernel is at the memory (32 experts, 8192 x 4096 with a residual
+  // 48.4 us, as a pair 49.2; 16384 x 7168 without 104, 107); with less the pair's shorter ways count (4096 x 4096: 25.8,
+  // 24.1; 1037 x 2048: 14.6, 12.3; 1 x 7168: 6.7, 4.8; 64 experts 31.6, 30.1; 17.3, 14.5; 8.3, 5.9).
+  if (a.E <= 64 && a.T * a.H > (int64_t)1 << 24) {
+    e = a.E <= 32 ? launch<1, true, true, 8, 2>(a, p, st) : launch<2, true, true, 8, 2>(a, p, st);
+  } else if (a.E <= 128) {
+    const auto pair = a.E <= 32   ? router_grad_pair_kernel<1>
+                      : a.E <= 64 ? router_grad_pair_kernel<2>
+                                  : router_grad_pair_kernel<4>;
+    hipLaunchKernelGGL(pair, dim3((unsigned)(2 * p.groups())), dim3(512), 0, st, a, p);
+    e = hipGetLastError();
+  } else {
+    e = a.E <= 256 ? launch<8, true, false, 8, 1>(a, plan_of(a.T, a.H, 256, 1), st)
+                   : launch<16, true, false, 4, 1>(a, plan_of(a.T, a.H, 128, 1), st);
     if (e != hipSuccess) return e;
-    e = launch<4, false, true, 8>(a, p, st);
+    e = launch<4, false, true, 8, 2>(a, p, st);
   }
   if (e != hipSuccess || p.slices <= 1) return e;
   const int64_t n4 = (int64_t)a.E * a.H / 4;

@@ -320,6 +320,18 @@ def test_grad_tokens(T, H, E):
     check_grad(T, H, E, residual=T % 2 == 1)
 
 
+@pytest.mark.parametrize("E", [7, 32, 33, 64])
+def test_grad_of_much_data(E):
+    """More than 2^24 values of x: both results come from one kernel."""
+    check_grad(4105, 4224, E, residual=E % 2 == 0, inplace=E == 64)
+
+
+@pytest.mark.parametrize("T,H,E", [(700, 7168, 100), (300, 1024, 70), (580, 896, 40), (97, 1152, 9)])
+def test_grad_of_odd_launches(T, H, E):
+    """Numbers of workgroups that are no multiple of 8 (252, 20, 36, 10)."""
+    check_grad(T, H, E)
+
+
 def test_grad_of_the_wide_layer():
     check_grad(3000, 7168, 32)
 
