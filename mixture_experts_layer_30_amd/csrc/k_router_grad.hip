@@ -10,6 +10,7 @@
 // 708 MB, 5.0 TB/s; a copy reaches 4.9), nearly so with 128 (16384 x 4096: 127 us for
 // 415 MB and 34 MB of partial sums that are written and read; from a graph 132, without
 // the matrix instructions 109).
+#include <algorithm>
 #include <type_traits>
 
 #include "gemm_core.h"
@@ -444,20 +445,30 @@ __global__ __launch_bounds__(256) void router_dwr_join_kernel(const float* __res
   reinterpret_cast<float4*>(dwr)[i] = s;
 }
 
-// A workgroup a CU, and two steps of tokens at least (1037 tokens x 2048, 60
-// experts: 16.3 us with two, 17.2 with one, 18.4 with four: partial sums against
-// workgroups). Two workgroups a CU of four wavefronts took 4 to 8% longer.
+// A slice a CU, and a few steps of tokens at least, the last slice fewer: partial sums
+// against workgroups. Two kinds of workgroups (pair): three steps (1037 tokens x 2048, 60
+// experts: 12.6 us with three, 13.7 with two or one, 12.8 with four; 300 x 1024: 10.2, 9.6
+// with two), and a CU each, so half the slices, while that is at most six (1000 x 4096,
+// 128 experts: 21.9 us, 24.6 with all; 3000 x 2048: 25.4, 27.4); with eight it is no longer
+// faster everywhere (2048 x 4096: 29.3, 30.3 with 128 experts, 17.4, 16.6 with 16). Else
+// two (200 experts, 1000 x 4096: 35.5 us, 37.2 with three; 300 x 1024: 25.2, 27.7).
 constexpr int kWorkgroups = 256;
-Plan plan_of(int64_t T, int H, int columns, int eblocks) {
+Plan plan_of(int64_t T, int H, int columns, int eblocks, bool pair) {
   Plan p;
   p.panels = (H + columns - 1) / columns;
   p.eblocks = eblocks;
-  const int64_t steps = (T + 31) / 32, most = steps < 2 ? 1 : steps / 2, s = kWorkgroups / ((int64_t)p.panels * eblocks);
-  p.slices = (int)(s < 1 ? 1 : s < most ? s : most);
+  const int64_t steps = (T + 31) / 32, tiles = (int64_t)p.panels * eblocks;
+  const auto steps_of = [&](int64_t workgroups) {
+    const int64_t s = std::max<int64_t>(1, workgroups / tiles);
+    return (steps + s - 1) / s;
+  };
+  const int64_t half = steps_of(kWorkgroups / 2);
+  const int64_t per = std::max<int64_t>(pair ? 3 : 2, pair && half <= 6 ? half : steps_of(kWorkgroups));
+  p.slices = (int)std::max<int64_t>(1, (steps + per - 1) / per);
   return p;
 }
 // of the launch that forms dWr
-Plan dwr_plan(int64_t T, int H, int E) { return plan_of(T, H, 256, (E + 127) / 128); }
+Plan dwr_plan(int64_t T, int H, int E) { return plan_of(T, H, 256, (E + 127) / 128, E <= 128); }
 
 template <int KS, bool DX, bool DWR, int NW, int AHEAD>
 hipError_t launch(const mok_logits_bwd_args& a, const Plan& p, hipStream_t st) {
@@ -490,8 +501,8 @@ hipError_t mok_launch_logits_bwd(const mok_logits_bwd_args& a, hipStream_t st) {
     hipLaunchKernelGGL(pair, dim3((unsigned)(2 * p.groups())), dim3(512), 0, st, a, p);
     e = hipGetLastError();
   } else {
-    e = a.E <= 256 ? launch<8, true, false, 8, 1>(a, plan_of(a.T, a.H, 256, 1), st)
-                   : launch<16, true, false, 4, 1>(a, plan_of(a.T, a.H, 128, 1), st);
+    e = a.E <= 256 ? launch<8, true, false, 8, 1>(a, plan_of(a.T, a.H, 256, 1, false), st)
+                   : launch<16, true, false, 4, 1>(a, plan_of(a.T, a.H, 128, 1, false), st);
     if (e != hipSuccess) return e;
     e = launch<4, false, true, 8, 2>(a, p, st);
   }
