@@ -7,7 +7,7 @@
 // whole, is left out.
 //
 // Bound by memory with few experts (16384 x 7168, 32 experts, residual: 141 us for
-// 708 MB, 5.0 TB/s; a copy reaches 4.9), nearly so with 128 (16384 x 4096: 127 us for
+// 708 MB, 5.0 TB/s; a copy reaches 4.9), nearly so with 128 (16384 x 4096: 121 us for
 // 415 MB and 34 MB of partial sums that are written and read; from a graph 132, without
 // the matrix instructions 109).
 #include <algorithm>
