@@ -1,15 +1,15 @@
 // Router backward from the gradient of every logit: dx = dl . Wr (+ residual)
-// and dWr = dl^T . x, on the matrix cores. dl and Wr are fp32, the operands bf16:
-// for dWr, which is fp32, dl is split exactly into three bf16 parts (x is bf16, so
-// every product is exact); for dx, which is rounded to bf16, dl and Wr go in as two
-// parts each, the nearest bf16 and the nearest to what that leaves (at most 2^-16 of
-// a value is lost), and the product of the two small parts, at most 2^-16 of the
-// whole, is left out.
+// and dWr = dl^T . x, on the matrix cores. dl and Wr are fp32, the operands bf16: dl
+// and Wr are split exactly into three bf16 parts each. For dWr, x is bf16, so every
+// product is exact. For dx, of the nine products of parts the six down to 2^-16 of the
+// whole go in, all exact; the other three are less than 2^-21 of it, in the mean square
+// less than half of what fp32 sums lose. Two parts each do not do, although dx is
+// rounded to bf16 in the end: a row of dl adds up to nearly zero over the experts, and
+// they moved 0.3% of the roundings at 1037 x 2048 with 60 experts, an fp32 product 0.01%.
 //
 // Bound by memory with few experts (16384 x 7168, 32 experts, residual: 141 us for
-// 708 MB, 5.0 TB/s; a copy reaches 4.9), nearly so with 128 (16384 x 4096: 121 us for
-// 415 MB and 34 MB of partial sums that are written and read; from a graph 132, without
-// the matrix instructions 109).
+// 708 MB, 5.0 TB/s; a copy reaches 4.9), by the matrix instructions with many (16384 x
+// 4096 with 128: 155 GFLOP in 158 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -27,12 +27,7 @@ typedef __attribute__((address_space(3))) i16x4_t* lds_i16x4_ptr;
 MOK_DEV float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 MOK_DEV float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// the nearest bf16 of a pair, and the nearest to what it leaves
-MOK_DEV void split2(float a, float b, uint32_t& hi, uint32_t& mid) {
-  hi = pack_bf16x2(a, b);
-  mid = pack_bf16x2(a - bf_lo(hi), b - bf_hi(hi));
-}
-// and a third part: hi + mid + lo is exact (8 + 8 + 8 bits)
+// the nearest bf16 of a pair, the nearest to what it leaves, and a third part: hi + mid + lo is exact (8 + 8 + 8 bits)
 MOK_DEV void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   hi = pack_bf16x2(a, b);
   const float ra = a - bf_lo(hi), rb = b - bf_hi(hi);
@@ -82,51 +77,52 @@ struct Slice {
   }
 };
 
-// f(step's buffer, first token) for every 32 tokens. With the loads of two steps in
+// f(step's buffer, first token) for every ST tokens. With the loads of two steps in
 // flight (AHEAD) the buffer is a constant, as the registers that hold a step are; with
 // one it is not, and the accumulators have one place (in two copies of the step, which
 // the loop leaves after either, they take twice their registers).
-template <int AHEAD, class F>
+template <int AHEAD, int ST, class F>
 MOK_DEV void steps(const Slice& s, F&& f) {
   if constexpr (AHEAD == 1) {
     int p = 0;
 #pragma unroll 1
-    for (int64_t t = s.t0; t < s.t1; t += 32, p ^= 1) f(p, t);
+    for (int64_t t = s.t0; t < s.t1; t += ST, p ^= 1) f(p, t);
   } else {
-    for (int64_t t = s.t0; t < s.t1; t += 64) {
+    for (int64_t t = s.t0; t < s.t1; t += 2 * ST) {
       f(0, t);
-      if (t + 32 >= s.t1) break;
-      f(1, t + 32);
+      if (t + ST >= s.t1) break;
+      f(1, t + ST);
     }
   }
 }
 
 // ---------------------------------------------------------------- kernel
-// A workgroup takes 32 NW columns and a slice of the tokens, 32 tokens at a time
-// through two sets of LDS buffers: while one is multiplied, the other is filled
-// from registers that were loaded two steps ahead (one where registers are few). Its
-// barriers wait for LDS alone (__syncthreads would wait for every load and store in
-// flight). Up to 64 experts and with much data a workgroup forms both results (DX and
-// DWR), so that dl is read and split once (16384 x 4096 with 64 experts: 92 us, as a
-// pair 95). Else up to 128 experts workgroups of either kind share the CUs, two on each,
-// one's instructions beside the other's copies (16384 x 4096 with 128 experts: 132 us on
-// the card, in two launches 140, one workgroup for both, with spilled registers, 160;
-// 1000 x 4096: 25, 30). Beyond, Wr leaves no registers for a second workgroup: two
-// launches, and DWR takes 128 experts a workgroup.
+// A workgroup of eight wavefronts takes 128 MT columns and a slice of the tokens, ST
+// tokens at a time through two sets of LDS buffers: while one is multiplied, the other
+// is filled from registers that were loaded two steps ahead (one where registers are
+// few). Its barriers wait for LDS alone (__syncthreads would wait for every load and
+// store in flight). With much data a workgroup forms both results (DX and DWR) up to 64
+// experts, so that dl is read and split once (16384 x 4096 with 64 experts: 104 us, as a
+// pair 113), and beyond, where Wr leaves no registers for that, there is a launch for
+// each. With little data, up to 128 experts, workgroups of either kind share the CUs,
+// two on each, one's instructions beside the other's copies. DWR takes 128 experts a
+// workgroup at most.
 //
-// dl of a step lies in LDS as bf16 parts [32 tokens][EP experts]; 16-byte chunk c
+// dl of a step lies in LDS as bf16 parts [ST tokens][EP experts]; 16-byte chunk c
 // of token row t at c ^ swz(t): eight rows at one chunk (dx), and four rows at two
 // neighbouring chunks (dWr, transposed), fall on the eight places of 128 bytes.
 //
 // dx: the columns of dx are rows of the first operand, tokens columns of the
-// second. A wavefront keeps its 32 columns of Wr, both parts, in registers (16 KS
+// second. A wavefront keeps its 16 MT columns of Wr, all parts, in registers (12 MT KS
 // of them, KS = EP / 32) and the tokens stream past. v_mfma_f32_16x16x32_bf16: lane
 // l supplies row l % 16 of an operand, 8 values of K from 8 (l / 16) on, and holds
 // of result column l % 16 the rows 4 (l / 16) + i. Row r of the wavefront's tile m
-// (0, 1) is column 8 (r / 4) + 4 m + r % 4, so a lane ends up with 8 neighbouring
+// is column 4 MT (r / 4) + 4 m + r % 4, so a lane ends up with 4 MT neighbouring
 // columns of a token. dx goes through LDS once more, in fp32, so that rows of it and
-// of the residual are written and read in 512 bytes (16384 x 7168 with 32 experts: in
-// the operand's 64-byte pieces 155 us, so 138).
+// of the residual are written and read in 256 MT bytes (with 32 experts and two parts
+// 16384 x 7168 took 155 us in the operand's 64-byte pieces, so 138). One tile a wavefront
+// halves Wr's registers and doubles the reading of dl from LDS: beyond 256 experts
+// (16384 x 4096 with 512: 580 us in eight wavefronts of one tile, 755 in four of two).
 //
 // dWr: x as it is and dl in its three parts are both read transposed
 // (ds_read_b64_tr_b16: lane 4 q + p of 16 names row q and columns 4 p .. + 3, and
@@ -141,25 +137,27 @@ struct Plan {
   __host__ __device__ int groups() const { return panels * eblocks * slices; }
 };
 
-// One workgroup of NW wavefronts. LOW: registers for two of them on a CU.
-template <int KS, bool DX, bool DWR, int NW, int AHEAD, bool LOW>
+// LOW: registers for two workgroups on a CU
+constexpr int NW = 8;
+template <int KS, bool DX, bool DWR, int AHEAD, bool LOW, int MT = 2, int ST = 32>
 struct Body {
-  static constexpr int BT = 64 * NW, NC = 32 * NW, EP = 32 * KS;
+  static_assert((!DWR || (MT == 2 && ST == 32)) && ST % 16 == 0, "dWr's tiles");
+  static constexpr int BT = 64 * NW, NC = 16 * MT * NW, EP = 32 * KS, NT = ST / 16;
   static constexpr int DP = 2 * EP < 128 ? 128 : 2 * EP, XP = 2 * NC;  // row pitches of dl and x in bytes
-  static constexpr int PARTS = DWR ? 3 : 2;
-  static constexpr int kD = 32 * DP, kX = DWR ? 32 * XP : 0;
+  static constexpr int PARTS = 3;
+  static constexpr int kD = ST * DP, kX = DWR ? ST * XP : 0;
   static constexpr int kW = DX ? 32 * (NC + 4) * 4 : 0;                // 32 rows of Wr, before the first step
-  static constexpr int OP = 4 * NC + 16, kO = DX ? 32 * OP : 0, NO = 32 * NC / 8 / BT;
+  static constexpr int OP = 4 * NC + 16, kO = DX ? ST * OP : 0, NO = (ST * NC / 8 + BT - 1) / BT;
   static constexpr int kBuf = 2 * (PARTS * kD + kX) + kO, kLds = kBuf > kW ? kBuf : kW;
   static constexpr int WM = KS == 4 ? 2 : 1, TM = KS / WM, TN = WM;    // dWr: 32 x 32 tiles of a wavefront
-  static constexpr int ND = (32 * EP / 4 + BT - 1) / BT, NX = 32 * NC / 8 / BT;   // 16-byte loads of a thread and step
+  static constexpr int ND = (ST * EP / 4 + BT - 1) / BT, NX = ST * NC / 8 / BT;   // 16-byte loads of a thread and step
 
   MOK_DEV static void run(const mok_logits_bwd_args& a, const Plan& plan, int block, uint8_t* lds);
 };
 
-template <int KS, bool DX, bool DWR, int NW, int AHEAD, bool LOW>
-MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a, const Plan& plan, int block,
-                                                    uint8_t* lds) {
+template <int KS, bool DX, bool DWR, int AHEAD, bool LOW, int MT, int ST>
+MOK_DEV void Body<KS, DX, DWR, AHEAD, LOW, MT, ST>::run(const mok_logits_bwd_args& a, const Plan& plan, int block,
+                                                        uint8_t* lds) {
   const int panels = plan.panels, eblocks = plan.eblocks, slices = plan.slices;
   const auto dl_buf = [&](int buf, int part) { return lds + (buf * PARTS + part) * kD; };
   const auto x_buf = [&](int buf) { return lds + 2 * PARTS * kD + buf * kX; };
@@ -171,7 +169,7 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
   const int nks = (a.E - e0 + 31) / 32;          // steps of 32 experts that hold any
 
   // ---- Wr: 32 rows at a time through LDS into the operand's registers
-  uint4 whi[2][DX ? KS : 1], wmid[2][DX ? KS : 1];
+  uint4 w[3][MT][DX ? KS : 1];
   if constexpr (DX) {
     constexpr int NWL = 32 * NC / 4 / BT;
     float* wl = reinterpret_cast<float*>(lds);
@@ -195,14 +193,15 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
       if (s + 1 < KS) load_w(s + 1);
       barrier_lds_only();
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
+      for (int m = 0; m < MT; ++m) {
         float v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = wl[(8 * g + u) * (NC + 4) + 32 * wave + 8 * (r >> 2) + 4 * m + (r & 3)];
-        split2(v[0], v[1], whi[m][s].x, wmid[m][s].x);
-        split2(v[2], v[3], whi[m][s].y, wmid[m][s].y);
-        split2(v[4], v[5], whi[m][s].z, wmid[m][s].z);
-        split2(v[6], v[7], whi[m][s].w, wmid[m][s].w);
+        for (int u = 0; u < 8; ++u)
+          v[u] = wl[(8 * g + u) * (NC + 4) + 16 * MT * wave + 4 * MT * (r >> 2) + 4 * m + (r & 3)];
+        split3(v[0], v[1], w[0][m][s].x, w[1][m][s].x, w[2][m][s].x);
+        split3(v[2], v[3], w[0][m][s].y, w[1][m][s].y, w[2][m][s].y);
+        split3(v[4], v[5], w[0][m][s].z, w[1][m][s].z, w[2][m][s].z);
+        split3(v[6], v[7], w[0][m][s].w, w[1][m][s].w, w[2][m][s].w);
       }
       barrier_lds_only();
     }
@@ -224,7 +223,7 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
 #pragma unroll
   for (int i = 0; i < ND; ++i) {
     const int q = (int)threadIdx.x + BT * i, row = q / (EP / 4), e = 4 * (q % (EP / 4));
-    doff[i] = row < 32 && e0 + e < a.E ? 4u * (row * a.E + e) : kOut;
+    doff[i] = row < ST && e0 + e < a.E ? 4u * (row * a.E + e) : kOut;
   }
   if constexpr (DWR) {
     // (columns past H read the next row, for sums that are not stored)
@@ -237,7 +236,7 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
 #pragma unroll
   for (int i = 0; i < NO; ++i) {
     const int q = (int)threadIdx.x + BT * i, c = c0 + 8 * (q % (NC / 8));
-    roff[i] = c < a.H ? 2u * (q / (NC / 8) * a.H + c) : kOut;
+    roff[i] = c < a.H && q / (NC / 8) < ST ? 2u * (q / (NC / 8) * a.H + c) : kOut;
   }
   // of four experts from 4 j on, how many there are (E is not always a multiple of 4: the others' place holds the next
   // token's, and must not enter a product)
@@ -246,7 +245,7 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
   uint4 dn[AHEAD][ND], xn[AHEAD][DWR ? NX : 1], rn[AHEAD][DX ? NO : 1];
   const auto load = [&](int buf, int64_t t) {
     const int P = buf % AHEAD;
-    const int64_t left = min(sl.t1 - t, (int64_t)32);                  // tokens of the step
+    const int64_t left = min(sl.t1 - t, (int64_t)ST);                  // tokens of the step
     const buf_t dl = make_buf(a.dl + t * a.E + e0, (left * a.E - e0) * 4);
 #pragma unroll
     for (int i = 0; i < ND; ++i) dn[P][i] = load16(dl, doff[i]);
@@ -260,7 +259,7 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
   const auto load_res = [&](int buf, int64_t t) {
     const int P = buf % AHEAD;
     if constexpr (DX) {
-      const buf_t res = make_buf(a.res ? a.res + t * a.H : nullptr, min(sl.t1 - t, (int64_t)32) * a.H * 2);
+      const buf_t res = make_buf(a.res ? a.res + t * a.H : nullptr, min(sl.t1 - t, (int64_t)ST) * a.H * 2);
 #pragma unroll
       for (int i = 0; i < NO; ++i) rn[P][i] = load16(res, roff[i]);
     }
@@ -268,8 +267,8 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
   load(0, sl.t0);
   load_res(0, sl.t0);
   if constexpr (AHEAD == 2) {
-    load(1, sl.t0 + 32);
-    load_res(1, sl.t0 + 32);
+    load(1, sl.t0 + ST);
+    load_res(1, sl.t0 + ST);
   }
 
   // places in dl's buffers: this thread's when it fills them, and this lane's of the two kinds of operand. A step of 32
@@ -294,12 +293,13 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
 #pragma unroll
     for (int i = 0; i < ND; ++i) {
       const int q = (int)threadIdx.x + BT * i;
-      if (32 * EP / 4 < BT && wave >= 32 * EP / 4 / 64) break;         // (fewer places than threads)
+      if (ST * EP / 4 < BT && wave >= ST * EP / 4 / 64) break;         // (fewer places than threads)
       const int at = RI % 8 == 0 ? put0 + i * RI * DP : put_at(q / (EP / 4), q % (EP / 4));
       uint2 p[3];
       const int n = loaded(i);
-      const float4 v = make_float4(__uint_as_float(dn[R][i].x), n > 1 ? __uint_as_float(dn[R][i].y) : 0.f,
-                                   n > 2 ? __uint_as_float(dn[R][i].z) : 0.f, n > 3 ? __uint_as_float(dn[R][i].w) : 0.f);
+      const auto within = [n](int u, uint32_t word) { return n > u ? __uint_as_float(word) : 0.f; };
+      const float4 v = make_float4(__uint_as_float(dn[R][i].x), within(1, dn[R][i].y), within(2, dn[R][i].z),
+                                   within(3, dn[R][i].w));
       split3(v.x, v.y, p[0].x, p[1].x, p[2].x);
       split3(v.z, v.w, p[0].y, p[1].y, p[2].y);
 #pragma unroll
@@ -313,10 +313,10 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
         *reinterpret_cast<uint4*>(x_buf(P) + row * XP + ((q % (NC / 8) ^ swz(row)) << 4)) = xn[R][i];
       }
     }
-    load(buf, t + 32 * AHEAD);
+    load(buf, t + ST * AHEAD);
   };
   stage(0, sl.t0);
-  steps<AHEAD>(sl, [&](int buf, int64_t t) {
+  steps<AHEAD, ST>(sl, [&](int buf, int64_t t) {
     const int P = buf, R = P % AHEAD;
     // everyone has written this step's buffers, and is done with the other ones
     barrier_lds_only();
@@ -334,7 +334,7 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
           const uint8_t* p = x_buf(P) + 16 * k * XP;
           xf[n] = pair(p + (trx ^ (n << 6)), p + (trxh ^ (n << 6)));
         }
-        if (k == 0) stage(P ^ 1, t + 32);
+        if (k == 0) stage(P ^ 1, t + ST);
 #pragma unroll
         for (int m = 0; m < TM; ++m)
 #pragma unroll
@@ -349,49 +349,52 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
       }
     }
     if constexpr (DX) {
-      f32x4_t o[2][2];
+      f32x4_t o[MT][NT];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) o[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < NT; ++n) o[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         if (s < nks) {
-          uint4 d[2][2];
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < NT; ++n) {
+            uint4 d[3];
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-              d[n][p] = *reinterpret_cast<const uint4*>(dl_buf(P, p) + 16 * n * DP + at_step(get0, s));
-          if (!DWR && s == 0) stage(P ^ 1, t + 32);
+            for (int p = 0; p < 3; ++p)
+              d[p] = *reinterpret_cast<const uint4*>(dl_buf(P, p) + 16 * n * DP + at_step(get0, s));
+            if (!DWR && s == 0 && n == NT - 1) stage(P ^ 1, t + ST);
+            // part i of one with part j of the other, the small products first
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+            for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              o[m][n] = mfma16(wmid[m][s], d[n][0], o[m][n]);
-              o[m][n] = mfma16(whi[m][s], d[n][1], o[m][n]);
-              o[m][n] = mfma16(whi[m][s], d[n][0], o[m][n]);
-            }
+              for (int i = sum; i >= 0; --i)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) o[m][n] = mfma16(w[i][m][s], d[sum - i], o[m][n]);
+          }
         }
       }
-      // through LDS, so that rows are read and written 512 bytes at a time
+      // through LDS, so that rows are read and written 256 MT bytes at a time
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-          *reinterpret_cast<f32x4_t*>(o_buf + (16 * n + r) * OP + 4 * (32 * wave + 8 * g + 4 * m)) = o[m][n];
+        for (int n = 0; n < NT; ++n)
+          *reinterpret_cast<f32x4_t*>(o_buf + (16 * n + r) * OP + 4 * (16 * MT * wave + 4 * MT * g + 4 * m)) = o[m][n];
       barrier_lds_only();
-      const buf_t dx = make_buf(a.dx + t * a.H, min(sl.t1 - t, (int64_t)32) * a.H * 2);
+      const buf_t dx = make_buf(a.dx + t * a.H, min(sl.t1 - t, (int64_t)ST) * a.H * 2);
 #pragma unroll
       for (int i = 0; i < NO; ++i) {
         const int q = (int)threadIdx.x + BT * i;
-        const float4* p = reinterpret_cast<const float4*>(o_buf + q / (NC / 8) * OP + 32 * (q % (NC / 8)));
+        const float4* p = reinterpret_cast<const float4*>(o_buf + min(q / (NC / 8), ST - 1) * OP + 32 * (q % (NC / 8)));
         const float4 x = p[0], y = p[1];
-        const uint4 w = rn[R][i];
-        store16(dx, roff[i], make_uint4(pack_bf16x2(x.x + bf_lo(w.x), x.y + bf_hi(w.x)), pack_bf16x2(x.z + bf_lo(w.y), x.w + bf_hi(w.y)),
-                                        pack_bf16x2(y.x + bf_lo(w.z), y.y + bf_hi(w.z)), pack_bf16x2(y.z + bf_lo(w.w), y.w + bf_hi(w.w))));
+        const uint4 v = rn[R][i];
+        const uint4 sum = make_uint4(pack_bf16x2(x.x + bf_lo(v.x), x.y + bf_hi(v.x)),
+                                     pack_bf16x2(x.z + bf_lo(v.y), x.w + bf_hi(v.y)),
+                                     pack_bf16x2(y.x + bf_lo(v.z), y.y + bf_hi(v.z)),
+                                     pack_bf16x2(y.z + bf_lo(v.w), y.w + bf_hi(v.w)));
+        store16(dx, roff[i], sum);
       }
-      load_res(buf, t + 32 * AHEAD);
+      load_res(buf, t + ST * AHEAD);
     }
   });
 
@@ -410,26 +413,31 @@ MOK_DEV void Body<KS, DX, DWR, NW, AHEAD, LOW>::run(const mok_logits_bwd_args& a
   }
 }
 
-template <int KS, bool DX, bool DWR, int NW, int AHEAD>
-__global__ __launch_bounds__(64 * NW, KS < 16 ? 2 : 1) void router_grad_kernel(const mok_logits_bwd_args a,
-                                                                               const Plan p) {
-  using B = Body<KS, DX, DWR, NW, AHEAD, false>;
+template <int KS, bool DX, bool DWR, int AHEAD, int MT, int ST>
+__global__ __launch_bounds__(64 * NW, 2) void router_grad_kernel(const mok_logits_bwd_args a, const Plan p) {
+  using B = Body<KS, DX, DWR, AHEAD, false, MT, ST>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[B::kLds];
   B::run(a, p, (int)blockIdx.x, lds);
 }
 
-// dx and dWr in one launch, p.groups() workgroups each, two a CU. They take turns by
-// eights, so that each die has both, and what eights leave comes last.
+// dx and dWr in one launch, two workgroups a CU: pw.groups() that form dWr, and R for each of them that form dx (or
+// fewer, where H leaves the last one no columns). They take turns by eights, so that each die has both, and what
+// eights leave comes last.
 template <int KS>
-__global__ __launch_bounds__(512, 4) void router_grad_pair_kernel(const mok_logits_bwd_args a, const Plan p) {
-  using X = Body<KS, true, false, 8, 1, true>;
-  using W = Body<KS, false, true, 8, 1, true>;
+constexpr int kPairMT = KS < 4 ? 2 : 1;
+template <int KS>
+__global__ __launch_bounds__(64 * NW, 4) void router_grad_pair_kernel(const mok_logits_bwd_args a, const Plan px,
+                                                                  const Plan pw) {
+  using X = Body<KS, true, false, 1, true, kPairMT<KS>>;
+  using W = Body<KS, false, true, 1, true>;
+  constexpr int R = W::NC / X::NC;
   __shared__ __attribute__((aligned(16))) uint8_t lds[X::kLds > W::kLds ? X::kLds : W::kLds];
-  const int b = (int)blockIdx.x, n = p.groups(), eights = n & ~7, rest = b - 2 * eights;
-  const bool w = rest < 0 ? (b & 8) != 0 : rest < n - eights;
-  const int i = rest < 0 ? (b >> 4) * 8 + (b & 7) : w ? eights + rest : rest + 2 * eights - n;
-  if (w) W::run(a, p, i, lds);
-  else X::run(a, p, i, lds);
+  const int b = (int)blockIdx.x, nx = px.groups(), nw = pw.groups();
+  const int rounds = min(nx / (8 * R), nw / 8), rest = b - rounds * 8 * (R + 1), left = nw - 8 * rounds;
+  const int turn = b / 8 % (R + 1);
+  const bool w = rest < 0 ? turn == 1 : rest < left;
+  if (w) W::run(a, pw, rest < 0 ? b / (8 * (R + 1)) * 8 + (b & 7) : 8 * rounds + rest, lds);
+  else X::run(a, px, rest < 0 ? (b / (8 * (R + 1)) * R + turn / 2) * 8 + (b & 7) : 8 * R * rounds + rest - left, lds);
 }
 
 __global__ __launch_bounds__(256) void router_dwr_join_kernel(const float* __restrict__ part, int slices, int64_t n4,
@@ -470,10 +478,20 @@ Plan plan_of(int64_t T, int H, int columns, int eblocks, bool pair) {
 // of the launch that forms dWr
 Plan dwr_plan(int64_t T, int H, int E) { return plan_of(T, H, 256, (E + 127) / 128, E <= 128); }
 
-template <int KS, bool DX, bool DWR, int NW, int AHEAD>
+template <int KS, bool DX, bool DWR, int AHEAD, int MT = 2, int ST = 32>
 hipError_t launch(const mok_logits_bwd_args& a, const Plan& p, hipStream_t st) {
-  hipLaunchKernelGGL((router_grad_kernel<KS, DX, DWR, NW, AHEAD>), dim3((unsigned)p.groups()), dim3(64 * NW), 0, st, a,
-                     p);
+  hipLaunchKernelGGL((router_grad_kernel<KS, DX, DWR, AHEAD, MT, ST>), dim3((unsigned)p.groups()), dim3(64 * NW), 0, st,
+                     a, p);
+  return hipGetLastError();
+}
+
+template <int KS>
+hipError_t launch_pair(const mok_logits_bwd_args& a, const Plan& pw, hipStream_t st) {
+  constexpr int NC = 128 * kPairMT<KS>;
+  Plan px = pw;
+  px.panels = (a.H + NC - 1) / NC;
+  hipLaunchKernelGGL(router_grad_pair_kernel<KS>, dim3((unsigned)(px.groups() + pw.groups())), dim3(64 * NW), 0, st, a,
+                     px, pw);
   return hipGetLastError();
 }
 
@@ -488,23 +506,22 @@ hipError_t mok_launch_logits_bwd(const mok_logits_bwd_args& a, hipStream_t st) {
   const Plan p = dwr_plan(a.T, a.H, a.E);
   hipError_t e = hipSuccess;
   // no tokens: empty sums, and nothing that reads Wr, which may be NULL then
-  if (a.T == 0) return launch<4, false, true, 8, 2>(a, p, st);
-  // With much data, and x read for both at once, the one kernel is at the memory (32 experts, 8192 x 4096 with a residual
-  // 48.4 us, as a pair 49.2; 16384 x 7168 without 104, 107); with less the pair's shorter ways count (4096 x 4096: 25.8,
-  // 24.1; 1037 x 2048: 14.6, 12.3; 1 x 7168: 6.7, 4.8; 64 experts 31.6, 30.1; 17.3, 14.5; 8.3, 5.9).
-  if (a.E <= 64 && a.T * a.H > (int64_t)1 << 24) {
-    e = a.E <= 32 ? launch<1, true, true, 8, 2>(a, p, st) : launch<2, true, true, 8, 2>(a, p, st);
-  } else if (a.E <= 128) {
-    const auto pair = a.E <= 32   ? router_grad_pair_kernel<1>
-                      : a.E <= 64 ? router_grad_pair_kernel<2>
-                                  : router_grad_pair_kernel<4>;
-    hipLaunchKernelGGL(pair, dim3((unsigned)(2 * p.groups())), dim3(512), 0, st, a, p);
-    e = hipGetLastError();
+  if (a.T == 0) return launch<4, false, true, 2>(a, p, st);
+  // With much data, and x read for both at once, the one kernel is nearer the memory (64 experts, 8192 x 4096 with a
+  // residual 60.5 us, as a pair 64.9; 32 experts 49.3, 51.5); with less the pair's shorter ways count (4096 x 4096:
+  // 34.9, 34.0; 26.6, 25.5; 1037 x 2048: 17.0, 14.3; 13.5, 11.3). From 65 to 128 experts, with two launches in place of the
+  // one: 8192 x 4096 93 us, as a pair 102; 4096 x 4096 59, 62; 2048 x 4096 40.1, 40.7; 1000 x 4096 29.8, 25.1.
+  const bool much = a.T * a.H > (int64_t)1 << 24;
+  if (a.E <= 64 && much) {
+    e = a.E <= 32 ? launch<1, true, true, 2>(a, p, st) : launch<2, true, true, 2>(a, p, st);
+  } else if (a.E <= 128 && !much) {
+    e = a.E <= 32 ? launch_pair<1>(a, p, st) : a.E <= 64 ? launch_pair<2>(a, p, st) : launch_pair<4>(a, p, st);
   } else {
-    e = a.E <= 256 ? launch<8, true, false, 8, 1>(a, plan_of(a.T, a.H, 256, 1, false), st)
-                   : launch<16, true, false, 4, 1>(a, plan_of(a.T, a.H, 128, 1, false), st);
+    e = a.E <= 128   ? launch<4, true, false, 2>(a, plan_of(a.T, a.H, 256, 1, false), st)
+        : a.E <= 256 ? launch<8, true, false, 1, 2, 16>(a, plan_of(a.T, a.H, 256, 1, false), st)
+                     : launch<16, true, false, 1, 1, 16>(a, plan_of(a.T, a.H, 128, 1, false), st);
     if (e != hipSuccess) return e;
-    e = launch<4, false, true, 8, 2>(a, p, st);
+    e = launch<4, false, true, 2>(a, p, st);
   }
   if (e != hipSuccess || p.slices <= 1) return e;
   const int64_t n4 = (int64_t)a.E * a.H / 4;
