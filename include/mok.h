@@ -565,9 +565,10 @@ mok_status mok_router_losses_backward(const mok_problem* problem, const float* l
  *   d_w_router[e] = sum_t d_logits[t][e] x[t]                     [E][H] fp32
  * residual [T][H] bf16 (NULL: none) is the layer's own dx, added before the one
  * rounding; it may be dx itself. fp32 sums in a fixed order on the matrix
- * cores, d_logits and w_router in three bf16 parts each: for d_w_router the
- * products are exact, for dx to 2^-21 of a product before the one rounding; a value
- * of d_logits or w_router that is not finite makes NaN of what it enters. x, dx,
+ * cores, d_logits and w_router in three bf16 parts each (all bits of a value down to
+ * 2^-110, below it those from 2^-133 on): for d_w_router the products are exact, for
+ * dx to 2^-21 of a product before the one rounding; a value of d_logits or w_router
+ * that is not finite makes NaN of what it enters. x, dx,
  * residual, w_router, d_logits and d_w_router are 16-byte aligned. T = 0 gives zeros in
  * d_w_router. Outputs and workspace share no memory with another operand but
  * dx with residual (MOK_ERR_INVALID_ARG). */

@@ -33,20 +33,6 @@ MOK_DEV float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 // (score, expert) a beats b: higher score, or equal score and lower id
 MOK_DEV bool beats(float sa, int ea, float sb, int eb) { return sa > sb || (sa == sb && ea < eb); }
 
-// Exact three-way split of fp32 values into bf16: w = hi + mid + lo, each
-// part the truncation of what remains (8 significant bits each, 24 in all),
-// so x * part is exact in fp32 for bf16 x and the MFMA sums exact products.
-// Pairs are packed two bf16 per dword (element 2i in the low half).
-MOK_DEV void split3(float w0, float w1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  const uint32_t u0 = __float_as_uint(w0), u1 = __float_as_uint(w1);
-  const float r0 = w0 - __uint_as_float(u0 & 0xFFFF0000u), r1 = w1 - __uint_as_float(u1 & 0xFFFF0000u);
-  const uint32_t v0 = __float_as_uint(r0), v1 = __float_as_uint(r1);
-  const float q0 = r0 - __uint_as_float(v0 & 0xFFFF0000u), q1 = r1 - __uint_as_float(v1 & 0xFFFF0000u);
-  hi = (u0 >> 16) | (u1 & 0xFFFF0000u);
-  mid = (v0 >> 16) | (v1 & 0xFFFF0000u);
-  lo = (__float_as_uint(q0) >> 16) | (__float_as_uint(q1) & 0xFFFF0000u);
-}
-
 // Forward: one workgroup per TT tokens (TT = 16, or 64 on large inputs with
 // E <= 128). The logits x . Wr^T are a dense contraction (TT token rows x E
 // expert columns x H), done on the matrix cores with

@@ -27,14 +27,6 @@ typedef __attribute__((address_space(3))) i16x4_t* lds_i16x4_ptr;
 MOK_DEV float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 MOK_DEV float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// the nearest bf16 of a pair, the nearest to what it leaves, and a third part: hi + mid + lo is exact (8 + 8 + 8 bits)
-MOK_DEV void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  hi = pack_bf16x2(a, b);
-  const float ra = a - bf_lo(hi), rb = b - bf_hi(hi);
-  mid = pack_bf16x2(ra, rb);
-  lo = pack_bf16x2(ra - bf_lo(mid), rb - bf_hi(mid));
-}
-
 MOK_DEV f32x16_t mfma32(const uint4& a, const uint4& b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
                                                  0, 0);

@@ -46,6 +46,45 @@ def test_dx_keeps_all_bits_with_much_data(E):
     check_cancelled(4105, 4224, E)
 
 
+@pytest.mark.parametrize("E", [30, 60, 100, 200, 300])
+def test_grad_of_the_largest_and_smallest_values(E):
+    """One token of each column and one expert of each row different from zero, at the ends of fp32: finite values stay finite,
+    above bf16's largest too, and keep their 24 bits down to 2^-110. A value v below has a last bit of less than 2^(-110 - 23) =
+    2^-133, bf16's smallest step, and its third part, cut to multiples of that, is short of it by less than 2^-133; the other two
+    parts are multiples of at least 2^-126 where v is at least 2^-111."""
+    import torch
+    T, H = 64, 256
+    g = np.random.default_rng(E)
+    big = np.float32(np.finfo(np.float32).max)
+    ends = np.concatenate([[big, -big], big * (1 - np.arange(1, 40) * 2.0 ** -10), 2.0 ** np.arange(-110, -90)]).astype(np.float32)
+    ends = np.concatenate([ends, ends * np.float32(1 - 2.0 ** -9)])
+    value = lambda *s: g.choice(ends, size=s) * (1 - g.integers(0, 2 ** 10, size=s) * 2.0 ** -24).astype(np.float32)  # noqa: E731
+    ws = F.get_router_workspace(T, H, E, 1)
+    # d_w_router: x = 2^-3 or 2^3 where the value is small, so that neither side leaves the range
+    dl = value(T, E)
+    tok = g.integers(0, T, size=H)
+    for x in (2.0 ** -3, -2.0 ** 6):
+        v = np.where((np.abs(dl) > 1) == (np.abs(x) < 1), dl, 0).astype(np.float32)
+        X = np.zeros((T, H))
+        X[tok, np.arange(H)] = x
+        _, dwr = F.run_router_logits_backward(ws, bf(X), torch.zeros((E, H), device="cuda"), f32(v))
+        torch.cuda.synchronize()
+        want = v[tok].T.astype(np.float64) * x
+        with np.errstate(invalid="ignore"):            # (0 / 0 in its message)
+            assert_within(f64(dwr), want, np.where(np.abs(v[tok].T) < 2.0 ** -110, 2.0 ** -133 * abs(x), 0), "dwr")
+    # dx = 2^-20 w and 2^20 w: one product of each part, then rounded
+    wr, pick = value(E, H), g.integers(0, E, size=T)
+    for d in (2.0 ** -20, 2.0 ** 20):
+        v = np.where((np.abs(wr) > 1) == (d < 1), wr, 0).astype(np.float32)
+        one = np.zeros((T, E), np.float32)
+        one[np.arange(T), pick] = d
+        dx, _ = F.run_router_logits_backward(ws, torch.zeros((T, H), dtype=torch.bfloat16, device="cuda"), f32(v), f32(one))
+        torch.cuda.synchronize()
+        want = v[pick].astype(np.float64) * d
+        lost = np.where(np.abs(v[pick]) < 2.0 ** -110, 2.0 ** -133 * d, 0)
+        assert_within(f64(dx), want, lost + HALF * (np.abs(want) + lost), "dx")
+
+
 @pytest.mark.parametrize("E", [70, 128])
 def test_grad_of_much_data(E):
     check_grad(4105, 4224, E, residual=E % 4 == 0, inplace=E == 128)
