@@ -218,7 +218,7 @@ class NormWorkspace:
 
 class NormOutput(NamedTuple):
     y: torch.Tensor | None       # [T][H] bf16
-    sum: torch.Tensor            # [T][H] bf16: the residual stream (x itself without a residual)
+    sum: torch.Tensor | None     # [T][H] bf16: the residual stream (x itself without a residual; None: y lies over it)
     rstd: torch.Tensor | None    # [T] fp32, in training
     q: torch.Tensor | None       # [T][H] MXFP8 codes of y, and
     scales: torch.Tensor | None  # [T][H/32] their scales
@@ -235,7 +235,8 @@ def get_norm_workspace(T, H, eps=1e-6, weight_dtype=torch.bfloat16, device="cuda
 
 def run_norm_forward(w: NormWorkspace, x, weight, residual=None, out="bf16", y=None, sum_out=None):
     """The norm of x, or of the stream x + residual, which is returned too (sum_out=residual updates it in place).
-    out: "bf16" (y), "mxfp8" (q and scales, as run_mx_matmul takes them) or "both". weight None: ones."""
+    out: "bf16" (y), "mxfp8" (q and scales, as run_mx_matmul takes them) or "both". weight None: ones. y=x without a
+    residual overwrites the stream, which a backward needs: sum is None then."""
     if out not in ("bf16", "mxfp8", "both"):
         raise ValueError(f"out: {out!r}, wanted 'bf16', 'mxfp8' or 'both'")
     given = y is not None or sum_out is not None
@@ -257,7 +258,9 @@ def run_norm_forward(w: NormWorkspace, x, weight, residual=None, out="bf16", y=N
         norm_forward(w.problem, x, weight, y, residual, sum_out, rstd, q, scales)
     else:
         _norm_forward(w.problem, _device_of(x), x, weight, y, residual, sum_out, rstd, q, scales, None)
-    return NormOutput(y, x if residual is None else sum_out, rstd, q, scales)
+    if residual is None:
+        sum_out = None if given and x.numel() and y.data_ptr() == x.data_ptr() else x
+    return NormOutput(y, sum_out, rstd, q, scales)
 
 
 def _rows_like(t):
@@ -272,6 +275,8 @@ def run_norm_backward(w: NormWorkspace, z, rstd, weight, dy, d_sum=None, dx=None
     added to dx. dw is None without a weight."""
     if not w.training:
         raise ValueError("a norm workspace without training has no backward")
+    if z is None:
+        raise ValueError("z: None, the stream that the forward normed is wanted (y was written over it)")
     dw = None if weight is None else torch.empty_like(weight)
     if dx is not None:
         norm_backward(w.problem, dy, z, rstd, weight, dx, dw, w.workspace, d_sum=d_sum)

@@ -155,6 +155,30 @@ def test_forward_strides_and_places():
     assert torch.equal(o.y, F.run_norm_forward(workspace(T, H), bf(x), wb).y)
 
 
+def test_forward_names_no_stream_that_y_lies_over():
+    """Without a residual the stream is x itself, and where y was written over it there is none left to name."""
+    import torch
+    x, r, w = (bf(a) for a in make(6, 96, 1))
+    ws = workspace(6, 96)
+    a = x.clone()
+    o = F.run_norm_forward(ws, a, w, y=a)
+    assert o.sum is None and o.y is a
+    with pytest.raises(ValueError):
+        F.run_norm_backward(ws, o.sum, o.rstd, w, x)
+    # the window of a wider matrix, and y elsewhere in it
+    m = torch.zeros((6, 192), dtype=torch.bfloat16, device="cuda")
+    m[:, :96] = x
+    o = F.run_norm_forward(ws, m[:, :96], w, y=m[:, 96:])
+    assert o.sum.data_ptr() == m.data_ptr() and torch.equal(o.sum, x)
+    assert F.run_norm_forward(ws, m[:, :96], w, y=m[:, :96]).sum is None
+    # with a residual the stream is what the call wrote
+    a, ref = x.clone(), F.run_norm_forward(ws, x, w, r)
+    o = F.run_norm_forward(ws, a, w, r, y=a)
+    assert torch.equal(o.sum, ref.sum) and torch.equal(a, ref.y)
+    e = torch.empty((0, 96), dtype=torch.bfloat16, device="cuda")
+    assert F.run_norm_forward(workspace(0, 96), e, w, y=torch.empty_like(e)).sum is e
+
+
 def test_forward_leaves_what_lies_behind():
     import torch
     T, H = 5, 96

@@ -151,3 +151,9 @@ def test_python_refuses_other_tensors():
         F.get_norm_workspace(4, 64, weight_dtype=torch.float16)
     with pytest.raises(ValueError):
         F.run_norm_backward(F.get_norm_workspace(4, 64, device="cpu", training=False), x, x, None, x)
+
+
+def test_python_refuses_a_stream_that_was_overwritten():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        F.run_norm_backward(F.get_norm_workspace(4, 64, device="cpu"), None, torch.zeros(4), None, x)
