@@ -568,10 +568,10 @@ mok_status mok_router_losses_backward(const mok_problem* problem, const float* l
  * cores, d_logits and w_router in three bf16 parts each (all bits of a value down to
  * 2^-110, below it those from 2^-133 on): for d_w_router the products are exact, for
  * dx to 2^-21 of a product before the one rounding; a value of d_logits or w_router
- * that is not finite makes NaN of what it enters. x, dx,
- * residual, w_router, d_logits and d_w_router are 16-byte aligned. T = 0 gives zeros in
- * d_w_router. Outputs and workspace share no memory with another operand but
- * dx with residual (MOK_ERR_INVALID_ARG). */
+ * that is not finite makes NaN of what it enters. x, dx, residual, w_router and
+ * d_w_router are 16-byte aligned, d_logits as above. T = 0 gives zeros in d_w_router.
+ * Outputs and workspace share no memory with another operand but dx with residual
+ * (MOK_ERR_INVALID_ARG). */
 mok_status mok_router_logits_backward(const mok_problem* problem, const void* x, const float* w_router,
                                       const float* d_logits, const void* residual, void* dx, float* d_w_router,
                                       void* workspace, size_t workspace_bytes, void* stream);

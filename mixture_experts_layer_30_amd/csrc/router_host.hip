@@ -30,6 +30,10 @@ bool any_overlap(const Span* outs, int no, const Span* ins, int ni) {
   return false;
 }
 
+// Alignment of [T][E] logits and their gradient. Where E is not a multiple of 4 their rows start at any value, so the
+// losses' kernels go through them value by value, and the dense backward loads 16 bytes from any value on.
+size_t row_align(size_t E) { return E % 4 == 0 ? 16 : 4; }
+
 mok_losses_args losses_args(const mok_problem& p) {
   mok_losses_args a;
   memset(&a, 0, sizeof a);
@@ -82,7 +86,7 @@ mok_status mok_router_losses(const mok_problem* problem, const float* logits, co
   if (s != MOK_OK) return s;
   const size_t T = (size_t)problem->T, E = (size_t)problem->E, k = (size_t)problem->topk;
   if (!losses || !counts || !prob_sum || !n_tokens || (T > 0 && (!logits || !topk_ids))) return MOK_ERR_INVALID_ARG;
-  if (!aligned(logits, 16) || !aligned(topk_ids, 4) || !aligned(losses, 4) || !aligned(counts, 4) ||
+  if (!aligned(logits, row_align(E)) || !aligned(topk_ids, 4) || !aligned(losses, 4) || !aligned(counts, 4) ||
       !aligned(prob_sum, 4) || !aligned(n_tokens, 4) || !aligned(workspace, 16))
     return MOK_ERR_INVALID_ARG;
   const size_t need = mok_losses_part_bytes(problem->T, problem->E);
@@ -115,8 +119,8 @@ mok_status mok_router_losses_backward(const mok_problem* problem, const float* l
   const size_t T = (size_t)problem->T, E = (size_t)problem->E, k = (size_t)problem->topk;
   if (!counts || !n_tokens || !d_losses) return MOK_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !topk_ids || !d_logits || !topk_w != !d_topk_w)) return MOK_ERR_INVALID_ARG;
-  if (!aligned(logits, 16) || !aligned(topk_ids, 4) || !aligned(counts, 4) || !aligned(n_tokens, 4) ||
-      !aligned(d_losses, 4) || !aligned(topk_w, 4) || !aligned(d_topk_w, 4) || !aligned(d_logits, 16))
+  if (!aligned(logits, row_align(E)) || !aligned(topk_ids, 4) || !aligned(counts, 4) || !aligned(n_tokens, 4) ||
+      !aligned(d_losses, 4) || !aligned(topk_w, 4) || !aligned(d_topk_w, 4) || !aligned(d_logits, row_align(E)))
     return MOK_ERR_INVALID_ARG;
   const Span out = {d_logits, T * E * 4};
   // (a row is read before the same lanes write it)
@@ -147,9 +151,10 @@ mok_status mok_router_logits_backward(const mok_problem* problem, const void* x,
   if (s != MOK_OK) return s;
   const size_t T = (size_t)problem->T, H = (size_t)problem->H, E = (size_t)problem->E;
   if (!d_w_router || (T > 0 && (!x || !w_router || !d_logits || !dx))) return MOK_ERR_INVALID_ARG;
-  for (const void* p : {x, (const void*)w_router, (const void*)d_logits, residual, (const void*)dx,
-                        (const void*)d_w_router, (const void*)workspace})
+  for (const void* p : {x, (const void*)w_router, residual, (const void*)dx, (const void*)d_w_router,
+                        (const void*)workspace})
     if (!aligned(p, 16)) return MOK_ERR_INVALID_ARG;
+  if (!aligned(d_logits, row_align(E))) return MOK_ERR_INVALID_ARG;
   const size_t need = mok_logits_bwd_part_bytes(problem->T, (int)H, (int)E);
   if (need && (!workspace || workspace_bytes < need)) return MOK_ERR_BUFFER_TOO_SMALL;
   const Span outs[3] = {{dx, T * H * 2}, {d_w_router, E * H * 4}, {workspace, need}};

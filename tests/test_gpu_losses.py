@@ -245,6 +245,28 @@ def test_losses_over_two_ranks():
         assert torch.equal(F.run_router_losses_backward(half, L[p], I[p], s, D, mask=M[p]), d[p])
 
 
+@pytest.mark.parametrize("E", [1, 7, 37, 130, 511])
+def test_slices_of_tokens(E):
+    """Rows of the middle of a batch, at whatever place they start: the bits of the same rows in memory of their own."""
+    import torch
+    T, H, k, a, b = 90, 256, min(E, 3), 11, 74
+    logits, ids, w, g, m = routing(T, E, k)
+    L, I, W, G, M, D = f32(logits), i32(ids), f32(w), f32(g), torch.from_numpy(m).cuda(), f32(np.array([1.0, 0.5]))
+    rng = np.random.default_rng(0)
+    x, wr = bf(rng.normal(size=(b - a, H))), f32(rng.normal(size=(E, H)))
+    ws = F.get_router_workspace(b - a, H, E, k)
+    out = torch.full_like(L, 7.0)
+    got = []
+    for own in (False, True):
+        v = [t[a:b].clone() if own else t[a:b] for t in (L, I, W, G, M)]
+        o = F.run_router_losses(ws, v[0], v[1], mask=v[4])
+        d = torch.empty_like(v[0]) if own else out[a:b]
+        mok.router_losses_backward(ws.problem, v[0], v[1], o.counts, o.n_tokens, D, d, v[2], v[3], mask=v[4])
+        got.append((*o, d, *F.run_router_logits_backward(ws, x, wr, d)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(*got)) and (out[:a] == 7).all() and (out[b:] == 7).all()
+
+
 def test_losses_leave_what_lies_behind():
     import torch
     T, E, k = 33, 21, 3

@@ -133,3 +133,17 @@ def test_python_refuses_other_tensors():
         F.run_router_losses(w, torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32))
     with pytest.raises(mok.MokError):
         F.run_router_forward(w, torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(8, 128))
+
+
+def test_rows_that_start_at_any_value():
+    """Where E is not a multiple of 4, a slice of the tokens starts wherever it does."""
+    for e in (37, 38, 39):
+        p = P(E=e)
+        for k in (4, 8, 12, 4 * e):
+            assert loss(p=p, logits=LOSS["logits"] + k) == GONE and grad(p=p, dl=GRAD["dl"] + k) == GONE
+            assert back(p=p, logits=BACK["logits"] + k, out=BACK["out"] + 4) == GONE
+        assert loss(p=p, logits=LOSS["logits"] + 2) == INV and grad(p=p, dl=GRAD["dl"] + 2) == INV
+        assert back(p=p, logits=BACK["logits"] + 2) == INV and back(p=p, out=BACK["out"] + 2) == INV
+    for k in (4, 8):
+        assert loss(logits=LOSS["logits"] + k) == INV and grad(dl=GRAD["dl"] + k) == INV
+        assert back(logits=BACK["logits"] + k) == INV and back(out=BACK["out"] + k) == INV
