@@ -520,7 +520,8 @@ mok_status mok_norm_backward(const mok_norm_problem* problem, const void* dy, co
  * and 0 both where n = 0. Ids outside [0, E) are counted nowhere. A token that
  * the mask leaves out is not looked at, whatever its logits hold. Logits of
  * -infinity are experts that cannot be chosen; a row of nothing else has p = 0
- * and lse = 0. Sums are fp32 in a fixed order, counts exact integers.
+ * and lse = 0. Sums have a fixed order, prob_sum in fp32 and the z loss in fp64;
+ * counts are exact integers.
  * problem: as the router's, T at most 2^30 (MOK_ERR_UNSUPPORTED); the two
  * losses' calls do not look at H and I beyond their being valid, and take any
  * topk. logits and d_logits are 16-byte aligned. */

@@ -115,7 +115,7 @@ __global__ __launch_bounds__(kFT) void losses_rows_kernel(const mok_losses_args 
   constexpr int SPW = 64 / L, TPB = kFWaves * SPW;
   __shared__ int hist[512];
   __shared__ __attribute__((aligned(16))) float ps[kFWaves][4 * L * I];
-  __shared__ float zs[kFWaves];
+  __shared__ double zs[kFWaves];
   __shared__ int ns[kFWaves];
   __shared__ double red[kFWaves];
   const int lane = lane_id(), wave = (int)threadIdx.x >> 6, l = lane % L;
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kFT) void losses_rows_kernel(const mok_losses_args 
   float acc[I][4];
 #pragma unroll
   for (int i = 0; i < I; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  float z = 0.f;
+  double z = 0.0;                                // one term a token: in 64 bits it costs nothing
   int n = 0;
   const int64_t step = (int64_t)gridDim.x * TPB, t0 = (int64_t)blockIdx.x * TPB;
   const int at = wave * SPW + lane / L;
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kFT) void losses_rows_kernel(const mok_losses_args 
 #pragma unroll
       for (int u = 0; u < 4; ++u) acc[i][u] = fmaf(v[i][u], inv, acc[i][u]);
     if (l == 0 && live) {
-      z = fmaf(lse, lse, z);
+      z = fma((double)lse, (double)lse, z);
       ++n;
     }
   }
@@ -195,9 +195,9 @@ __global__ __launch_bounds__(kFT) void losses_rows_kernel(const mok_losses_args 
     n += ns[w];
   }
   if (alone) {
-    finish<kFT>(a, cp, (double)z, n, red);
+    finish<kFT>(a, cp, z, n, red);
   } else if (threadIdx.x == 0) {
-    part[2 * a.E] = __float_as_uint(z);
+    part[2 * a.E] = __float_as_uint((float)z);   // (rounded once, and added in 64 bits again)
     part[2 * a.E + 1] = (uint32_t)n;
   }
 }

@@ -127,6 +127,21 @@ def test_losses_tokens(T, E, k):
     check(T, E, k, mask=T % 2 == 1)
 
 
+def test_z_loss_of_large_and_small_rows():
+    """Squares of 2^24 and then of 1, which fp32 loses beside them. With one expert lse is the logit itself, its square is exact
+    in 64 bits and so are the sums of a workgroup, each rounded once to fp32; with the loss's own rounding that is 2 u."""
+    import torch
+    T = 1 << 20
+    L = torch.ones((T, 1), device="cuda")
+    L[:T // 8] = 4096.0
+    ws = F.get_router_workspace(T, 128, 1, 1)
+    o = F.run_router_losses(ws, L, torch.zeros((T, 1), dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    z = (T // 8 * 2.0 ** 24 + T // 8 * 7) / T
+    assert abs(float(o.losses[1]) - z) <= 2.0 * F32 * (1 + F32) * z
+    assert float(o.losses[0]) == 1.0 and float(o.prob_sum) == T and int(o.n_tokens) == T
+
+
 @pytest.mark.parametrize("E", [7, 8, 128, 512])
 @pytest.mark.parametrize("dl", [(np.inf, 0.0), (0.0, np.nan)])
 def test_losses_backward_of_overflowed_gradients(E, dl):
