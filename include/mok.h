@@ -464,9 +464,9 @@ mok_status mok_mxfp8_dequantize(const uint8_t* q, const uint8_t* scales, int64_t
  *       z = x), rstd[t] = 1 / sqrt(mean_h z[t][h]^2 + eps),
  *   y[t][h] = z[t][h] * rstd[t] * weight[h]
  * What is normed is the stream as it is stored: the same bits as a second call
- * on `sum` gives, and what the backward reads. Sums are fp32 in a fixed order
- * that depends on H alone, so a row's results do not depend on the rows beside
- * it. y is written in bf16, or as the MXFP8 rows that mok_mx_matmul takes
+ * on `sum` gives, and what the backward reads. Sums (over a row in the forward
+ * in fp64, else in fp32) have a fixed order that depends on H alone, so a row's
+ * results do not depend on the rows beside it. y is written in bf16, or as the MXFP8 rows that mok_mx_matmul takes
  * (codes q [T][H] with scales [T][H/32], quantized from y in fp32), or both.
  * Any T >= 0; H a multiple of 8, with q of 32, at most 32768
  * (MOK_ERR_UNSUPPORTED otherwise). x has row pitch ld_x; residual, sum, d_sum

@@ -41,15 +41,15 @@ struct RowShape {
 // alternates between calls, so that one barrier a call is enough: a wavefront
 // that writes a half again has passed the barrier of the call between, which
 // every other one reached after its reads.
-template <int TPR>
-MOK_DEV float row_sum(float v, float (*red)[RowShape<TPR>::BT / 64], int turn) {
+template <int TPR, class V>
+MOK_DEV V row_sum(V v, V (*red)[RowShape<TPR>::BT / 64], int turn) {
   v = lanes_sum<(TPR < 64 ? TPR : 64)>(v);
   if constexpr (TPR > 64) {
     constexpr int NW = RowShape<TPR>::NW;
     const int wave = (int)threadIdx.x >> 6;
     if (lane_id() == 0) red[turn][wave] = v;
     __syncthreads();
-    const float* r = red[turn] + wave / NW * NW;
+    const V* r = red[turn] + wave / NW * NW;
     v = r[0];
 #pragma unroll
     for (int i = 1; i < NW; ++i) v += r[i];
@@ -74,7 +74,7 @@ MOK_DEV void load_weight(const void* w, int wf, int c, float v[8]) {
 template <int TPR, int CH>
 __global__ __launch_bounds__(RowShape<TPR>::BT) void norm_fwd_kernel(const mok_norm_args a) {
   using S = RowShape<TPR>;
-  __shared__ float red[2][S::BT / 64];
+  __shared__ double red[2][S::BT / 64];
   const int sub = (int)threadIdx.x / TPR, l = (int)threadIdx.x % TPR;
   const int n8 = a.H / 8;
   float w[CH][8];
@@ -84,14 +84,12 @@ __global__ __launch_bounds__(RowShape<TPR>::BT) void norm_fwd_kernel(const mok_n
     for (int u = 0; u < 8; ++u) w[i][u] = 0.f;
     if (l + i * TPR < n8) load_weight(a.w, a.wf, l + i * TPR, w[i]);
   }
-  const double inv_h64 = 1.0 / a.H;
-  const float inv_h = (float)inv_h64;
+  const double inv_h = 1.0 / a.H;
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * S::RPB; r0 < a.T; r0 += (int64_t)gridDim.x * S::RPB) {
     const int64_t row = r0 + sub;
     const bool live = row < a.T;
-    float z[CH][8];
-    float ss = 0.f;
+    double ss = 0.0;                             // in 64 bits, at the rate of 32
     uint4 xv[CH], rv[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -114,33 +112,38 @@ __global__ __launch_bounds__(RowShape<TPR>::BT) void norm_fwd_kernel(const mok_n
         xv[i] = pack8(p);                        // the stream is kept, and normed, in bf16
         if (live && c < n8) store_nt(reinterpret_cast<uint4*>(a.sum + row * a.lds) + c, xv[i]);
       }
-      unpack8(xv[i], z[i]);
+      float z[8];
+      unpack8(xv[i], z);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) ss = fmaf(z[i][u], z[i][u], ss);
+      for (int u = 0; u < 8; ++u) ss = fma((double)z[u], (double)z[u], ss);
+      // (kept packed, and unpacked once more below: with the values held over the sum a CU holds one row of 1024 threads
+      // in place of two, 202 us at 16384 x 7168)
+      asm volatile("" : "+v"(xv[i].x), "+v"(xv[i].y), "+v"(xv[i].z), "+v"(xv[i].w));
     }
     ss = row_sum<TPR>(ss, red, turn);
     turn ^= 1;
-    const float rstd = 1.0f / sqrtf(fmaf(ss, inv_h, a.eps));
-    // for the codes: one Newton step in 64 bits
-    double rstd64 = rstd;
-    if (a.q && rstd > 0.f)
-      rstd64 += 0.5 * rstd64 * (1.0 - fma((double)ss, inv_h64, (double)a.eps) * rstd64 * rstd64);
+    // a Newton step in 64 bits from the fp32 value (0 where the sum passes fp32's range)
+    const double var = fma(ss, inv_h, (double)a.eps);
+    double rstd64 = 1.0f / sqrtf((float)var);
+    if (rstd64 > 0.0) rstd64 += 0.5 * rstd64 * (1.0 - var * rstd64 * rstd64);
+    const float rstd = (float)rstd64;
     if (live && l == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = l + i * TPR;
       const bool ok = live && c < n8;
-      float y[8];
+      float z[8], y[8];
+      unpack8(xv[i], z);
       if (a.y) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) y[u] = z[i][u] * rstd * w[i][u];
+        for (int u = 0; u < 8; ++u) y[u] = z[u] * rstd * w[i][u];
         if (ok) store_nt(reinterpret_cast<uint4*>(a.y + row * a.ldy) + c, pack8(y));
       }
       if (a.q) {
-        // (a value within its error of the middle between two codes may take either: in 64 bits, at the rate of 32,
-        // the products add nothing to rstd's error)
+        // (a value within its error of the middle between two codes may take either: sum, rstd and products in 64 bits
+        // leave that to the one rounding of y to fp32)
 #pragma unroll
-        for (int u = 0; u < 8; ++u) y[u] = (float)((double)z[i][u] * rstd64 * (double)w[i][u]);
+        for (int u = 0; u < 8; ++u) y[u] = (float)((double)z[u] * rstd64 * (double)w[i][u]);
         // four neighbouring threads hold a block (H is a multiple of 32: all four or none are in the row)
         uint32_t m = 0;
 #pragma unroll

@@ -100,6 +100,21 @@ def test_forward_mxfp8(H, out):
     check_forward(7, H, out=out, wf32=out == "both")
 
 
+@pytest.mark.parametrize("T,H", [(2000, 96), (1500, 4096), (400, 7168), (60, 32768)])
+def test_forward_sums_in_64_bits(T, H):
+    """rstd is its value rounded once: the sum (of exact products), the mean and a Newton step from a value within 4 u, which
+    leaves 1.5 (4 u)^2 < 2^-43, are in 64 bits. MXFP8 rows are those of values within one fp32 rounding of y."""
+    import torch
+    x, r, w = make(T, H, 11)
+    o = F.run_norm_forward(workspace(T, H, eps=2.0 ** -20), bf(x), bf(w), bf(r), out="both")
+    torch.cuda.synchronize()
+    y, z, rstd = no.norm_forward(x, w, r, 2.0 ** -20)
+    one = F32 * (1 + 2.0 ** -16)
+    assert_within(f64(o.rstd), rstd, one * rstd, "rstd")
+    check_mx(o.q, o.scales, y, one * np.abs(y))
+    assert_within(f64(o.y), y, rnd(y, 4 * F32 * np.abs(y)), "y")
+
+
 @pytest.mark.parametrize("T", [1, 2, 31, 33, 1000, 4099])
 @pytest.mark.parametrize("H", [32, 640, 4096])
 def test_forward_rows(T, H):
