@@ -170,6 +170,21 @@ def test_losses_of_large_logits():
         check(50, 33, 4, data=(logits, ids, w, g, m))
 
 
+def test_small_probabilities_keep_their_bits():
+    """One token with logits of 0 and down to -80: every probability within 25 u of itself. Its exponential is within 4 u (2 u of
+    the instruction, 1 of the correction's addition), the denominator within those 4 u and 14 additions, its reciprocal within 2
+    and the product within 1. (The difference from the largest logit, 0, is exact.)"""
+    import torch
+    for E in (8, 100, 512):
+        ws = F.get_router_workspace(1, 128, E, 1)
+        l = np.concatenate([[0.0], -80 * np.random.default_rng(E).random(E - 1)]).astype(np.float32)
+        o = F.run_router_losses(ws, f32(l[None]), torch.zeros((1, 1), dtype=torch.int32, device="cuda"))
+        torch.cuda.synchronize()
+        p = np.exp(l.astype(np.float64))
+        p /= p.sum()
+        assert_within(f64(o.prob_sum), p, 25 * F32 * p, "prob_sum")
+
+
 def test_losses_masks_and_holes():
     import torch
     T, E, k = 40, 20, 3
