@@ -7,6 +7,7 @@ there are 6 k terms: dx is within ((6 k + 8) u + 2^-21) sum |dl Wr| of its value
 import numpy as np
 import pytest
 
+import mixture_experts_layer_30_amd as mok
 from ffn_testlib import HALF, assert_within, dot
 from mixture_experts_layer_30_amd import functional as F
 from test_gpu_losses import check_grad, f32
@@ -88,3 +89,38 @@ def test_grad_of_the_largest_and_smallest_values(E):
 @pytest.mark.parametrize("E", [70, 128])
 def test_grad_of_much_data(E):
     check_grad(4105, 4224, E, residual=E % 4 == 0, inplace=E == 128)
+
+
+@pytest.mark.parametrize("T,H,E,steps", [(4099, 4096, 130, 16), (4099, 4096, 200, 16), (4001, 4096, 257, 25), (4099, 4096, 512, 32),
+                                         (2080, 2048, 256, 4), (2050, 640, 300, 2)])
+def test_grad_of_many_steps(T, H, E, steps):
+    """Above 128 experts with at least `steps` times 32 tokens for each workgroup that forms d_w_router, odd numbers of them among
+    these. (Those that form dx go through 8 or 9 times 32 tokens at H = 4096 up to 256 experts and 16 or 17 beyond, 16 tokens a
+    step.) The workspace holds one [E][H] for each slice of the tokens."""
+    slices = mok.router_workspace(mok.make_problem(T, H, 128, E, 1)) // (4 * E * H)
+    assert (T + 31) // 32 // max(slices, 1) >= steps
+    check_grad(T, H, E, residual=E != 200, inplace=E in (130, 512))
+
+
+@pytest.mark.parametrize("E", [8, 60, 100, 200, 300])
+def test_grad_past_32_bits(E):
+    """More than 2^31 values, 2^32 bytes, of x, dx and the residual: the last rows are what they are alone. All of x but the last
+    32 rows, one step of one workgroup, is zero, and so d_w_router is that step's."""
+    import torch
+    T, H = 300_032, 7168
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB")
+    g = torch.Generator(device="cuda").manual_seed(E)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    x[-32:] = rnd(32, H).bfloat16()
+    res = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    res[-96:] = rnd(96, H).bfloat16()
+    dl, wr = rnd(T, E), rnd(E, H)
+    tail = res[-96:].clone()
+    dx, dwr = F.run_router_logits_backward(F.get_router_workspace(T, H, E, 1), x, wr, dl, residual=res, dx=res)
+    dx2, _ = F.run_router_logits_backward(F.get_router_workspace(96, H, E, 1), x[-96:], wr, dl[-96:], residual=tail)
+    _, dwr2 = F.run_router_logits_backward(F.get_router_workspace(32, H, E, 1), x[-32:], wr, dl[-32:])
+    first = F.run_router_logits_backward(F.get_router_workspace(96, H, E, 1), x[:96], wr, dl[:96])[0]
+    torch.cuda.synchronize()
+    assert torch.equal(dx[-96:], dx2) and torch.equal(dwr, dwr2) and torch.equal(dx[:96], first)

@@ -147,3 +147,19 @@ def test_rows_that_start_at_any_value():
     for k in (4, 8):
         assert loss(logits=LOSS["logits"] + k) == INV and grad(dl=GRAD["dl"] + k) == INV
         assert back(logits=BACK["logits"] + k) == INV and back(out=BACK["out"] + k) == INV
+
+
+def test_workspace_limits():
+    """At most 256 partial rows of the losses' 2 E + 2 words, and 256 tiles of 128 x 256 of d_w_router, whatever the problem."""
+    for t in (0, 1, 33, 203, 1037, 4099, 16384, 65536, 1 << 30):
+        for h in (128, 256, 384, 2048, 4096, 7168, 1 << 14):
+            for e in (1, 2, 37, 60, 64, 128, 129, 256, 300, 512):
+                n = mok.router_workspace(P(T=t, H=h, E=e, topk=1))
+                assert n <= max(256 * (2 * e + 2) * 4, 256 * 128 * 256 * 4), (t, h, e)
+    # one slice of the tokens needs none, and the losses of few tokens neither
+    assert mok.router_workspace(P(T=64, H=4096, E=128)) == 0
+    # 16 slices of [128][4096], 9 of [32][7168]
+    assert mok.router_workspace(P(T=16384, H=4096, E=128)) == 16 * 128 * 4096 * 4
+    assert mok.router_workspace(P(T=16384, H=7168, E=32)) == 9 * 32 * 7168 * 4
+    # 256 workgroups of the losses, at an H that needs less for d_w_router
+    assert mok.router_workspace(P(T=1 << 20, H=128, E=1, topk=1)) >= 256 * 4 * 4
