@@ -170,6 +170,48 @@ def test_forward_strides_and_places():
     assert torch.equal(o.y, F.run_norm_forward(workspace(T, H), bf(x), wb).y)
 
 
+@pytest.mark.parametrize("H", [96, 1056, 8224])
+def test_forward_mxfp8_strides_and_places(H):
+    """MXFP8 rows from windows of wider matrices, the stream beside them, in place over the residual, and over x."""
+    import torch
+    T, P, Q = 19, H + 40, 2 * H + 8
+    x, r, w = make(T, H, 6)
+    wb, ws = bf(w), workspace(T, H)
+    ref = F.run_norm_forward(ws, bf(x), wb, bf(r), out="both")
+    same = lambda o: torch.equal(o.q, ref.q) and torch.equal(o.scales, ref.scales) and torch.equal(o.sum, ref.sum)  # noqa: E731
+    for out in ("mxfp8", "both"):
+        X, R = (torch.full((T, n), 7.0, dtype=torch.bfloat16, device="cuda") for n in (P, Q))
+        X[:, 8:8 + H], R[:, H:2 * H] = bf(x), bf(r)
+        o = F.run_norm_forward(ws, X[:, 8:8 + H], wb, R[:, H:2 * H], out=out)
+        assert same(o) and torch.equal(X[:, 8:8 + H], bf(x)) and torch.equal(R[:, H:2 * H], bf(r))
+        assert out == "mxfp8" or torch.equal(o.y, ref.y)
+        o = F.run_norm_forward(ws, X[:, 8:8 + H], wb, R[:, H:2 * H], out=out, sum_out=R[:, H:2 * H])
+        assert same(o) and (R[:, :H] == 7).all() and (R[:, 2 * H:] == 7).all() and (X[:, :8] == 7).all()
+        a, b = bf(x), bf(r)
+        assert same(F.run_norm_forward(ws, a, wb, b, out=out, sum_out=a)) and torch.equal(a, ref.sum)
+        if out == "both":
+            a, b = bf(x), bf(r)
+            o = F.run_norm_forward(ws, a, wb, b, out=out, y=a, sum_out=b)
+            assert same(o) and torch.equal(a, ref.y)
+    torch.cuda.synchronize()
+
+
+def test_forward_more_rows_than_a_launch_holds():
+    """A launch holds 2^22 rows of this width: workgroups that go round three times give every row the bits it has among fewer."""
+    import torch
+    T, H, N = (2 << 22) + 5, 544, 1 << 20
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GiB")
+    x = torch.empty((T, H), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    w = bf(make(1, H)[2])
+    o = F.run_norm_forward(workspace(T, H), x, w, out="both")
+    for a in range(0, T, N):
+        n = min(N, T - a)
+        p = F.run_norm_forward(workspace(n, H), x[a:a + n], w, out="both")
+        assert torch.equal(p.y, o.y[a:a + n]) and torch.equal(p.rstd, o.rstd[a:a + n])
+        assert torch.equal(p.q, o.q[a:a + n]) and torch.equal(p.scales, o.scales[a:a + n])
+
+
 def test_forward_names_no_stream_that_y_lies_over():
     """Without a residual the stream is x itself, and where y was written over it there is none left to name."""
     import torch
@@ -313,6 +355,28 @@ def test_backward_against_differences_of_the_forward():
         assert abs(num - (f64(dw) * dwv).sum()) <= HALF * 1.01 * (np.abs(f64(dw)) * np.abs(dwv)).sum() + 1e-6
 
 
+@pytest.mark.parametrize("T,H", [(70, 16640), (300, 32768)])
+def test_backward_of_wide_rows_in_strides_and_places(T, H):
+    """Beyond 16384 columns the sums of dw lie in LDS."""
+    import torch
+    z, ds, w = make(T, H, 1)
+    dy = bf16_round(np.random.default_rng(2).normal(size=(T, H)))
+    ws, wb = workspace(T, H), bf(w)
+    rs = F.run_norm_forward(ws, bf(z), wb).rstd
+    ref = F.run_norm_backward(ws, bf(z), rs, wb, bf(dy), d_sum=bf(ds))
+    Z, D, G = (torch.full((T, H + n), 7.0, dtype=torch.bfloat16, device="cuda") for n in (24, 40, 8))
+    Z[:, 16:16 + H], D[:, 8:8 + H], G[:, :H] = bf(z), bf(ds), bf(dy)
+    O = torch.full_like(D, 5.0)
+    for dx in (O[:, 32:32 + H], D[:, 8:8 + H]):
+        got = F.run_norm_backward(ws, Z[:, 16:16 + H], rs, wb, G[:, :H], d_sum=D[:, 8:8 + H], dx=dx)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    assert (O[:, :32] == 5).all() and (O[:, 32 + H:] == 5).all() and (D[:, :8] == 7).all() and (D[:, 8 + H:] == 7).all()
+    a = bf(dy)
+    got = F.run_norm_backward(ws, bf(z), rs, wb, a, d_sum=bf(ds), dx=a)
+    torch.cuda.synchronize()
+    assert torch.equal(a, ref[0]) and torch.equal(got[1], ref[1])
+
+
 def test_backward_strides_and_places():
     import torch
     T, H = 300, 520
@@ -415,6 +479,24 @@ def test_dequantize_returns_the_quantizers_values(rows, K):
     torch.cuda.synchronize()
     np.testing.assert_array_equal(f64(out[:rows * K]).reshape(rows, K), do.mxfp8_round(v))
     assert (out[rows * K:] == 3).all()
+
+
+def test_dequantize_past_32_bits():
+    """More than 2^32 codes, 2^33 bytes of values: the first and last rows are what they are alone."""
+    import torch
+    rows, K = (1 << 20) + 3, 4128
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GiB")
+    g = torch.Generator("cuda").manual_seed(2)
+    q = torch.zeros((rows, K), dtype=torch.uint8, device="cuda")
+    s = torch.full((rows, K // 32), 127, dtype=torch.uint8, device="cuda")
+    for a in (slice(0, 64), slice(rows - 64, rows)):
+        q[a] = torch.randint(0, 127, (64, K), generator=g, device="cuda", dtype=torch.uint8)
+        s[a] = torch.randint(100, 150, (64, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    v = F.mxfp8_dequantize(q, s)
+    for a in (slice(0, 64), slice(rows - 64, rows)):
+        assert torch.equal(v[a], F.mxfp8_dequantize(q[a], s[a])) and v[a].any()
+    assert not v[64:rows - 64].any()
 
 
 def test_norm_into_an_mxfp4_product():
