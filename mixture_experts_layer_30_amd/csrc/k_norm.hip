@@ -116,8 +116,8 @@ __global__ __launch_bounds__(RowShape<TPR>::BT) void norm_fwd_kernel(const mok_n
       unpack8(xv[i], z);
 #pragma unroll
       for (int u = 0; u < 8; ++u) ss = fma((double)z[u], (double)z[u], ss);
-      // (kept packed, and unpacked once more below: with the values held over the sum a CU holds one row of 1024 threads
-      // in place of two, 202 us at 16384 x 7168)
+      // (kept packed, and unpacked once more below: with the values held over the sum a CU holds one row of 1024
+      // threads in place of two, 202 us at 16384 x 7168 for 161)
       asm volatile("" : "+v"(xv[i].x), "+v"(xv[i].y), "+v"(xv[i].z), "+v"(xv[i].w));
     }
     ss = row_sum<TPR>(ss, red, turn);

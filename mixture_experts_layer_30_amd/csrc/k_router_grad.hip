@@ -445,30 +445,35 @@ __global__ __launch_bounds__(256) void router_dwr_join_kernel(const float* __res
   reinterpret_cast<float4*>(dwr)[i] = s;
 }
 
-// A slice a CU, and a few steps of tokens at least, the last slice fewer: partial sums
-// against workgroups. Two kinds of workgroups (pair): three steps (1037 tokens x 2048, 60
-// experts: 12.6 us with three, 13.7 with two or one, 12.8 with four; 300 x 1024: 10.2, 9.6
-// with two), and a CU each, so half the slices, while that is at most six (1000 x 4096,
-// 128 experts: 21.9 us, 24.6 with all; 3000 x 2048: 25.4, 27.4); with eight it is no longer
-// faster everywhere (2048 x 4096: 29.3, 30.3 with 128 experts, 17.4, 16.6 with 16). Else
-// two (200 experts, 1000 x 4096: 35.5 us, 37.2 with three; 300 x 1024: 25.2, 27.7).
+// Partial sums against workgroups: `workgroups` of them at most, and about two steps of 32 tokens each at least (200
+// experts, 1000 x 4096: 40.5 us, 44.1 with three; 300 x 1024: 29.9, 34.4). The steps are spread evenly over the slices:
+// where they do not divide, slices differ by one step, and of so few some have one.
 constexpr int kWorkgroups = 256;
-Plan plan_of(int64_t T, int H, int columns, int eblocks, bool pair) {
+int64_t steps_of(int64_t T, int64_t tiles, int workgroups) {
+  const int64_t steps = (T + 31) / 32, slices = std::max<int64_t>(1, workgroups / tiles);
+  return (steps + slices - 1) / slices;
+}
+Plan plan_of(int64_t T, int H, int columns, int eblocks, int workgroups) {
   Plan p;
   p.panels = (H + columns - 1) / columns;
   p.eblocks = eblocks;
-  const int64_t steps = (T + 31) / 32, tiles = (int64_t)p.panels * eblocks;
-  const auto steps_of = [&](int64_t workgroups) {
-    const int64_t s = std::max<int64_t>(1, workgroups / tiles);
-    return (steps + s - 1) / s;
-  };
-  const int64_t half = steps_of(kWorkgroups / 2);
-  const int64_t per = std::max<int64_t>(pair ? 3 : 2, pair && half <= 6 ? half : steps_of(kWorkgroups));
-  p.slices = (int)std::max<int64_t>(1, (steps + per - 1) / per);
+  const int64_t per = std::max<int64_t>(2, steps_of(T, (int64_t)p.panels * eblocks, workgroups));
+  p.slices = (int)std::max<int64_t>(1, ((T + 31) / 32 + per - 1) / per);
   return p;
 }
-// of the launch that forms dWr
-Plan dwr_plan(int64_t T, int H, int E) { return plan_of(T, H, 256, (E + 127) / 128, E <= 128); }
+// With much data, and x read for both at once, the one kernel is nearer the memory (64 experts, 8192 x 4096 with a
+// residual 60.5 us, as a pair 64.9; 32 experts 49.3, 51.5); with less the pair's shorter ways count (4096 x 4096:
+// 34.9, 34.0; 26.6, 25.5; 1037 x 2048: 17.0, 14.3; 13.5, 11.3). From 65 to 128 experts, with two launches in place of
+// the one: 8192 x 4096 97 us, as a pair 107; 4096 x 4096 59, 59; 2048 x 4096 40.1, 35.4; 1000 x 4096 29.8, 25.1.
+bool paired(int64_t T, int H, int E) { return E <= 128 && T * H <= (int64_t)1 << 24; }
+// Of the launch that forms dWr. Of a pair's two kinds of workgroups each has half of the CUs, up to 64 experts while
+// that makes slices of six steps at most (16 experts, 2048 x 4096: all 17.2 us, half 18.0; 128 experts, where dx comes
+// in twice as many workgroups: 1000 x 4096 29.1, 25.3; 3000 x 2048 33.2, 29.9; 2048 x 4096 40.0, 35.4; 4096 x 4096 62,
+// 59).
+Plan dwr_plan(int64_t T, int H, int E) {
+  const bool half = paired(T, H, E) && (E > 64 || steps_of(T, (H + 255) / 256, kWorkgroups / 2) <= 6);
+  return plan_of(T, H, 256, (E + 127) / 128, half ? kWorkgroups / 2 : kWorkgroups);
+}
 
 template <int KS, bool DX, bool DWR, int AHEAD, int MT = 2, int ST = 32>
 hipError_t launch(const mok_logits_bwd_args& a, const Plan& p, hipStream_t st) {
@@ -499,19 +504,15 @@ hipError_t mok_launch_logits_bwd(const mok_logits_bwd_args& a, hipStream_t st) {
   hipError_t e = hipSuccess;
   // no tokens: empty sums, and nothing that reads Wr, which may be NULL then
   if (a.T == 0) return launch<4, false, true, 2>(a, p, st);
-  // With much data, and x read for both at once, the one kernel is nearer the memory (64 experts, 8192 x 4096 with a
-  // residual 60.5 us, as a pair 64.9; 32 experts 49.3, 51.5); with less the pair's shorter ways count (4096 x 4096:
-  // 34.9, 34.0; 26.6, 25.5; 1037 x 2048: 17.0, 14.3; 13.5, 11.3). From 65 to 128 experts, with two launches in place of the
-  // one: 8192 x 4096 93 us, as a pair 102; 4096 x 4096 59, 62; 2048 x 4096 40.1, 40.7; 1000 x 4096 29.8, 25.1.
-  const bool much = a.T * a.H > (int64_t)1 << 24;
-  if (a.E <= 64 && much) {
-    e = a.E <= 32 ? launch<1, true, true, 2>(a, p, st) : launch<2, true, true, 2>(a, p, st);
-  } else if (a.E <= 128 && !much) {
+  if (paired(a.T, a.H, a.E)) {
     e = a.E <= 32 ? launch_pair<1>(a, p, st) : a.E <= 64 ? launch_pair<2>(a, p, st) : launch_pair<4>(a, p, st);
+  } else if (a.E <= 64) {
+    e = a.E <= 32 ? launch<1, true, true, 2>(a, p, st) : launch<2, true, true, 2>(a, p, st);
   } else {
-    e = a.E <= 128   ? launch<4, true, false, 2>(a, plan_of(a.T, a.H, 256, 1, false), st)
-        : a.E <= 256 ? launch<8, true, false, 1, 2, 16>(a, plan_of(a.T, a.H, 256, 1, false), st)
-                     : launch<16, true, false, 1, 1, 16>(a, plan_of(a.T, a.H, 128, 1, false), st);
+    const Plan px = plan_of(a.T, a.H, a.E <= 256 ? 256 : 128, 1, kWorkgroups);
+    e = a.E <= 128   ? launch<4, true, false, 2>(a, px, st)
+        : a.E <= 256 ? launch<8, true, false, 1, 2, 16>(a, px, st)
+                     : launch<16, true, false, 1, 1, 16>(a, px, st);
     if (e != hipSuccess) return e;
     e = launch<4, false, true, 2>(a, p, st);
   }

@@ -102,6 +102,15 @@ def test_grad_of_many_steps(T, H, E, steps):
     check_grad(T, H, E, residual=E != 200, inplace=E in (130, 512))
 
 
+@pytest.mark.parametrize("T,H,E,dwr,dx", [(300, 1024, 70, 20, 40), (97, 1152, 9, 10, 10), (333, 1408, 100, 36, 66),
+                                          (1100, 896, 70, 72, 126), (2000, 1152, 33, 105, 105), (4099, 1664, 128, 119, 221)])
+def test_grad_of_workgroups_of_either_kind(T, H, E, dwr, dx):
+    """Numbers of workgroups that form d_w_router and dx in one launch which are no multiples of 8, or of each other."""
+    slices = mok.router_workspace(mok.make_problem(T, H, 128, E, 1)) // (4 * E * H)
+    assert (slices * ((H + 255) // 256), slices * ((H + 127) // 128 if E > 64 else (H + 255) // 256)) == (dwr, dx)
+    check_grad(T, H, E, residual=E % 2 == 0)
+
+
 @pytest.mark.parametrize("E", [8, 60, 100, 200, 300])
 def test_grad_past_32_bits(E):
     """More than 2^31 values, 2^32 bytes, of x, dx and the residual: the last rows are what they are alone. All of x but the last
