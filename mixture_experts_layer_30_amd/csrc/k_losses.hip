@@ -29,7 +29,10 @@ constexpr int kBT = 256, kWaves = kBT / 64;      // backward
 // forward: few large workgroups, so that few partial sums have to be added
 constexpr int kFT = 1024, kFWaves = kFT / 64;
 constexpr int kGroups = 256;                     // most of them
-constexpr int kAlone = 4;                        // passes that one workgroup makes by itself
+// Passes that one workgroup makes by itself, without a second launch that joins: both losses' calls of 1024 to 2048
+// tokens x 8 10.1 us, 11.3 where two passes are split up; 203 x 37 10.7, 10.8; 60 x 512 12.6, 13.2. Where eight passes
+// stay with one, 400 x 37 takes 13.3 us, not 11.1, and 256 x 128 13.8, not 10.9.
+constexpr int kAlone = 4;
 
 // LDS accesses of a wavefront's lanes above land before those below
 MOK_DEV void wave_order() {

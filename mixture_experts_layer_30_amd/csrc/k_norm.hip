@@ -363,6 +363,9 @@ hipError_t mok_launch_norm_forward(const mok_norm_args& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// 1024 threads a CU, as one workgroup or several: 16384 x 7168 166 us, with half as many 255, with twice as many 173;
+// 1000 x 32768 95, 113, 112; 4096 x 4096 31.3, 32.4, 35.3; 24871 x 128 11.0, 10.7, 11.9. (More workgroups make more
+// partial rows, fewer leave loads unissued.)
 int mok_norm_groups(int64_t T, int H) {
   return by_width(H, [&](auto tpr, auto) {
     using S = RowShape<decltype(tpr)::value>;

@@ -41,7 +41,8 @@ MOK_DEV f32x4_t mfma16(const uint4& a, const uint4& b, f32x4_t c) {
 // (With branches round them the compiler cannot tell how many are in flight at the
 // wait for one, and waits for all: dWr of 16384 x 4096 with 128 experts 77 us against
 // 57.) A 16-byte load that the end of the bytes cuts reads its part before the end and
-// zeros (checked on gfx950). Offsets are 32 bits: a step's rows, at most 2^26 bytes.
+// zeros (checked on gfx950). Offsets are 32 bits: a step's rows, at most 2^26 bytes of
+// x, dx and the residual, and 2^27 of Wr.
 typedef __amdgpu_buffer_rsrc_t buf_t;
 constexpr uint32_t kOut = 0x7ffffff0u;           // past every descriptor's bytes
 MOK_DEV buf_t make_buf(const void* p, int64_t bytes) {
@@ -467,9 +468,9 @@ Plan plan_of(int64_t T, int H, int columns, int eblocks, int workgroups) {
 // the one: 8192 x 4096 97 us, as a pair 107; 4096 x 4096 59, 59; 2048 x 4096 40.1, 35.4; 1000 x 4096 29.8, 25.1.
 bool paired(int64_t T, int H, int E) { return E <= 128 && T * H <= (int64_t)1 << 24; }
 // Of the launch that forms dWr. Of a pair's two kinds of workgroups each has half of the CUs, up to 64 experts while
-// that makes slices of six steps at most (16 experts, 2048 x 4096: all 17.2 us, half 18.0; 128 experts, where dx comes
-// in twice as many workgroups: 1000 x 4096 29.1, 25.3; 3000 x 2048 33.2, 29.9; 2048 x 4096 40.0, 35.4; 4096 x 4096 62,
-// 59).
+// that makes slices of six steps at most (64 experts, 1000 x 4096: all 19.8 us, half 18.2; 32 experts, 1037 x 2048:
+// 12.4, 11.4; eight steps, 16 experts, 2048 x 4096: 17.2, 18.0; 128 experts, where dx comes in twice as many
+// workgroups: 1000 x 4096 29.1, 25.3; 3000 x 2048 33.2, 29.9; 2048 x 4096 40.0, 35.4; 4096 x 4096 62, 59).
 Plan dwr_plan(int64_t T, int H, int E) {
   const bool half = paired(T, H, E) && (E > 64 || steps_of(T, (H + 255) / 256, kWorkgroups / 2) <= 6);
   return plan_of(T, H, 256, (E + 127) / 128, half ? kWorkgroups / 2 : kWorkgroups);
