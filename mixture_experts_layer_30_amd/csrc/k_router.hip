@@ -12,6 +12,7 @@
 // d_sel[t][j] = w_j (g_j - sum_i w_i g_i) with g = d topk_w; then
 // dx[t] = sum_j d_sel[t][j] Wr[e_j] and dWr[e] = sum over the rows routed
 // to e of d_sel * x[t]. No atomics: every sum has a fixed order.
+#include "bf16_split.h"
 #include "mok_device.h"
 #include "mok_launch.h"
 #include "router_launch.h"

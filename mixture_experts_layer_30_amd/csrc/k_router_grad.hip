@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "bf16_split.h"
 #include "gemm_core.h"
 #include "router_launch.h"
 
