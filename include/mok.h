@@ -466,8 +466,10 @@ mok_status mok_mxfp8_dequantize(const uint8_t* q, const uint8_t* scales, int64_t
  * What is normed is the stream as it is stored: the same bits as a second call
  * on `sum` gives, and what the backward reads. Sums (over a row in the forward
  * in fp64, else in fp32) have a fixed order that depends on H alone, so a row's
- * results do not depend on the rows beside it. y is written in bf16, or as the MXFP8 rows that mok_mx_matmul takes
- * (codes q [T][H] with scales [T][H/32], quantized from y in fp32), or both.
+ * results do not depend on the rows beside it. y is written in bf16, or as the
+ * MXFP8 rows that mok_mx_matmul takes (codes q [T][H] with scales [T][H/32],
+ * quantized from y in fp32), or both. (mok_forward and mok_ffn_forward take x in
+ * bf16 and quantize it themselves where they need it in MXFP8.)
  * Any T >= 0; H a multiple of 8, with q of 32, at most 32768
  * (MOK_ERR_UNSUPPORTED otherwise). x has row pitch ld_x; residual, sum, d_sum
  * and dx ld_s; y and dy ld_y (elements, multiples of 8, 0 = H, at most 2^31).

@@ -11,8 +11,8 @@
 // Both are one pass over the logits and bound by reading (and writing) them, small
 // ones by latency. A token lies in L lanes of a wavefront, 4 I experts each (lane l:
 // the experts 4 (l + L i) .. + 3), so a wavefront works on 64 / L tokens at once.
-// 65536 tokens x 512 experts: forward 34 us for 134 MB and 8 us for the joining of
-// the sums, gradient 45 us for 268 MB (6.0 TB/s); 16384 x 128: 5.5, 6.4 and 8.4 us.
+// 65536 tokens x 512 experts: forward 36 us for 134 MB and 9 us for the joining of
+// the sums, gradient 46 us for 268 MB (5.8 TB/s); 16384 x 128: 5.8, 6.5 and 8.8 us.
 // Tried and dropped: several rows side by side in a lane, and loading a row ahead
 // (the forward as it is, the gradient 5 to 10 us longer for its registers and LDS);
 // joining in one launch whose last workgroup goes on (every wavefront's fence writes
