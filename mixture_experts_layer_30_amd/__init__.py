@@ -560,8 +560,8 @@ def _norm_forward(problem, dev, x, weight, y, residual, sum_out, rstd, q, scales
         if _pitch(sum_out) != ld_s:
             raise MokError(MOK_ERR_INVALID_ARG, "sum_out: another row pitch than residual")
     _run("mok_norm_forward", dev, stream, lib().mok_norm_forward,
-         _norm_call(problem, _pitch(x), ld_s, 0 if y is None else _pitch(y)), x.data_ptr(), _addr(residual), _addr(weight),
-         _addr(y), _addr(sum_out), _addr(rstd), _addr(q), _addr(scales))
+         _norm_call(problem, _pitch(x), ld_s, 0 if y is None else _pitch(y)), x.data_ptr(), _addr(residual),
+         _addr(weight), _addr(y), _addr(sum_out), _addr(rstd), _addr(q), _addr(scales))
 
 
 def norm_forward(problem, x, weight, y=None, residual=None, sum_out=None, rstd=None, q=None, scales=None, stream=None):
@@ -665,8 +665,8 @@ def router_losses(problem, logits, topk_ids, losses, counts, prob_sum, n_tokens,
     _router_losses(problem, dev, logits, topk_ids, losses, counts, prob_sum, n_tokens, workspace, mask, stream)
 
 
-def _router_losses_backward(problem, dev, logits, topk_ids, counts, n_tokens, d_losses, d_logits, topk_w, d_topk_w, mask,
-                            stream):
+def _router_losses_backward(problem, dev, logits, topk_ids, counts, n_tokens, d_losses, d_logits, topk_w, d_topk_w,
+                            mask, stream):
     """router_losses_backward with a d_logits that is known to fit."""
     T, E, k = problem.T, problem.E, problem.topk
     if (topk_w is None) != (d_topk_w is None):
@@ -690,8 +690,8 @@ def router_losses_backward(problem, logits, topk_ids, counts, n_tokens, d_losses
     [T][k] fp32, through the combine weights."""
     dev = _device_of(logits)
     _want("d_logits", d_logits, "f32", (problem.T, problem.E), dev)
-    _router_losses_backward(problem, dev, logits, topk_ids, counts, n_tokens, d_losses, d_logits, topk_w, d_topk_w, mask,
-                            stream)
+    _router_losses_backward(problem, dev, logits, topk_ids, counts, n_tokens, d_losses, d_logits, topk_w, d_topk_w,
+                            mask, stream)
 
 
 def _router_logits_backward(problem, dev, x, w_router, d_logits, dx, d_w_router, workspace, residual, stream):

@@ -19,7 +19,8 @@ from . import mxfp4_dequantize as _mxfp4_dequantize
 from . import mxfp4_quantize as _mxfp4_quantize
 from . import mxfp8_dequantize as _mxfp8_dequantize
 # the calls below that allocate their outputs leave out the checks of those
-from . import _device_of, _norm_backward, _norm_forward, _router_logits_backward, _router_losses, _router_losses_backward
+from . import (_device_of, _norm_backward, _norm_forward, _router_logits_backward, _router_losses,
+               _router_losses_backward)
 
 
 @dataclasses.dataclass
